@@ -8,8 +8,9 @@ quantisation and the experts' product.
   of 128 channels; ``swiglu``: the same of SwiGLU(h), h = [gate | up];
   ``swiglu_grad``: the same of SwiGLU's gradient with respect to h.
 - ``product``: expert-major fp8 rows times each expert's fp8 weights
-  [N, K] (one scale per 128 x 128 block) to bf16; ``gated``: that product with
-  2I output channels, SwiGLU and the quantisation of its result.
+  [N, K] (one scale per 128 x 128 block) to bf16; ``experts``: an expert layer,
+  the product with 2I gate and up channels, SwiGLU and the quantisation of its
+  result, then the product back to K channels in bf16.
 
 ``own`` False computes the plain form in fp32 torch operations; ``own`` True
 makes the calls of the framework. ``exact`` is the definition in float64.
@@ -66,14 +67,14 @@ def listed():
         _rows("swiglu_8_rows", "swiglu", 8, 2048),
         # The gradient on its way back through the activation, 32768 routed rows and some.
         _rows("swiglu_grad_32777", "swiglu_grad", 32777, 2048),
-        # One token's 8 experts of the 32 on this GPU, gate and up projection.
-        _product("gated_one_token", "gated", 8, 32, 7168, 2048, 1, "uniform"),
+        # One token's 8 experts of the 32 on this GPU.
+        _product("experts_one_token", "experts", 8, 32, 7168, 2048, 1, "uniform"),
         # 64 decoded tokens, down projection, buckets unaligned.
         _product("product_512_rows", "product", 512, 32, 2048, 7168, 1, "uniform"),
         # A skewed prefill on 8 experts of width 4096.
         _product("product_zipf_8191", "product", 8191, 8, 4096, 4096, 16, "zipf"),
-        # The 4096-token batch: gate and up projection, buckets of 128.
-        _product("gated_32768", "gated", 32768, 32, 7168, 2048, 128, "uniform"),
+        # The 4096-token batch, buckets of 128.
+        _product("experts_32768", "experts", 32768, 32, 7168, 2048, 128, "uniform"),
         # Its input gradient through the down projection: the product with transposed weights.
         _product("product_grad_32768", "product", 32768, 32, 7168, 2048, 128, "uniform"),
     ]
@@ -84,7 +85,7 @@ def _log_int(rng, lo, hi):
 
 
 def draw(rng):
-    op = rng.choice(["gate", "gate", "quantize", "swiglu", "swiglu_grad", "product", "product", "gated", "gated"])
+    op = rng.choice(["gate", "gate", "quantize", "swiglu", "swiglu_grad", "product", "product", "experts", "experts"])
     if op == "gate":
         experts = _log_int(rng, 6, 512)
         tokens = _log_int(rng, 1, min(65536, 65536 * 256 // experts))
@@ -100,12 +101,12 @@ def draw(rng):
     while True:
         experts = _log_int(rng, 2, 64)
         k = 16 * _log_int(rng, 16, 448)
-        n = BLOCK * _log_int(rng, 2, 16) if op == "gated" else 8 * _log_int(rng, 32, 896)
+        n = BLOCK * _log_int(rng, 2, 16) if op == "experts" else 8 * _log_int(rng, 32, 896)
         routing = rng.choice(["uniform", "uniform", "zipf"])
         rows = _log_int(rng, 1, 32768)
-        wide = 2 * n if op == "gated" else n
+        wide = 3 * n if op == "experts" else n
         cap = 1.9e12 if routing == "uniform" else 0.4e12
-        if experts * wide * k <= 940e6 and 2.0 * rows * wide * k <= cap and 3072 not in (k, n, rows):
+        if experts * wide * k <= 1400e6 and 2.0 * rows * wide * k <= cap and 3072 not in (k, n, rows):
             return _product(None, op, rows, experts, k, n, rng.choice([1, 16, 128]), routing)
 
 
@@ -179,8 +180,10 @@ def _inputs(case, seed):
     q, sf = _quantize_plain(x)
     sf[torch.ones(capacity, dtype=torch.bool, device="cuda").index_fill_(0, place, False)] = 0.0  # pad rows, as dispatched
     s["x"], s["x_sf"] = q, sf
-    wide = 2 * n if op == "gated" else n
+    wide = 2 * n if op == "experts" else n
     s["w"], s["w_sf"] = _to_blocks(_normal((e, wide, k), seed, 2, torch.bfloat16) * (k ** -0.5))
+    if op == "experts":
+        s["down"], s["down_sf"] = _to_blocks(_normal((e, k, n), seed, 3, torch.bfloat16) * (n ** -0.5))
     return s
 
 
@@ -217,21 +220,21 @@ def prepare(case, seed):
             else:
                 s["plan"] = M.SwigluBackwardQuantizePlan(s["x"], s["grad"], s["q"], s["q_sf"])
         return s
-    n = case["n"]
-    if op == "product":
-        s["out"] = new((s["capacity"], n), torch.bfloat16)
-    else:
-        s["out"] = new((s["capacity"], n), torch.float8_e4m3fn)
-        s["out_sf"] = new((s["capacity"], n // BLOCK), torch.float32)
+    n, k = case["n"], case["k"]
+    s["out"] = new((s["capacity"], n if op == "product" else k), torch.bfloat16)
     if own:
         import moe_token_dispatch_amd as M
 
-        p = M.make_expert_problem(case["experts"], case["k"], 2 * n if op == "gated" else n, s["capacity"], case["rows"])
+        layout = (s["psum"], s["count"])
         if op == "product":
-            s["plan"] = M.ExpertProductPlan(p, s["psum"], s["count"], s["x"], s["x_sf"], s["w"], s["w_sf"], s["out"])
+            p = M.make_expert_problem(case["experts"], k, n, s["capacity"], case["rows"])
+            s["plan"] = M.ExpertProductPlan(p, *layout, s["x"], s["x_sf"], s["w"], s["w_sf"], s["out"])
         else:
-            s["plan"] = M.ExpertSwigluPlan(p, s["psum"], s["count"], s["x"], s["x_sf"], s["w"], s["w_sf"], s["out"],
-                                           s["out_sf"])
+            a, a_sf = new((s["capacity"], n), torch.float8_e4m3fn), new((s["capacity"], n // BLOCK), torch.float32)
+            up = M.make_expert_problem(case["experts"], k, 2 * n, s["capacity"], case["rows"])
+            down = M.make_expert_problem(case["experts"], n, k, s["capacity"], case["rows"])
+            s["up"] = M.ExpertSwigluPlan(up, *layout, s["x"], s["x_sf"], s["w"], s["w_sf"], a, a_sf)
+            s["plan"] = M.ExpertProductPlan(down, *layout, a, a_sf, s["down"], s["down_sf"], s["out"])
     return s
 
 
@@ -309,20 +312,21 @@ def _wide_scales(sf, dim, size):
     return torch.repeat_interleave(sf, BLOCK, dim=dim).narrow(dim, 0, size)
 
 
-def _product_plain(s):
-    """fp32 [rows of each active expert, padded to the longest] products, and the place of every live row."""
-    case = s["case"]
-    k, active = case["k"], s["active"]
-    n = s["w"].shape[1]
-    x = s["x"].float() * _wide_scales(s["x_sf"], 1, k)
-    w = s["w"].view(torch.uint8)[active].view(torch.float8_e4m3fn).float()
-    w = w * _wide_scales(_wide_scales(s["w_sf"][active], 2, k), 1, n)
-    count, first = s["count"].long()[active], s["psum"].long()[:-1][active]
+def _place_plain(s):
+    """[active experts, longest] rows of the buffer, and which of them are live."""
+    count, first = s["count"].long()[s["active"]], s["psum"].long()[:-1][s["active"]]
     at = torch.arange(s["most"], device="cuda")
     live = at[None, :] < count[:, None]
-    place = torch.where(live, first[:, None] + at[None, :], 0)
-    y = torch.bmm(x[place], w.transpose(1, 2).contiguous())
-    return y[live], place[live]
+    return torch.where(live, first[:, None] + at[None, :], 0), live
+
+
+def _product_plain(x, x_sf, w, w_sf, active):
+    """fp32 products of each active expert's rows x [active, longest, K]."""
+    n, k = w.shape[1:]
+    x = x.float() * _wide_scales(x_sf, 2, k)
+    w = w.view(torch.uint8)[active].view(torch.float8_e4m3fn).float()
+    w = w * _wide_scales(_wide_scales(w_sf[active], 2, k), 1, n)
+    return torch.bmm(x, w.transpose(1, 2).contiguous())
 
 
 def run(s):
@@ -349,16 +353,18 @@ def run(s):
         q, sf = _quantize_plain(x)
         return {"q": q, "sf": sf}
     if own:
+        if op == "experts":
+            s["up"]()
         s["plan"]()
-    else:
-        y, place = _product_plain(s)
-        if op == "product":
-            s["out"][place] = y.to(torch.bfloat16)
-        else:
-            q, sf = _quantize_plain(_swiglu_plain(y))
-            s["out"].view(torch.uint8)[place] = q.view(torch.uint8)
-            s["out_sf"][place] = sf
-    return {"out": s["out"]} if op == "product" else {"q": s["out"], "sf": s["out_sf"]}
+        return {"out": s["out"]}
+    place, live = _place_plain(s)
+    x = s["x"].view(torch.uint8)[place].view(torch.float8_e4m3fn)
+    y = _product_plain(x, s["x_sf"][place], s["w"], s["w_sf"], s["active"])
+    if op == "experts":
+        q, sf = _quantize_plain(_swiglu_plain(y.view(-1, y.shape[2])))
+        y = _product_plain(q.view(*live.shape, -1), sf.view(*live.shape, -1), s["down"], s["down_sf"], s["active"])
+    s["out"][place[live]] = y[live].to(torch.bfloat16)
+    return {"out": s["out"]}
 
 
 # --------------------------------------------------------------------- exact
@@ -419,12 +425,9 @@ def _exact_rows(x):
     return torch.round(v / step) * step, sf
 
 
-def _exact_product(s, e):
-    lo, c = s["host_psum"][e], s["host_count"][e]
-    k, n = s["case"]["k"], s["w"].shape[1]
-    block = torch.arange(k, device="cuda") // BLOCK
-    x = s["x"][lo:lo + c].double() * s["x_sf"][lo:lo + c].double()[:, block]
-    w = s["w"][e].double() * s["w_sf"][e].double()[torch.arange(n, device="cuda") // BLOCK][:, block]
+def _exact_product(x, w, w_sf):
+    n, k = w.shape
+    w = w.double() * w_sf.double()[torch.arange(n, device="cuda") // BLOCK][:, torch.arange(k, device="cuda") // BLOCK]
     return x @ w.t()
 
 
@@ -446,20 +449,19 @@ def exact(case, seed):
                 x = torch.cat([d * u * (sig + g * sig * torch.sigmoid(-g)), d * g * sig], 1)
         q, sf = _exact_rows(x)
         return {"q": q, "sf": sf}
-    n = case["n"]
-    out = torch.zeros((s["capacity"], n), dtype=torch.float64, device="cuda")
-    sf = None if op == "product" else torch.zeros((s["capacity"], n // BLOCK), dtype=torch.float64, device="cuda")
+    n, k = case["n"], case["k"]
+    out = torch.zeros((s["capacity"], n if op == "product" else k), dtype=torch.float64, device="cuda")
     for e in range(case["experts"]):
         lo, c = s["host_psum"][e], s["host_count"][e]
         if not c:
             continue
-        y = _exact_product(s, e)
-        if op == "product":
-            out[lo:lo + c] = y
-        else:
-            g, u = y[:, :n], y[:, n:]
-            out[lo:lo + c], sf[lo:lo + c] = _exact_rows(g * torch.sigmoid(g) * u)
-    return {"out": out} if op == "product" else {"q": out, "sf": sf}
+        x = s["x"][lo:lo + c].double() * s["x_sf"][lo:lo + c].double()[:, torch.arange(k, device="cuda") // BLOCK]
+        y = _exact_product(x, s["w"][e], s["w_sf"][e])
+        if op == "experts":
+            q, sf = _exact_rows(y[:, :n] * torch.sigmoid(y[:, :n]) * y[:, n:])
+            y = _exact_product(q * sf[:, torch.arange(n, device="cuda") // BLOCK], s["down"][e], s["down_sf"][e])
+        out[lo:lo + c] = y
+    return {"out": out}
 
 
 # ---------------------------------------------------------------------- work
@@ -482,9 +484,11 @@ def work(case):
             return {"bytes": r * (5 * w + 4 * _ceil(w, BLOCK)), "flops": 9 * r * w}
         return {"bytes": r * (8 * w + 4 * _ceil(2 * w, BLOCK)), "flops": 20 * r * w}
     rows, k, n = case["rows"], case["k"], case["n"]
-    wide = 2 * n if op == "gated" else n
-    kb = _ceil(k, BLOCK)
+    kb, nb = _ceil(k, BLOCK), _ceil(n, BLOCK)
     active = sum(1.0 - (1.0 - p) ** rows for p in _expert_probability(case))
-    out = rows * (n + 4 * n // BLOCK) if op == "gated" else rows * 2 * n
-    weights = active * (wide * k + 4 * kb * _ceil(wide, BLOCK))
-    return {"bytes": rows * (k + 4 * kb) + weights + out + 8 * case["experts"] + 4, "flops": 2.0 * rows * wide * k}
+    if op == "product":
+        weights, values, out = n * k + 4 * nb * kb, n * k, n
+    else:
+        weights, values, out = 3 * (n * k + 4 * nb * kb), 3 * n * k, k
+    return {"bytes": rows * (k + 4 * kb + 2 * out) + active * weights + 8 * case["experts"] + 4,
+            "flops": 2.0 * rows * values}
