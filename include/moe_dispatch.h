@@ -345,6 +345,159 @@ typedef struct dispatch_combine_problem {
 int dispatch_combine(const dispatch_combine_problem_t* problem, const int32_t* expert_slot,
                      const float* topk_weights, const void* y, void* out, hipStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Gate: the routing table and the top-k weights of a token batch from its
+ * router logits z[T, E], with the per-expert counts and the balance loss.
+ *
+ *   DISPATCH_GATE_SOFTMAX: score s = softmax(z) over the experts, share p = s;
+ *     the K experts with the largest z are taken.
+ *   DISPATCH_GATE_SIGMOID: s = 1 / (1 + exp(-z)), p = s / sum_e s; the K
+ *     experts with the largest s + select_bias are taken (the bias moves the
+ *     choice alone, no weight).
+ *   topk_weights = route_scale * s, divided by the taken experts' sum of s
+ *     under DISPATCH_GATE_NORMALIZE.
+ *   loss = loss_coef * E / (K * N^2) * sum_e expert_count[e] * prob_sum[e],
+ *     prob_sum[e] = sum over the live tokens of p, N = live tokens: loss_coef
+ *     when the counts are even.
+ *
+ * Entries of a token are in descending order of what they were taken by, ties
+ * to the lowest expert. An expert whose logit is -inf or NaN (or whose s +
+ * select_bias is -inf or NaN) is never taken; entries left over are -1 with
+ * weight 0, so dispatch_layout sees them masked. A token whose token_mask is 0
+ * gets K such entries and counts nowhere. A row of nothing but -inf has p = 0
+ * everywhere. A NaN logit (for softmax +inf too) makes its token's p NaN, and
+ * so the loss; under softmax the token's weights too. All sums are fp32 or
+ * wider; results do not depend on the order in which workgroups run.
+ * ------------------------------------------------------------------------- */
+#define DISPATCH_GATE_SOFTMAX 0
+#define DISPATCH_GATE_SIGMOID 1
+#define DISPATCH_GATE_NORMALIZE 1u
+
+typedef struct dispatch_gate_problem {
+    int64_t num_tokens;     /* T >= 0, T * K <= 2^31 - 1 */
+    int32_t num_experts;    /* E, 1..DISPATCH_MAX_EXPERTS */
+    int32_t num_topk;       /* K, 1..min(E, DISPATCH_MAX_TOPK) */
+    int32_t scoring;        /* DISPATCH_GATE_SOFTMAX or DISPATCH_GATE_SIGMOID */
+    int32_t logits_bytes;   /* logits and their gradient: 2 (bf16) or 4 (fp32) */
+    int32_t topk_idx_bytes; /* 8 (int64) or 4 (int32) */
+    uint32_t flags;         /* DISPATCH_GATE_NORMALIZE or 0 */
+    float route_scale;      /* finite */
+    float loss_coef;        /* finite */
+} dispatch_gate_problem_t;
+
+/* Outputs; caller-owned device pointers. The last four are the balance
+ * outputs: all of them or none (NULL). */
+typedef struct dispatch_gate_out {
+    void* topk_idx;        /* [T, K] of topk_idx_bytes wide integers */
+    float* topk_weights;   /* [T, K] */
+    int32_t* expert_count; /* [E] live tokens that took the expert */
+    float* prob_sum;       /* [E] sum of p over the live tokens */
+    int32_t* live_tokens;  /* [1] N */
+    float* loss;           /* [1] 0 when N is 0 */
+} dispatch_gate_out_t;
+
+/* Bytes of device workspace dispatch_gate needs for the balance outputs
+ * (256-byte aligned; it need not be initialised and holds nothing between
+ * calls). */
+int dispatch_gate_workspace_size(const dispatch_gate_problem_t* problem, size_t* bytes);
+
+/* logits: device [T, E], aligned to its element. select_bias: device fp32 [E]
+ * or NULL, with DISPATCH_GATE_SIGMOID only. token_mask: device bytes [T], 0 =
+ * not routed, or NULL. The workspace may be NULL without balance outputs. One
+ * kernel, two with the balance outputs. */
+int dispatch_gate(const dispatch_gate_problem_t* problem, const void* logits, const float* select_bias,
+                  const uint8_t* token_mask, const dispatch_gate_out_t* out, void* workspace,
+                  size_t workspace_bytes, hipStream_t stream);
+
+/* Gradient of the logits, grad_logits [T, E] in the logits' type, from the
+ * gradient of the weights (grad_weights: device fp32 [T, K], or NULL = 0) and
+ * of the loss (grad_loss: device fp32 [1], or NULL = 0). topk_idx,
+ * expert_count and live_tokens are dispatch_gate's outputs for these logits
+ * (entries outside [0, E) are skipped; expert_count and live_tokens may be
+ * sums over several calls and GPUs, and are needed with grad_loss only). The
+ * counts are constants of the differentiation, as the choice itself is.
+ * Tokens that are not routed get zeros. */
+int dispatch_gate_backward(const dispatch_gate_problem_t* problem, const void* logits, const uint8_t* token_mask,
+                           const void* topk_idx, const float* grad_weights, const int32_t* expert_count,
+                           const int32_t* live_tokens, const float* grad_loss, void* grad_logits,
+                           hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Quantisation to fp8 (OCP e4m3) with one fp32 scale per row and block of 128
+ * channels, the rows and scale factors that the dispatch moves:
+ *   amax = max(largest |x| of the block, 2^-100), sf = amax / 448,
+ *   q = x * (448 / amax) rounded to nearest, ties to even.
+ * The last block may be short. A block holding NaN or an infinity gives a
+ * scale of NaN or infinity and NaN values. x is bf16 and widened to fp32.
+ * num_valid_rows: device int32 [1] or NULL; rows at or beyond it are neither
+ * read nor written (an expert-major buffer's total, &expert_psum[E]).
+ * ------------------------------------------------------------------------- */
+#define DISPATCH_SF_BLOCK 128
+
+typedef struct dispatch_quantize_problem {
+    int64_t num_rows;  /* R >= 0 rows of the buffers; R * ceil(width / 128) <= 2^31 - 1 */
+    int64_t width;     /* channels per row (see each call), a multiple of 16, at most 2^30 */
+} dispatch_quantize_problem_t;
+
+/* x: device bf16 [R, width], 16-byte aligned; q: device bytes [R, width],
+ * 16-byte aligned; sf: device fp32 [R, ceil(width / 128)]. */
+int dispatch_quantize(const dispatch_quantize_problem_t* problem, const void* x, const int32_t* num_valid_rows,
+                      void* q, float* sf, hipStream_t stream);
+
+/* The same of SwiGLU: h: device bf16 [R, 2 * width] = [g | u];
+ * x = g / (1 + exp(-g)) * u in fp32. width must be a multiple of 128. */
+int dispatch_swiglu_quantize(const dispatch_quantize_problem_t* problem, const void* h,
+                             const int32_t* num_valid_rows, void* q, float* sf, hipStream_t stream);
+
+/* The same of SwiGLU's gradient with respect to h, from grad: device bf16
+ * [R, width]: with s = 1 / (1 + exp(-g)), x = [grad u s (1 + g (1 - s)) |
+ * grad g s], 2 * width channels: q [R, 2 * width], sf [R, 2 * width / 128].
+ * width must be a multiple of 128. */
+int dispatch_swiglu_backward_quantize(const dispatch_quantize_problem_t* problem, const void* h, const void* grad,
+                                      const int32_t* num_valid_rows, void* q, float* sf, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The experts' product over an expert-major buffer: for every expert e and
+ * each of its rows r in [expert_psum[e], expert_psum[e] + expert_count[e]),
+ *   y[r, n] = sum_b x_sf[r, b] * w_sf[e, n / 128, b]
+ *                   * sum_{k in block b} x[r, k] * w[e, n, k]
+ * with fp8 (e4m3) x and w, blocks of 128 channels (the last may be short),
+ * the fp8 matrix instruction's sum within a block and fp32 sums across them.
+ * Pad rows and rows beyond the totals are neither read nor
+ * written. The rows' gradient of a product with weights w[E, N, K] is this
+ * product with the weights laid out as [E, K, N] and their scales as
+ * [E, ceil(K / 128), ceil(N / 128)].
+ * expert_psum and expert_count are those of dispatch_layout or
+ * dispatch_expand_layout (with status 0), read on the device.
+ * ------------------------------------------------------------------------- */
+typedef struct dispatch_expert_problem {
+    int32_t num_experts;      /* E, 1..DISPATCH_MAX_EXPERTS, of this buffer */
+    uint32_t reserved;        /* must be 0 */
+    int64_t in_features;      /* K: channels of x, a multiple of 16, 16..2^20 */
+    int64_t out_features;     /* N: rows of an expert's weights, a multiple of 8, 8..2^20 */
+    int64_t expert_rows;      /* rows of x and of the output, <= 2^31 - 1 (and their 16 x 64 tiles of
+                                 the output too); rows outside are skipped */
+    int64_t max_routed_rows;  /* about how many rows are routed at most (T * K); picks the kernel and
+                                 its grid, more rows are computed all the same */
+} dispatch_expert_problem_t;
+
+/* x: device bytes [expert_rows, K]; x_sf: device fp32 [expert_rows,
+ * ceil(K / 128)]; w: device bytes [E, N, K]; w_sf: device fp32 [E,
+ * ceil(N / 128), ceil(K / 128)]; out: device bf16 [expert_rows, N]. x, w and
+ * out are 16-byte aligned. */
+int dispatch_expert_product(const dispatch_expert_problem_t* problem, const int32_t* expert_psum,
+                            const int32_t* expert_count, const void* x, const float* x_sf, const void* w,
+                            const float* w_sf, void* out, hipStream_t stream);
+
+/* The product with gate and up weights and the activation behind it: N = 2I
+ * weight rows, gate first; a = SwiGLU of y's halves in fp32 (y is not rounded
+ * in between), quantised as dispatch_quantize does: out_q: device bytes
+ * [expert_rows, I], 16-byte aligned, out_sf: device fp32 [expert_rows,
+ * I / 128]. I must be a multiple of 128. */
+int dispatch_expert_product_swiglu(const dispatch_expert_problem_t* problem, const int32_t* expert_psum,
+                                   const int32_t* expert_count, const void* x, const float* x_sf, const void* w,
+                                   const float* w_sf, void* out_q, float* out_sf, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -18,4 +18,10 @@ from ._binding import (  # noqa: F401
     dispatch_expand_workspace_size, alloc_expand_layout, alloc_expand_workspace, dispatch_expand_layout,
     dispatch_expand_scatter, dispatch_expand_layout_and_scatter, ExpandPlan, CombineProblem, dispatch_combine,
     CombinePlan, STATUS_TIMEOUT, DEFAULT_WAIT_LIMIT, dispatch_set_wait_limit,
+    GATE_NORMALIZE, GATE_SIGMOID, GATE_SOFTMAX, SF_BLOCK, ExpertProblem, ExpertProductPlan, ExpertSwigluPlan,
+    GateBackwardPlan, GateOutPtrs, GatePlan, GateProblem, GateTensors, QuantizePlan, QuantizeProblem,
+    SwigluBackwardQuantizePlan, SwigluQuantizePlan, alloc_gate, alloc_gate_workspace, dispatch_expert_product,
+    dispatch_expert_product_swiglu, dispatch_gate, dispatch_gate_backward, dispatch_gate_workspace_size,
+    dispatch_quantize, dispatch_swiglu_backward_quantize, dispatch_swiglu_quantize, make_expert_problem,
+    make_gate_problem,
 )

@@ -43,6 +43,11 @@ ZERO_PAD = 4
 ALL_OUTPUTS = RANK_CONTIG | EXPERT_MAJOR | ZERO_PAD
 ROWS_READ_AHEAD = 8  # scatter hint: the rows were just read ahead (changes no result)
 
+GATE_SOFTMAX = 0
+GATE_SIGMOID = 1
+GATE_NORMALIZE = 1
+SF_BLOCK = 128  # channels per scale factor
+
 
 class DispatchError(RuntimeError):
     def __init__(self, code: int, what: str):
@@ -108,6 +113,48 @@ class CombineProblem(ctypes.Structure):
     ]
 
 
+class GateProblem(ctypes.Structure):
+    """dispatch_gate_problem_t."""
+
+    _fields_ = [
+        ("num_tokens", ctypes.c_int64),
+        ("num_experts", ctypes.c_int32),
+        ("num_topk", ctypes.c_int32),
+        ("scoring", ctypes.c_int32),
+        ("logits_bytes", ctypes.c_int32),
+        ("topk_idx_bytes", ctypes.c_int32),
+        ("flags", ctypes.c_uint32),
+        ("route_scale", ctypes.c_float),
+        ("loss_coef", ctypes.c_float),
+    ]
+
+
+class GateOutPtrs(ctypes.Structure):
+    """dispatch_gate_out_t."""
+
+    _fields_ = [(name, ctypes.c_void_p) for name in (
+        "topk_idx", "topk_weights", "expert_count", "prob_sum", "live_tokens", "loss")]
+
+
+class QuantizeProblem(ctypes.Structure):
+    """dispatch_quantize_problem_t."""
+
+    _fields_ = [("num_rows", ctypes.c_int64), ("width", ctypes.c_int64)]
+
+
+class ExpertProblem(ctypes.Structure):
+    """dispatch_expert_problem_t."""
+
+    _fields_ = [
+        ("num_experts", ctypes.c_int32),
+        ("reserved", ctypes.c_uint32),
+        ("in_features", ctypes.c_int64),
+        ("out_features", ctypes.c_int64),
+        ("expert_rows", ctypes.c_int64),
+        ("max_routed_rows", ctypes.c_int64),
+    ]
+
+
 _LIB = None
 
 # Exported symbols of include/moe_dispatch.h.
@@ -116,7 +163,10 @@ SYMBOLS = ("dispatch_abi_version", "dispatch_strerror", "dispatch_workspace_size
            "dispatch_scatter", "dispatch_layout_and_scatter", "dispatch_layout_and_scatter_noalloc",
            "dispatch_kernel_count", "dispatch_set_wait_limit",
            "dispatch_expand_workspace_size", "dispatch_expand_max_rows", "dispatch_expand_layout",
-           "dispatch_expand_scatter", "dispatch_expand_layout_and_scatter", "dispatch_combine")
+           "dispatch_expand_scatter", "dispatch_expand_layout_and_scatter", "dispatch_combine",
+           "dispatch_gate_workspace_size", "dispatch_gate", "dispatch_gate_backward", "dispatch_quantize",
+           "dispatch_swiglu_quantize", "dispatch_swiglu_backward_quantize", "dispatch_expert_product",
+           "dispatch_expert_product_swiglu")
 
 
 def load_library(path: str = LIB_PATH):
@@ -167,6 +217,17 @@ def load_library(path: str = LIB_PATH):
     lib.dispatch_expand_scatter.restype = i
     lib.dispatch_combine.argtypes = [ctypes.POINTER(CombineProblem), p, p, p, p, p]
     lib.dispatch_combine.restype = i
+    gp, qp, xp = ctypes.POINTER(GateProblem), ctypes.POINTER(QuantizeProblem), ctypes.POINTER(ExpertProblem)
+    for name, args in (("dispatch_gate_workspace_size", [gp, ctypes.POINTER(sz)]),
+                       ("dispatch_gate", [gp, p, p, p, ctypes.POINTER(GateOutPtrs), p, sz, p]),
+                       ("dispatch_gate_backward", [gp, p, p, p, p, p, p, p, p, p]),
+                       ("dispatch_quantize", [qp, p, p, p, p, p]),
+                       ("dispatch_swiglu_quantize", [qp, p, p, p, p, p]),
+                       ("dispatch_swiglu_backward_quantize", [qp, p, p, p, p, p, p]),
+                       ("dispatch_expert_product", [xp, p, p, p, p, p, p, p, p]),
+                       ("dispatch_expert_product_swiglu", [xp, p, p, p, p, p, p, p, p, p])):
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = i
     if lib.dispatch_abi_version() != ABI_VERSION:
         raise ImportError(f"{path}: ABI version {lib.dispatch_abi_version()} != {ABI_VERSION}")
     _LIB = lib
@@ -826,3 +887,348 @@ class CombinePlan:
         rc = self._lib.dispatch_combine(*self._args)
         if rc:
             raise DispatchError(rc, "dispatch_combine")
+
+
+# ---------------------------------------------------------------------- gate
+
+FP8 = torch.float8_e4m3fn
+_LOGIT_TYPES = {torch.bfloat16: 2, torch.float32: 4}
+_INDEX_TYPES = {4: torch.int32, 8: torch.int64}
+
+
+def make_gate_problem(num_tokens: int, num_experts: int, num_topk: int, scoring: int = GATE_SOFTMAX,
+                      logits_dtype: torch.dtype = torch.bfloat16, normalize: bool = True, route_scale: float = 1.0,
+                      loss_coef: float = 0.0, topk_idx_bytes: int = 8) -> GateProblem:
+    if logits_dtype not in _LOGIT_TYPES:
+        raise ValueError(f"logits must be bfloat16 or float32, got {logits_dtype}")
+    p = GateProblem(num_tokens, num_experts, num_topk, scoring, _LOGIT_TYPES[logits_dtype], topk_idx_bytes,
+                    GATE_NORMALIZE if normalize else 0, route_scale, loss_coef)
+    dispatch_gate_workspace_size(p)  # checks the problem
+    return p
+
+
+def dispatch_gate_workspace_size(problem: GateProblem) -> int:
+    out = ctypes.c_size_t(0)
+    rc = load_library().dispatch_gate_workspace_size(ctypes.byref(problem), ctypes.byref(out))
+    if rc:
+        raise DispatchError(rc, "dispatch_gate_workspace_size")
+    return int(out.value)
+
+
+@dataclasses.dataclass
+class GateTensors:
+    """Device outputs of dispatch_gate (see dispatch_gate_out_t); the last four are None without balance outputs."""
+
+    topk_idx: torch.Tensor                  # int64 or int32 [T, K]
+    topk_weights: torch.Tensor              # float32 [T, K]
+    expert_count: Optional[torch.Tensor]    # int32 [E]
+    prob_sum: Optional[torch.Tensor]        # float32 [E]
+    live_tokens: Optional[torch.Tensor]     # int32 [1]
+    loss: Optional[torch.Tensor]            # float32 [1]
+
+    def ptrs(self) -> GateOutPtrs:
+        return GateOutPtrs(*[_ptr(getattr(self, f.name)) for f in dataclasses.fields(self)])
+
+
+def alloc_gate(problem: GateProblem, device, balance: bool = True) -> GateTensors:
+    t, e, k = problem.num_tokens, problem.num_experts, problem.num_topk
+
+    def new(shape, dtype, on=True):
+        return torch.empty(shape, dtype=dtype, device=device) if on else None
+
+    return GateTensors(topk_idx=new((t, k), _INDEX_TYPES[problem.topk_idx_bytes]),
+                       topk_weights=new((t, k), torch.float32), expert_count=new(e, torch.int32, balance),
+                       prob_sum=new(e, torch.float32, balance), live_tokens=new(1, torch.int32, balance),
+                       loss=new(1, torch.float32, balance))
+
+
+def alloc_gate_workspace(problem: GateProblem, device) -> torch.Tensor:
+    """Workspace for dispatch_gate with balance outputs (it need not be initialised)."""
+    return torch.empty(dispatch_gate_workspace_size(problem), dtype=torch.uint8, device=device)
+
+
+def _check_sized(t: Optional[torch.Tensor], name: str, count: int, *dtypes) -> None:
+    """A device tensor of one of the types with at least `count` elements (None passes)."""
+    if t is None:
+        return
+    _check_device_tensor(t, name)
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    _need(t, name, count * t.element_size())
+
+
+def _logit_type(problem: GateProblem) -> torch.dtype:
+    return torch.bfloat16 if problem.logits_bytes == 2 else torch.float32
+
+
+def _gate_args(problem: GateProblem, logits, out: GateTensors, workspace, select_bias, token_mask, stream):
+    t, e, k = problem.num_tokens, problem.num_experts, problem.num_topk
+    _check_sized(logits, "logits", t * e, _logit_type(problem))
+    _check_sized(out.topk_idx, "topk_idx", t * k, _INDEX_TYPES[problem.topk_idx_bytes])
+    _check_sized(out.topk_weights, "topk_weights", t * k, torch.float32)
+    _check_sized(out.expert_count, "expert_count", e, torch.int32)
+    _check_sized(out.prob_sum, "prob_sum", e, torch.float32)
+    _check_sized(out.live_tokens, "live_tokens", 1, torch.int32)
+    _check_sized(out.loss, "loss", 1, torch.float32)
+    _check_sized(select_bias, "select_bias", e, torch.float32)
+    _check_sized(token_mask, "token_mask", t, torch.bool, torch.uint8)
+    nbytes = 0
+    if workspace is not None:
+        _check_device_tensor(workspace, "workspace")
+        nbytes = workspace.numel() * workspace.element_size()
+    ptrs = out.ptrs()
+    return (ctypes.byref(problem), _ptr(logits), _ptr(select_bias), _ptr(token_mask), ctypes.byref(ptrs),
+            _ptr(workspace), nbytes, _stream_handle(stream, logits.device)), ptrs
+
+
+def dispatch_gate(problem: GateProblem, logits: torch.Tensor, out: GateTensors,
+                  workspace: Optional[torch.Tensor] = None, select_bias: Optional[torch.Tensor] = None,
+                  token_mask: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Enqueue the gate: logits [T, E] to out.topk_idx and out.topk_weights,
+    and, where ``out`` has them, the balance outputs (these need a workspace)."""
+    args, _keep = _gate_args(problem, logits, out, workspace, select_bias, token_mask, stream)
+    rc = load_library().dispatch_gate(*args)
+    if rc:
+        raise DispatchError(rc, "dispatch_gate")
+
+
+class GatePlan:
+    """A prepared gate, like Plan: checked once, one C call per step."""
+
+    def __init__(self, problem: GateProblem, logits: torch.Tensor, out: GateTensors,
+                 workspace: Optional[torch.Tensor] = None, select_bias: Optional[torch.Tensor] = None,
+                 token_mask: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
+        problem = GateProblem.from_buffer_copy(problem)
+        self._args, ptrs = _gate_args(problem, logits, out, workspace, select_bias, token_mask, stream)
+        self._keep = (problem, logits, out, ptrs, workspace, select_bias, token_mask)
+        self._call = load_library().dispatch_gate
+
+    def __call__(self) -> None:
+        rc = self._call(*self._args)
+        if rc:
+            raise DispatchError(rc, "dispatch_gate")
+
+
+def _gate_backward_args(problem: GateProblem, logits, out: GateTensors, grad_weights, grad_loss, grad_logits,
+                        token_mask, stream):
+    t, e, k = problem.num_tokens, problem.num_experts, problem.num_topk
+    _check_sized(logits, "logits", t * e, _logit_type(problem))
+    _check_sized(out.topk_idx, "topk_idx", t * k, _INDEX_TYPES[problem.topk_idx_bytes])
+    _check_sized(out.expert_count, "expert_count", e, torch.int32)
+    _check_sized(out.live_tokens, "live_tokens", 1, torch.int32)
+    _check_sized(grad_weights, "grad_weights", t * k, torch.float32)
+    _check_sized(grad_loss, "grad_loss", 1, torch.float32)
+    _check_sized(grad_logits, "grad_logits", t * e, _logit_type(problem))
+    _check_sized(token_mask, "token_mask", t, torch.bool, torch.uint8)
+    return (ctypes.byref(problem), _ptr(logits), _ptr(token_mask), _ptr(out.topk_idx), _ptr(grad_weights),
+            _ptr(out.expert_count), _ptr(out.live_tokens), _ptr(grad_loss), _ptr(grad_logits),
+            _stream_handle(stream, logits.device))
+
+
+def dispatch_gate_backward(problem: GateProblem, logits: torch.Tensor, out: GateTensors,
+                           grad_weights: Optional[torch.Tensor], grad_loss: Optional[torch.Tensor],
+                           grad_logits: torch.Tensor, token_mask: Optional[torch.Tensor] = None,
+                           stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Enqueue the gradient of the logits from those of out.topk_weights and
+    out.loss (None = zero). ``out`` holds dispatch_gate's outputs for them."""
+    rc = load_library().dispatch_gate_backward(*_gate_backward_args(problem, logits, out, grad_weights, grad_loss,
+                                                                    grad_logits, token_mask, stream))
+    if rc:
+        raise DispatchError(rc, "dispatch_gate_backward")
+
+
+class GateBackwardPlan:
+    """A prepared gate gradient, like Plan."""
+
+    def __init__(self, problem: GateProblem, logits: torch.Tensor, out: GateTensors,
+                 grad_weights: Optional[torch.Tensor], grad_loss: Optional[torch.Tensor], grad_logits: torch.Tensor,
+                 token_mask: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
+        problem = GateProblem.from_buffer_copy(problem)
+        self._args = _gate_backward_args(problem, logits, out, grad_weights, grad_loss, grad_logits, token_mask, stream)
+        self._keep = (problem, logits, out, grad_weights, grad_loss, grad_logits, token_mask)
+        self._call = load_library().dispatch_gate_backward
+
+    def __call__(self) -> None:
+        rc = self._call(*self._args)
+        if rc:
+            raise DispatchError(rc, "dispatch_gate_backward")
+
+
+# -------------------------------------------------------------- quantisation
+
+
+def _sf_blocks(width: int) -> int:
+    return (width + SF_BLOCK - 1) // SF_BLOCK
+
+
+def _quantize_args(x, grad, q, sf, num_valid_rows, halves_in: int, halves_out: int, stream):
+    """halves_in, halves_out: x's and q's channels in units of the problem's width."""
+    _check_device_tensor(x, "x", torch.bfloat16)
+    if x.dim() != 2 or x.shape[1] % halves_in:
+        raise ValueError("x must be [rows, channels], with as many gate as up channels for SwiGLU")
+    rows, width = x.shape[0], x.shape[1] // halves_in
+    if grad is not None:
+        _check_sized(grad, "grad", rows * width, torch.bfloat16)
+    _check_sized(q, "q", rows * width * halves_out, FP8, torch.uint8)
+    _check_sized(sf, "sf", rows * _sf_blocks(width) * halves_out, torch.float32)
+    _check_sized(num_valid_rows, "num_valid_rows", 1, torch.int32)
+    problem = QuantizeProblem(rows, width)
+    rows_ptrs = (_ptr(x),) if grad is None else (_ptr(x), _ptr(grad))
+    return (ctypes.byref(problem), *rows_ptrs, _ptr(num_valid_rows), _ptr(q), _ptr(sf),
+            _stream_handle(stream, x.device)), problem
+
+
+def dispatch_quantize(x: torch.Tensor, q: torch.Tensor, sf: torch.Tensor,
+                      num_valid_rows: Optional[torch.Tensor] = None,
+                      stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Enqueue bf16 rows [R, H] to fp8 q [R, H] and scales sf [R, ceil(H / 128)]."""
+    args, _keep = _quantize_args(x, None, q, sf, num_valid_rows, 1, 1, stream)
+    rc = load_library().dispatch_quantize(*args)
+    if rc:
+        raise DispatchError(rc, "dispatch_quantize")
+
+
+def dispatch_swiglu_quantize(h: torch.Tensor, q: torch.Tensor, sf: torch.Tensor,
+                             num_valid_rows: Optional[torch.Tensor] = None,
+                             stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Enqueue SwiGLU of bf16 h [R, 2I] to fp8 q [R, I] and scales sf [R, I / 128]."""
+    args, _keep = _quantize_args(h, None, q, sf, num_valid_rows, 2, 1, stream)
+    rc = load_library().dispatch_swiglu_quantize(*args)
+    if rc:
+        raise DispatchError(rc, "dispatch_swiglu_quantize")
+
+
+def dispatch_swiglu_backward_quantize(h: torch.Tensor, grad: torch.Tensor, q: torch.Tensor, sf: torch.Tensor,
+                                      num_valid_rows: Optional[torch.Tensor] = None,
+                                      stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Enqueue SwiGLU's gradient with respect to h [R, 2I], from grad [R, I],
+    to fp8 q [R, 2I] and scales sf [R, 2I / 128]."""
+    args, _keep = _quantize_args(h, grad, q, sf, num_valid_rows, 2, 2, stream)
+    rc = load_library().dispatch_swiglu_backward_quantize(*args)
+    if rc:
+        raise DispatchError(rc, "dispatch_swiglu_backward_quantize")
+
+
+class QuantizePlan:
+    """A prepared dispatch_quantize, like Plan."""
+
+    _name, _halves = "dispatch_quantize", (1, 1)
+
+    def __init__(self, x: torch.Tensor, q: torch.Tensor, sf: torch.Tensor,
+                 num_valid_rows: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
+        self._prepare(x, None, q, sf, num_valid_rows, stream)
+
+    def _prepare(self, x, grad, q, sf, num_valid_rows, stream):
+        self._args, problem = _quantize_args(x, grad, q, sf, num_valid_rows, *self._halves, stream)
+        self._keep = (problem, x, grad, q, sf, num_valid_rows)
+        self._call = getattr(load_library(), self._name)
+
+    def __call__(self) -> None:
+        rc = self._call(*self._args)
+        if rc:
+            raise DispatchError(rc, self._name)
+
+
+class SwigluQuantizePlan(QuantizePlan):
+    """A prepared dispatch_swiglu_quantize, like Plan."""
+
+    _name, _halves = "dispatch_swiglu_quantize", (2, 1)
+
+
+class SwigluBackwardQuantizePlan(QuantizePlan):
+    """A prepared dispatch_swiglu_backward_quantize, like Plan."""
+
+    _name, _halves = "dispatch_swiglu_backward_quantize", (2, 2)
+
+    def __init__(self, h: torch.Tensor, grad: torch.Tensor, q: torch.Tensor, sf: torch.Tensor,
+                 num_valid_rows: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
+        if grad is None:
+            raise ValueError("grad must be a device tensor")
+        self._prepare(h, grad, q, sf, num_valid_rows, stream)
+
+
+# ---------------------------------------------------------- experts' product
+
+
+def make_expert_problem(num_experts: int, in_features: int, out_features: int, expert_rows: int,
+                        max_routed_rows: Optional[int] = None) -> ExpertProblem:
+    """``expert_rows``: rows of the expert-major buffers (recv_capacity_rows).
+    ``max_routed_rows``: about how many of them are routed at most (T * K; it
+    picks the kernel, and defaults to expert_rows)."""
+    return ExpertProblem(num_experts, 0, in_features, out_features, expert_rows,
+                         expert_rows if max_routed_rows is None else max_routed_rows)
+
+
+def _expert_args(problem: ExpertProblem, expert_psum, expert_count, x, x_sf, w, w_sf, out, out_sf, swiglu, stream):
+    e, k, n, rows = problem.num_experts, problem.in_features, problem.out_features, problem.expert_rows
+    _check_sized(expert_psum, "expert_psum", e + 1, torch.int32)
+    _check_sized(expert_count, "expert_count", e, torch.int32)
+    _check_sized(x, "x", rows * k, FP8, torch.uint8)
+    _check_sized(x_sf, "x_sf", rows * _sf_blocks(k), torch.float32)
+    _check_sized(w, "w", e * n * k, FP8, torch.uint8)
+    _check_sized(w_sf, "w_sf", e * _sf_blocks(n) * _sf_blocks(k), torch.float32)
+    if swiglu:
+        _check_sized(out, "out_q", rows * (n // 2), FP8, torch.uint8)
+        _check_sized(out_sf, "out_sf", rows * (n // 2 // SF_BLOCK), torch.float32)
+    else:
+        _check_sized(out, "out", rows * n, torch.bfloat16)
+    outs = (_ptr(out), _ptr(out_sf)) if swiglu else (_ptr(out),)
+    return (ctypes.byref(problem), _ptr(expert_psum), _ptr(expert_count), _ptr(x), _ptr(x_sf), _ptr(w), _ptr(w_sf),
+            *outs, _stream_handle(stream, w.device))
+
+
+def dispatch_expert_product(problem: ExpertProblem, expert_psum: torch.Tensor, expert_count: torch.Tensor,
+                            x: torch.Tensor, x_sf: torch.Tensor, w: torch.Tensor, w_sf: torch.Tensor,
+                            out: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Enqueue out[r] = x[r] @ w[e].T for the rows r of each expert e (fp8
+    operands with block scales, bf16 out)."""
+    rc = load_library().dispatch_expert_product(*_expert_args(problem, expert_psum, expert_count, x, x_sf, w, w_sf,
+                                                              out, None, False, stream))
+    if rc:
+        raise DispatchError(rc, "dispatch_expert_product")
+
+
+def dispatch_expert_product_swiglu(problem: ExpertProblem, expert_psum: torch.Tensor, expert_count: torch.Tensor,
+                                   x: torch.Tensor, x_sf: torch.Tensor, w: torch.Tensor, w_sf: torch.Tensor,
+                                   out_q: torch.Tensor, out_sf: torch.Tensor,
+                                   stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Enqueue SwiGLU of that product (w [E, 2I, K], gate rows first),
+    quantised: out_q [expert_rows, I] and out_sf [expert_rows, I / 128]."""
+    rc = load_library().dispatch_expert_product_swiglu(*_expert_args(problem, expert_psum, expert_count, x, x_sf, w,
+                                                                     w_sf, out_q, out_sf, True, stream))
+    if rc:
+        raise DispatchError(rc, "dispatch_expert_product_swiglu")
+
+
+class ExpertProductPlan:
+    """A prepared dispatch_expert_product, like Plan."""
+
+    def __init__(self, problem: ExpertProblem, expert_psum: torch.Tensor, expert_count: torch.Tensor,
+                 x: torch.Tensor, x_sf: torch.Tensor, w: torch.Tensor, w_sf: torch.Tensor, out: torch.Tensor,
+                 stream: Optional[torch.cuda.Stream] = None):
+        problem = ExpertProblem.from_buffer_copy(problem)
+        self._args = _expert_args(problem, expert_psum, expert_count, x, x_sf, w, w_sf, out, None, False, stream)
+        self._keep = (problem, expert_psum, expert_count, x, x_sf, w, w_sf, out)
+        self._call = load_library().dispatch_expert_product
+
+    def __call__(self) -> None:
+        rc = self._call(*self._args)
+        if rc:
+            raise DispatchError(rc, "dispatch_expert_product")
+
+
+class ExpertSwigluPlan:
+    """A prepared dispatch_expert_product_swiglu, like Plan."""
+
+    def __init__(self, problem: ExpertProblem, expert_psum: torch.Tensor, expert_count: torch.Tensor,
+                 x: torch.Tensor, x_sf: torch.Tensor, w: torch.Tensor, w_sf: torch.Tensor, out_q: torch.Tensor,
+                 out_sf: torch.Tensor, stream: Optional[torch.cuda.Stream] = None):
+        problem = ExpertProblem.from_buffer_copy(problem)
+        self._args = _expert_args(problem, expert_psum, expert_count, x, x_sf, w, w_sf, out_q, out_sf, True, stream)
+        self._keep = (problem, expert_psum, expert_count, x, x_sf, w, w_sf, out_q, out_sf)
+        self._call = load_library().dispatch_expert_product_swiglu
+
+    def __call__(self) -> None:
+        rc = self._call(*self._args)
+        if rc:
+            raise DispatchError(rc, "dispatch_expert_product_swiglu")

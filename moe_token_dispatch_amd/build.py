@@ -21,7 +21,8 @@ LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 ARCH = "gfx950"
 
 SOURCES = ["dispatch_api.cpp", "dispatch_layout.hip", "dispatch_scatter.hip", "dispatch_combine.hip",
-           "dispatch_noalloc.hip"]
+           "dispatch_noalloc.hip", "dispatch_experts_api.cpp", "dispatch_gate.hip", "dispatch_quantize.hip",
+           "dispatch_expert_product.hip"]
 
 HIPCC_FLAGS = [
     f"--offload-arch={ARCH}",

@@ -1,0 +1,106 @@
+// Arithmetic helpers of the gate, quantisation and product kernels (included
+// by .hip files only).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace moe_dispatch {
+
+constexpr float kFp8Max = 448.f;  // largest finite e4m3 value
+// The floor of a block's largest magnitude: below it 448 / amax would leave
+// fp32's range, and a block of zeros would have no scale.
+constexpr float kAmaxFloor = 0x1p-100f;
+
+__device__ __forceinline__ float bf16_low(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// Two fp32 values rounded to bf16 (to nearest, ties to even), packed.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    const bf16x2 v = {(__bf16)lo, (__bf16)hi};
+    return __builtin_bit_cast(uint32_t, v);
+}
+
+// Four fp32 values rounded to e4m3 (to nearest, ties to even), packed.
+__device__ __forceinline__ uint32_t pack_fp8(float a, float b, float c, float d) {
+    int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
+}
+
+// DPP controls: rotations within a row of 16 lanes, and broadcasts of a
+// row's last lane into the following rows.
+constexpr int kDppRowShr = 0x110;
+constexpr int kDppRowRor = 0x120;
+constexpr int kDppBcast15 = 0x142;
+constexpr int kDppBcast31 = 0x143;
+
+template <int kCtrl>
+__device__ __forceinline__ uint32_t dpp_ror(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, kCtrl, 0xf, 0xf, false);
+}
+
+// Largest of the 16 lanes of a row, in every lane of the row.
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {
+    uint32_t o = dpp_ror<kDppRowRor + 1>(v);
+    v = v > o ? v : o;
+    o = dpp_ror<kDppRowRor + 2>(v);
+    v = v > o ? v : o;
+    o = dpp_ror<kDppRowRor + 4>(v);
+    v = v > o ? v : o;
+    o = dpp_ror<kDppRowRor + 8>(v);
+    return v > o ? v : o;
+}
+
+// One block's 8 channels of a lane: quantised to dst, the scale by lane 0.
+__device__ __forceinline__ void quantize8(const float (&v)[8], bool live, bool first, uint8_t* dst, float* sf) {
+    // The largest magnitude by its bits, which order as the values do, NaN
+    // above infinity.
+    uint32_t top = __float_as_uint(kAmaxFloor);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t m = __float_as_uint(v[i]) & 0x7fffffffu;
+        top = top > m ? top : m;
+    }
+    const float amax = __uint_as_float(row_max(top));
+    const float scale = kFp8Max / amax;
+    uint2 o;
+    o.x = pack_fp8(v[0] * scale, v[1] * scale, v[2] * scale, v[3] * scale);
+    o.y = pack_fp8(v[4] * scale, v[5] * scale, v[6] * scale, v[7] * scale);
+    if (live) *reinterpret_cast<uint2*>(dst) = o;
+    if (first) *sf = amax / kFp8Max;
+}
+
+// Reductions over the 64 lanes, the result uniform. The order of the sum is
+// fixed.
+template <int kCtrl, int kRows>
+__device__ __forceinline__ float dpp_float(float old, float v) {
+    return __int_as_float(
+        __builtin_amdgcn_update_dpp(__float_as_int(old), __float_as_int(v), kCtrl, kRows, 0xf, false));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+    v += dpp_float<kDppRowShr + 1, 0xf>(0.f, v);
+    v += dpp_float<kDppRowShr + 2, 0xf>(0.f, v);
+    v += dpp_float<kDppRowShr + 4, 0xf>(0.f, v);
+    v += dpp_float<kDppRowShr + 8, 0xf>(0.f, v);
+    v += dpp_float<kDppBcast15, 0xa>(0.f, v);
+    v += dpp_float<kDppBcast31, 0xc>(0.f, v);
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+// NaN is ignored (every lane's value may be NaN: then the result is -inf).
+__device__ __forceinline__ float wave_max(float v) {
+    const float low = -__builtin_inff();
+    v = fmaxf(v, low);
+    v = fmaxf(v, dpp_float<kDppRowShr + 1, 0xf>(low, v));
+    v = fmaxf(v, dpp_float<kDppRowShr + 2, 0xf>(low, v));
+    v = fmaxf(v, dpp_float<kDppRowShr + 4, 0xf>(low, v));
+    v = fmaxf(v, dpp_float<kDppRowShr + 8, 0xf>(low, v));
+    v = fmaxf(v, dpp_float<kDppBcast15, 0xa>(low, v));
+    v = fmaxf(v, dpp_float<kDppBcast31, 0xc>(low, v));
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+
+// 1 / (1 + exp(-z)), the division rounded correctly.
+__device__ __forceinline__ float sigmoid(float z) { return 1.f / (1.f + expf(-z)); }
+
+}  // namespace moe_dispatch
