@@ -53,7 +53,7 @@ struct Tile {
     int expert;
     int n;
     int rows;
-    int64_t row;
+    int row;
 };
 
 // Live rows of expert e: within the buffer, never negative.
@@ -106,11 +106,12 @@ __device__ __forceinline__ Tile find_tile(const ProductParams& p, int64_t item) 
             const int first = __builtin_amdgcn_readlane(upto, l) - mine;
             const int live = __builtin_amdgcn_readlane(rows, l);
             const int local = (int)item - first * p.n_tiles;
-            t.expert = base + l;
-            t.n = local / mine;
+            // (All uniform; said so, they stay in scalar registers.)
+            t.expert = __builtin_amdgcn_readfirstlane(base + l);
+            t.n = __builtin_amdgcn_readfirstlane(local / mine);
             const int m = local - t.n * mine;
-            t.row = (int64_t)p.psum[t.expert] + (int64_t)m * kRows;
-            t.rows = live - m * kRows < kRows ? live - m * kRows : kRows;
+            t.row = __builtin_amdgcn_readfirstlane(p.psum[t.expert] + m * kRows);
+            t.rows = __builtin_amdgcn_readfirstlane(live - m * kRows < kRows ? live - m * kRows : kRows);
             return t;
         }
         before = __builtin_amdgcn_readlane(upto, kWave - 1);
@@ -190,8 +191,8 @@ stream_kernel(ProductParams p) {
         for (int m = 0; m < kTokens; ++m) {
             int r = m * 16 + col;
             r = r < t.rows ? r : t.rows - 1;
-            x[m] = p.x + (t.row + r) * p.K;
-            xs[m] = p.x_sf + (t.row + r) * p.k_blocks;
+            x[m] = p.x + (int64_t)(t.row + r) * p.K;
+            xs[m] = p.x_sf + (int64_t)(t.row + r) * p.k_blocks;
         }
         f32x4 acc[4][kTokens];
 #pragma unroll
@@ -254,7 +255,7 @@ stream_kernel(ProductParams p) {
                             uint2 o;
                             o.x = pack_bf16(acc[f][m][0], acc[f][m][1]);
                             o.y = pack_bf16(acc[f][m][2], acc[f][m][3]);
-                            *reinterpret_cast<uint2*>(out + (t.row + r) * p.N + n) = o;
+                            *reinterpret_cast<uint2*>(out + (int64_t)(t.row + r) * p.N + n) = o;
                         }
                     }
                 }
@@ -282,8 +283,8 @@ stream_kernel(ProductParams p) {
                     float v[8];
 #pragma unroll
                     for (int q = 0; q < 8; ++q) v[q] = g[q] * sigmoid(g[q]) * g[128 + q];
-                    uint8_t* dst = static_cast<uint8_t*>(p.out) + (t.row + token) * I + t.n * 128 + c;
-                    quantize8(v, true, c == 0, dst, p.out_sf + (t.row + token) * (I / 128) + t.n);
+                    uint8_t* dst = static_cast<uint8_t*>(p.out) + (int64_t)(t.row + token) * I + t.n * 128 + c;
+                    quantize8(v, true, c == 0, dst, p.out_sf + (int64_t)(t.row + token) * (I / 128) + t.n);
                 }
             }
             __syncthreads();
@@ -306,11 +307,279 @@ hipError_t launch_stream(ProductParams p, int64_t max_rows, hipStream_t stream) 
                            dim3(Shape::kWaves * kWave), args, shared, stream);
 }
 
+// ----------------------------------------------------- many rows per expert
+//
+// A workgroup of eight wavefronts computes 256 weight rows x 64 * kMt tokens.
+// Both operands go through LDS in stages of one 128-channel block, loaded
+// straight into it (no registers), two stages deep: while one is computed the
+// next is on its way. Wavefront (h, q) takes weight rows [128 h, 128 h + 128)
+// (for the SwiGLU product h = 0 are gate rows and h = 1 the up rows of the same
+// channels) and the q-th quarter of the tokens: the weights' scale is then one
+// number per wavefront and block. The sums stay in registers: fp32 updates
+// need them among the 256 that vector instructions reach, which is what
+// bounds a wavefront's tile to 128 x 64.
+//
+// A stage's row is 128 bytes, eight 16-byte chunks; chunk c of row r lies at
+// place c ^ (r % 8), so that the 16 rows a read instruction touches at one
+// chunk spread over the banks. Loads into LDS fill it in lane order, so the
+// permutation is applied to the addresses they read from.
+template <int kMt>
+struct TileShape {
+    static constexpr int kWaves = 8;
+    static constexpr int kTokens = 64 * kMt;
+    static constexpr int kWeightBytes = 256 * 128;
+    static constexpr int kStageBytes = kWeightBytes + kTokens * 128;
+    static constexpr int kScaleBlocks = 8;  // blocks whose x scales are staged at a time
+    static constexpr int kScaleFloats = kScaleBlocks * kTokens;
+    static constexpr int kLdsBytes = 2 * kStageBytes + 2 * (kScaleFloats + 2 * kScaleBlocks) * 4;
+};
+
+typedef __attribute__((address_space(3))) void lds_void;
+
+// Loads eight rows of a stage: 1 KB in lane order at dst. Lane offsets past
+// the descriptor's range read as zeros.
+__device__ __forceinline__ void load_rows(__amdgpu_buffer_rsrc_t src, uint8_t* dst, int lane_offset, int k) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (lds_void*)dst, 16, lane_offset, k, 0, 0);
+}
+
+__device__ __forceinline__ i32x8 read_fragment(const uint8_t* at, int lo, int hi) {
+    const u32x4 a = *reinterpret_cast<const u32x4*>(at + lo);
+    const u32x4 b = *reinterpret_cast<const u32x4*>(at + hi);
+    return i32x8{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
+}
+
+template <int kMt, bool kSwiglu>
+__global__ void __launch_bounds__(TileShape<kMt>::kWaves * kWave, 2) tile_kernel(ProductParams p) {
+    using Shape = TileShape<kMt>;
+    extern __shared__ __align__(16) uint8_t smem[];
+    float* const scales = reinterpret_cast<float*>(smem + 2 * Shape::kStageBytes);
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int half = wave & 1, quarter = wave >> 1;
+    const int col = lane & 15, quad = lane >> 4;
+    const int64_t total = (int64_t)count_row_tiles<Shape::kTokens>(p) * p.n_tiles;
+    // Reads: this lane's two chunks within the first 16 rows of a fragment.
+    const int read_lo = col * 128 + ((quad ^ (col & 7)) << 4);
+    const int read_hi = read_lo ^ 64;
+    // Loads: this lane's chunk within 8 rows.
+    const int load_row = lane >> 3;
+    const int load_k = ((lane & 7) ^ load_row) << 4;
+    for (int64_t i = blockIdx.x; i < (total + kXcds - 1) / kXcds * kXcds; i += gridDim.x) {
+        const int64_t item = xcd_item(i, total);
+        if (item >= total) continue;
+        const Tile t = find_tile<Shape::kTokens>(p, item);
+        // Weight rows of this wavefront's half; the other operand's loads are
+        // split over the wavefronts the same way: 32 weight rows and 8 kMt
+        // token rows each.
+        const int n_half = kSwiglu ? t.n * 128 + half * (p.N / 2) : t.n * 256 + half * 128;
+        int n_rows = p.N - n_half;
+        n_rows = __builtin_amdgcn_readfirstlane(n_rows < 0 ? 0 : (n_rows > 128 ? 128 : n_rows));
+        const int64_t w_row = n_rows > 0 ? (int64_t)t.expert * p.N + n_half : 0;
+        const auto w_src = __builtin_amdgcn_make_buffer_rsrc((void*)(p.w + w_row * p.K), 0, n_rows * p.K, kBufferWord3);
+        const auto x_src =
+            __builtin_amdgcn_make_buffer_rsrc((void*)(p.x + (int64_t)t.row * p.K), 0, t.rows * p.K, kBufferWord3);
+        const int w_first = quarter * 32, x_first = wave * 8 * kMt;
+        // Rows past the last one load that one again; their sums are dropped.
+        int w_offset[4], x_offset[kMt];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int r = w_first + j * 8 + load_row;
+            w_offset[j] = (r < n_rows ? r : (n_rows > 0 ? n_rows - 1 : 0)) * p.K + load_k;
+        }
+#pragma unroll
+        for (int j = 0; j < kMt; ++j) {
+            const int r = x_first + j * 8 + load_row;
+            x_offset[j] = (r < t.rows ? r : t.rows - 1) * p.K + load_k;
+        }
+        auto load_stage = [&](int kb) {
+            uint8_t* const stage = smem + (kb & 1) * Shape::kStageBytes;
+            // Chunks past K (a multiple of 16) are sent out of range.
+            const int k = kb * 128;
+            const int out = k + load_k < p.K ? 0 : INT32_MIN;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                load_rows(w_src, stage + (half * 128 + w_first + j * 8) * 128, w_offset[j] | out, k);
+#pragma unroll
+            for (int j = 0; j < kMt; ++j)
+                load_rows(x_src, stage + Shape::kWeightBytes + (x_first + j * 8) * 128, x_offset[j] | out, k);
+        };
+        // Scales, eight blocks at a time: a thread carries kMt blocks of one
+        // token's, the first 16 threads one block of a half's weights. (Past
+        // the last block the last one is loaded again and not used.)
+        constexpr int kS = Shape::kScaleBlocks;
+        const int s_token = threadIdx.x / kS * kMt + (threadIdx.x % kS) / (kS / kMt);
+        const int s_block = (threadIdx.x % (kS / kMt)) * kMt;
+        const int w_half = kSwiglu ? t.n * 128 + ((threadIdx.x / kS) & 1) * (p.N / 2) : t.n * 256 + ((threadIdx.x / kS) & 1) * 128;
+        int w_block = w_half >> 7;
+        w_block = w_block < p.n_blocks ? w_block : p.n_blocks - 1;
+        const float* const s_src =
+            p.x_sf + (int64_t)(t.row + (s_token < t.rows ? s_token : t.rows - 1)) * p.k_blocks;
+        const float* const ws_src = p.w_sf + ((int64_t)t.expert * p.n_blocks + w_block) * p.k_blocks;
+        float s_next[kMt], ws_next;
+        auto load_scales = [&](int chunk) {
+#pragma unroll
+            for (int j = 0; j < kMt; ++j) {
+                const int kb = chunk * kS + s_block + j;
+                s_next[j] = s_src[kb < p.k_blocks ? kb : p.k_blocks - 1];
+            }
+            const int kb = chunk * kS + (int)(threadIdx.x % kS);
+            ws_next = ws_src[kb < p.k_blocks ? kb : p.k_blocks - 1];
+        };
+        auto store_scales = [&](int chunk) {
+            float* const dst = scales + (chunk & 1) * (Shape::kScaleFloats + 2 * kS);
+#pragma unroll
+            for (int j = 0; j < kMt; ++j) dst[(s_block + j) * Shape::kTokens + s_token] = s_next[j];
+            if (threadIdx.x < 2 * kS) dst[Shape::kScaleFloats + threadIdx.x] = ws_next;
+        };
+
+        f32x4 acc[8][kMt];
+#pragma unroll
+        for (int f = 0; f < 8; ++f)
+#pragma unroll
+            for (int m = 0; m < kMt; ++m) acc[f][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+        load_stage(0);
+        load_scales(0);
+        store_scales(0);
+        for (int kb = 0; kb < p.k_blocks; ++kb) {
+            // This wavefront's part of the stage has arrived; past the
+            // barrier everybody's has, and the other stage is free.
+            __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+            __syncthreads();
+            // The next blocks' scales are loaded at the first block of eight
+            // and stored at the second, when nobody reads their place.
+            const int chunk = kb / kS, in_chunk = kb % kS;
+            if (in_chunk == 1) store_scales(chunk + 1);
+            if (in_chunk == 0) load_scales(chunk + 1);
+            if (kb + 1 < p.k_blocks) load_stage(kb + 1);
+            const uint8_t* const stage = smem + (kb & 1) * Shape::kStageBytes;
+            const uint8_t* const w_at = stage + half * 128 * 128;
+            const uint8_t* const x_at = stage + Shape::kWeightBytes + quarter * 16 * kMt * 128;
+            const float* const s_chunk = scales + (chunk & 1) * (Shape::kScaleFloats + 2 * kS);
+            const float* const s_at = s_chunk + in_chunk * Shape::kTokens + quarter * 16 * kMt + col;
+            const float sw = s_chunk[Shape::kScaleFloats + half * kS + in_chunk];
+            i32x8 b[kMt];
+            float s[kMt];
+#pragma unroll
+            for (int m = 0; m < kMt; ++m) {
+                b[m] = read_fragment(x_at + m * 16 * 128, read_lo, read_hi);
+                s[m] = s_at[m * 16] * sw;
+            }
+            f32x4 y[kMt];
+            i32x8 a = read_fragment(w_at, read_lo, read_hi);
+#pragma unroll
+            for (int f = 0; f < 9; ++f) {
+                // Rows f are multiplied while rows f + 1 are read and the
+                // products of rows f - 1 added. (The barriers to scheduling
+                // keep the steps apart: moved together, their operands no
+                // longer fit the registers.)
+                i32x8 next = a;
+                if (f < 7) next = read_fragment(w_at + (f + 1) * 16 * 128, read_lo, read_hi);
+#pragma unroll
+                for (int m = 0; m < kMt; ++m) {
+                    const f32x4 last = y[m];
+                    if (f < 8) y[m] = mfma_block(a, b[m]);
+                    if (f > 0) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) acc[f - 1][m][q] = __builtin_fmaf(s[m], last[q], acc[f - 1][m][q]);
+                    }
+                }
+                a = next;
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        if (!kSwiglu) {
+            uint16_t* out = static_cast<uint16_t*>(p.out);
+#pragma unroll
+            for (int m = 0; m < kMt; ++m) {
+                const int r = (quarter * kMt + m) * 16 + col;
+                if (r < t.rows) {
+#pragma unroll
+                    for (int f = 0; f < 8; ++f) {
+                        const int n = f * 16 + quad * 4;
+                        if (n < n_rows) {  // N is a multiple of 8
+                            uint2 o;
+                            o.x = pack_bf16(acc[f][m][0], acc[f][m][1]);
+                            o.y = pack_bf16(acc[f][m][2], acc[f][m][3]);
+                            *reinterpret_cast<uint2*>(out + (int64_t)(t.row + r) * p.N + n_half + n) = o;
+                        }
+                    }
+                }
+            }
+        } else {
+            // The up wavefronts hand their sums over through LDS, in the
+            // order of their registers.
+            __syncthreads();
+            f32x4* const swap = reinterpret_cast<f32x4*>(smem) + quarter * 8 * kMt * kWave;
+            if (half == 1) {
+#pragma unroll
+                for (int f = 0; f < 8; ++f)
+#pragma unroll
+                    for (int m = 0; m < kMt; ++m) swap[(f * kMt + m) * kWave + lane] = acc[f][m];
+            }
+            __syncthreads();
+            if (half == 0) {
+                const int I = p.N / 2;
+#pragma unroll
+                for (int m = 0; m < kMt; ++m) {
+                    uint32_t top = __float_as_uint(kAmaxFloor);
+#pragma unroll
+                    for (int f = 0; f < 8; ++f) {
+                        const f32x4 u = swap[(f * kMt + m) * kWave + lane];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const float g = acc[f][m][q];
+                            const float a = g * sigmoid(g) * u[q];
+                            acc[f][m][q] = a;
+                            const uint32_t mag = __float_as_uint(a) & 0x7fffffffu;
+                            top = top > mag ? top : mag;
+                        }
+                    }
+                    // A token's 128 channels are in the four lanes col + 16 i.
+                    uint32_t other = __shfl_xor(top, 16);
+                    top = top > other ? top : other;
+                    other = __shfl_xor(top, 32);
+                    top = top > other ? top : other;
+                    const float amax = __uint_as_float(top);
+                    const float scale = kFp8Max / amax;
+                    const int r = (quarter * kMt + m) * 16 + col;
+                    if (r < t.rows) {
+                        uint8_t* dst = static_cast<uint8_t*>(p.out) + (int64_t)(t.row + r) * I + t.n * 128 + quad * 4;
+#pragma unroll
+                        for (int f = 0; f < 8; ++f)
+                            *reinterpret_cast<uint32_t*>(dst + f * 16) =
+                                pack_fp8(acc[f][m][0] * scale, acc[f][m][1] * scale, acc[f][m][2] * scale,
+                                         acc[f][m][3] * scale);
+                        if (quad == 0) p.out_sf[(int64_t)(t.row + r) * (I / 128) + t.n] = amax / kFp8Max;
+                    }
+                }
+            }
+        }
+        __syncthreads();
+    }
+}
+
+template <int kMt, bool kSwiglu>
+hipError_t launch_tile(ProductParams p, int64_t max_rows, hipStream_t stream) {
+    using Shape = TileShape<kMt>;
+    p.n_tiles = kSwiglu ? p.N / 256 : (p.N + 255) / 256;
+    const int64_t row_tiles =
+        max_rows / Shape::kTokens + (max_rows < p.num_experts ? max_rows : p.num_experts);
+    int64_t groups = (row_tiles * p.n_tiles + kXcds - 1) / kXcds * kXcds;
+    if (groups > 65536) groups = 65536;
+    if (groups < kXcds) groups = kXcds;
+    void* args[] = {&p};
+    return hipLaunchKernel((const void*)&tile_kernel<kMt, kSwiglu>, dim3((unsigned)groups),
+                           dim3(Shape::kWaves * kWave), args, Shape::kLdsBytes, stream);
+}
+
 template <bool kSwiglu>
 hipError_t launch(const ProductParams& p, int64_t max_rows, hipStream_t stream) {
     const int64_t mean = max_rows / p.num_experts;
     if (mean <= 16) return launch_stream<1, kSwiglu>(p, max_rows, stream);
-    return launch_stream<2, kSwiglu>(p, max_rows, stream);
+    if (mean <= 32) return launch_stream<2, kSwiglu>(p, max_rows, stream);
+    if (mean <= 64) return launch_tile<1, kSwiglu>(p, max_rows, stream);
+    if (mean <= 192) return launch_tile<2, kSwiglu>(p, max_rows, stream);
+    return launch_tile<4, kSwiglu>(p, max_rows, stream);
 }
 
 }  // namespace
