@@ -9,18 +9,32 @@
 
 namespace moe_dispatch {
 
-constexpr int kGateMaxGroups = 256;  // workgroups of the gate's kernels: one per CU
+constexpr int kGateMaxGroups = 512;  // workgroups of a gate forward with balance outputs
 
 // Workgroups of a gate forward with balance outputs: each leaves one partial
 // row of E probability sums, E counts and its live tokens.
 inline int gate_groups(int64_t num_tokens, int waves) {
+    // One token per wavefront up to 256 workgroups, one per CU; a second one
+    // per CU (better hidden latencies, but twice the partial rows) where each
+    // wavefront still gets two tokens.
     const int64_t g = (num_tokens + waves - 1) / waves;
-    return g < 1 ? 1 : (g < kGateMaxGroups ? (int)g : kGateMaxGroups);
+    if (g <= kGateMaxGroups / 2) return g < 1 ? 1 : (int)g;
+    return g < 2 * kGateMaxGroups ? kGateMaxGroups / 2 : kGateMaxGroups;
 }
 inline size_t gate_partial_words(int32_t num_experts) { return 2 * (size_t)num_experts + 1; }
-inline size_t gate_workspace_bytes(int32_t num_experts) {
-    return (kGateMaxGroups * gate_partial_words(num_experts) * 4 + 255) & ~size_t(255);
+// Workspace: the partial rows, then the parts of the loss (one double for
+// each 16 experts) and the ticket of the workgroups that add them.
+struct GateWorkspace {
+    size_t loss_part, ticket, bytes;
+};
+inline GateWorkspace gate_workspace(int32_t num_experts) {
+    GateWorkspace w;
+    w.loss_part = (kGateMaxGroups * gate_partial_words(num_experts) * 4 + 255) & ~size_t(255);
+    w.ticket = w.loss_part + DISPATCH_MAX_EXPERTS / 16 * sizeof(double);
+    w.bytes = w.ticket + 256;
+    return w;
 }
+inline size_t gate_workspace_bytes(int32_t num_experts) { return gate_workspace(num_experts).bytes; }
 
 hipError_t launch_gate(const dispatch_gate_problem_t& p, const void* logits, const float* select_bias,
                        const uint8_t* token_mask, const dispatch_gate_out_t& out, void* workspace,
