@@ -481,13 +481,23 @@ typedef struct dispatch_expert_problem {
                                  its grid, more rows are computed all the same */
 } dispatch_expert_problem_t;
 
+/* Bytes of device workspace with which both products may share a tile's K
+ * among workgroups when there are too few tiles for the GPU (few rows, as in
+ * decoding; 0 where they would not). It must be 256-byte aligned and
+ * zero-filled before its first use; every call leaves it ready for the next
+ * of any problem that fits it, and nothing else may write into it. Calls that overlap
+ * in time need their own. */
+int dispatch_expert_workspace_size(const dispatch_expert_problem_t* problem, size_t* bytes);
+
 /* x: device bytes [expert_rows, K]; x_sf: device fp32 [expert_rows,
  * ceil(K / 128)]; w: device bytes [E, N, K]; w_sf: device fp32 [E,
  * ceil(N / 128), ceil(K / 128)]; out: device bf16 [expert_rows, N]. x, w and
- * out are 16-byte aligned. */
+ * out are 16-byte aligned. workspace: NULL (no tile is shared), or of at least
+ * dispatch_expert_workspace_size() bytes. */
 int dispatch_expert_product(const dispatch_expert_problem_t* problem, const int32_t* expert_psum,
                             const int32_t* expert_count, const void* x, const float* x_sf, const void* w,
-                            const float* w_sf, void* out, hipStream_t stream);
+                            const float* w_sf, void* out, void* workspace, size_t workspace_bytes,
+                            hipStream_t stream);
 
 /* The product with gate and up weights and the activation behind it: N = 2I
  * weight rows, gate first; a = SwiGLU of y's halves in fp32 (y is not rounded
@@ -496,7 +506,8 @@ int dispatch_expert_product(const dispatch_expert_problem_t* problem, const int3
  * I / 128]. I must be a multiple of 128. */
 int dispatch_expert_product_swiglu(const dispatch_expert_problem_t* problem, const int32_t* expert_psum,
                                    const int32_t* expert_count, const void* x, const float* x_sf, const void* w,
-                                   const float* w_sf, void* out_q, float* out_sf, hipStream_t stream);
+                                   const float* w_sf, void* out_q, float* out_sf, void* workspace,
+                                   size_t workspace_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

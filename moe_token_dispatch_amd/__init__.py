@@ -20,7 +20,8 @@ from ._binding import (  # noqa: F401
     CombinePlan, STATUS_TIMEOUT, DEFAULT_WAIT_LIMIT, dispatch_set_wait_limit,
     GATE_NORMALIZE, GATE_SIGMOID, GATE_SOFTMAX, SF_BLOCK, ExpertProblem, ExpertProductPlan, ExpertSwigluPlan,
     GateBackwardPlan, GateOutPtrs, GatePlan, GateProblem, GateTensors, QuantizePlan, QuantizeProblem,
-    SwigluBackwardQuantizePlan, SwigluQuantizePlan, alloc_gate, alloc_gate_workspace, dispatch_expert_product,
+    SwigluBackwardQuantizePlan, SwigluQuantizePlan, alloc_expert_workspace, alloc_gate, alloc_gate_workspace,
+    dispatch_expert_product, dispatch_expert_workspace_size,
     dispatch_expert_product_swiglu, dispatch_gate, dispatch_gate_backward, dispatch_gate_workspace_size,
     dispatch_quantize, dispatch_swiglu_backward_quantize, dispatch_swiglu_quantize, make_expert_problem,
     make_gate_problem,

@@ -165,8 +165,8 @@ SYMBOLS = ("dispatch_abi_version", "dispatch_strerror", "dispatch_workspace_size
            "dispatch_expand_workspace_size", "dispatch_expand_max_rows", "dispatch_expand_layout",
            "dispatch_expand_scatter", "dispatch_expand_layout_and_scatter", "dispatch_combine",
            "dispatch_gate_workspace_size", "dispatch_gate", "dispatch_gate_backward", "dispatch_quantize",
-           "dispatch_swiglu_quantize", "dispatch_swiglu_backward_quantize", "dispatch_expert_product",
-           "dispatch_expert_product_swiglu")
+           "dispatch_swiglu_quantize", "dispatch_swiglu_backward_quantize", "dispatch_expert_workspace_size",
+           "dispatch_expert_product", "dispatch_expert_product_swiglu")
 
 
 def load_library(path: str = LIB_PATH):
@@ -224,8 +224,9 @@ def load_library(path: str = LIB_PATH):
                        ("dispatch_quantize", [qp, p, p, p, p, p]),
                        ("dispatch_swiglu_quantize", [qp, p, p, p, p, p]),
                        ("dispatch_swiglu_backward_quantize", [qp, p, p, p, p, p, p]),
-                       ("dispatch_expert_product", [xp, p, p, p, p, p, p, p, p]),
-                       ("dispatch_expert_product_swiglu", [xp, p, p, p, p, p, p, p, p, p])):
+                       ("dispatch_expert_workspace_size", [xp, ctypes.POINTER(sz)]),
+                       ("dispatch_expert_product", [xp, p, p, p, p, p, p, p, p, sz, p]),
+                       ("dispatch_expert_product_swiglu", [xp, p, p, p, p, p, p, p, p, p, sz, p])):
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = i
     if lib.dispatch_abi_version() != ABI_VERSION:
@@ -1159,7 +1160,23 @@ def make_expert_problem(num_experts: int, in_features: int, out_features: int, e
                          expert_rows if max_routed_rows is None else max_routed_rows)
 
 
-def _expert_args(problem: ExpertProblem, expert_psum, expert_count, x, x_sf, w, w_sf, out, out_sf, swiglu, stream):
+def dispatch_expert_workspace_size(problem: ExpertProblem) -> int:
+    out = ctypes.c_size_t(0)
+    rc = load_library().dispatch_expert_workspace_size(ctypes.byref(problem), ctypes.byref(out))
+    if rc:
+        raise DispatchError(rc, "dispatch_expert_workspace_size")
+    return int(out.value)
+
+
+def alloc_expert_workspace(problem: ExpertProblem, device) -> Optional[torch.Tensor]:
+    """Workspace for the products of a problem: zero-filled, as its first use
+    requires; None where the problem has no use for one."""
+    n = dispatch_expert_workspace_size(problem)
+    return torch.zeros(n, dtype=torch.uint8, device=device) if n else None
+
+
+def _expert_args(problem: ExpertProblem, expert_psum, expert_count, x, x_sf, w, w_sf, out, out_sf, swiglu, workspace,
+                 stream):
     e, k, n, rows = problem.num_experts, problem.in_features, problem.out_features, problem.expert_rows
     _check_sized(expert_psum, "expert_psum", e + 1, torch.int32)
     _check_sized(expert_count, "expert_count", e, torch.int32)
@@ -1172,18 +1189,24 @@ def _expert_args(problem: ExpertProblem, expert_psum, expert_count, x, x_sf, w, 
         _check_sized(out_sf, "out_sf", rows * (n // 2 // SF_BLOCK), torch.float32)
     else:
         _check_sized(out, "out", rows * n, torch.bfloat16)
+    nbytes = 0
+    if workspace is not None:
+        _check_device_tensor(workspace, "workspace")
+        nbytes = workspace.numel() * workspace.element_size()
     outs = (_ptr(out), _ptr(out_sf)) if swiglu else (_ptr(out),)
     return (ctypes.byref(problem), _ptr(expert_psum), _ptr(expert_count), _ptr(x), _ptr(x_sf), _ptr(w), _ptr(w_sf),
-            *outs, _stream_handle(stream, w.device))
+            *outs, _ptr(workspace), nbytes, _stream_handle(stream, w.device))
 
 
 def dispatch_expert_product(problem: ExpertProblem, expert_psum: torch.Tensor, expert_count: torch.Tensor,
                             x: torch.Tensor, x_sf: torch.Tensor, w: torch.Tensor, w_sf: torch.Tensor,
-                            out: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> None:
+                            out: torch.Tensor, workspace: Optional[torch.Tensor] = None,
+                            stream: Optional[torch.cuda.Stream] = None) -> None:
     """Enqueue out[r] = x[r] @ w[e].T for the rows r of each expert e (fp8
-    operands with block scales, bf16 out)."""
+    operands with block scales, bf16 out). ``workspace``: from
+    alloc_expert_workspace, for few rows (optional)."""
     rc = load_library().dispatch_expert_product(*_expert_args(problem, expert_psum, expert_count, x, x_sf, w, w_sf,
-                                                              out, None, False, stream))
+                                                              out, None, False, workspace, stream))
     if rc:
         raise DispatchError(rc, "dispatch_expert_product")
 
@@ -1191,44 +1214,48 @@ def dispatch_expert_product(problem: ExpertProblem, expert_psum: torch.Tensor, e
 def dispatch_expert_product_swiglu(problem: ExpertProblem, expert_psum: torch.Tensor, expert_count: torch.Tensor,
                                    x: torch.Tensor, x_sf: torch.Tensor, w: torch.Tensor, w_sf: torch.Tensor,
                                    out_q: torch.Tensor, out_sf: torch.Tensor,
+                                   workspace: Optional[torch.Tensor] = None,
                                    stream: Optional[torch.cuda.Stream] = None) -> None:
     """Enqueue SwiGLU of that product (w [E, 2I, K], gate rows first),
     quantised: out_q [expert_rows, I] and out_sf [expert_rows, I / 128]."""
     rc = load_library().dispatch_expert_product_swiglu(*_expert_args(problem, expert_psum, expert_count, x, x_sf, w,
-                                                                     w_sf, out_q, out_sf, True, stream))
+                                                                     w_sf, out_q, out_sf, True, workspace, stream))
     if rc:
         raise DispatchError(rc, "dispatch_expert_product_swiglu")
 
 
 class ExpertProductPlan:
-    """A prepared dispatch_expert_product, like Plan."""
+    """A prepared dispatch_expert_product, like Plan. A plan of few rows makes
+    a workspace of its own unless it is given one, so a plan's calls must not
+    overlap in time."""
 
     def __init__(self, problem: ExpertProblem, expert_psum: torch.Tensor, expert_count: torch.Tensor,
                  x: torch.Tensor, x_sf: torch.Tensor, w: torch.Tensor, w_sf: torch.Tensor, out: torch.Tensor,
-                 stream: Optional[torch.cuda.Stream] = None):
-        problem = ExpertProblem.from_buffer_copy(problem)
-        self._args = _expert_args(problem, expert_psum, expert_count, x, x_sf, w, w_sf, out, None, False, stream)
-        self._keep = (problem, expert_psum, expert_count, x, x_sf, w, w_sf, out)
+                 workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
+        self._prepare(False, problem, (expert_psum, expert_count, x, x_sf, w, w_sf), out, None, workspace, stream)
         self._call = load_library().dispatch_expert_product
+
+    def _prepare(self, swiglu, problem, ins, out, out_sf, workspace, stream):
+        problem = ExpertProblem.from_buffer_copy(problem)
+        if workspace is None:
+            # Cleared on the stream that the calls run on.
+            with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(ins[4].device)):
+                workspace = alloc_expert_workspace(problem, ins[4].device)
+        self._args = _expert_args(problem, *ins, out, out_sf, swiglu, workspace, stream)
+        self._keep = (problem, ins, out, out_sf, workspace)
 
     def __call__(self) -> None:
         rc = self._call(*self._args)
         if rc:
-            raise DispatchError(rc, "dispatch_expert_product")
+            raise DispatchError(rc, self._call.__name__)
 
 
-class ExpertSwigluPlan:
-    """A prepared dispatch_expert_product_swiglu, like Plan."""
+class ExpertSwigluPlan(ExpertProductPlan):
+    """A prepared dispatch_expert_product_swiglu, like ExpertProductPlan."""
 
     def __init__(self, problem: ExpertProblem, expert_psum: torch.Tensor, expert_count: torch.Tensor,
                  x: torch.Tensor, x_sf: torch.Tensor, w: torch.Tensor, w_sf: torch.Tensor, out_q: torch.Tensor,
-                 out_sf: torch.Tensor, stream: Optional[torch.cuda.Stream] = None):
-        problem = ExpertProblem.from_buffer_copy(problem)
-        self._args = _expert_args(problem, expert_psum, expert_count, x, x_sf, w, w_sf, out_q, out_sf, True, stream)
-        self._keep = (problem, expert_psum, expert_count, x, x_sf, w, w_sf, out_q, out_sf)
+                 out_sf: torch.Tensor, workspace: Optional[torch.Tensor] = None,
+                 stream: Optional[torch.cuda.Stream] = None):
+        self._prepare(True, problem, (expert_psum, expert_count, x, x_sf, w, w_sf), out_q, out_sf, workspace, stream)
         self._call = load_library().dispatch_expert_product_swiglu
-
-    def __call__(self) -> None:
-        rc = self._call(*self._args)
-        if rc:
-            raise DispatchError(rc, "dispatch_expert_product_swiglu")

@@ -29,6 +29,11 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kXcds = 8;  // workgroup i runs on XCD i % 8
+constexpr int kCus = 256;
+
+// Tickets at the start of a workspace, as many as any problem shares tiles
+// (then there are at most kCus), so that one workspace serves several.
+constexpr size_t kTicketBytes = kCus * sizeof(uint32_t);
 
 struct ProductParams {
     const int32_t* psum;
@@ -46,6 +51,10 @@ struct ProductParams {
     int32_t k_blocks;   // ceil(K / 128)
     int32_t n_blocks;   // ceil(N / 128)
     int32_t n_tiles;    // tiles of the output's width
+    int32_t parts;      // workgroups that share a tile's K
+    int32_t slots;      // sums of them that the workspace holds
+    f32x4* sums;        // [slots][one workgroup's sums]
+    uint32_t* tickets;  // one per tile, zero between calls
 };
 
 // A product tile: rows [row, row + rows) of the buffer, tile n of the width.
@@ -76,45 +85,59 @@ __device__ __forceinline__ int wave_scan(int x) {
     return x;
 }
 
-// Row tiles of kRows rows over all experts.
+// Row tiles of kRows rows. Lane l looks at experts l, l + 64, ...; what it
+// found of the first 64 stays in registers, so that with at most that many
+// experts a workgroup reads their counts once.
 template <int kRows>
-__device__ __forceinline__ int count_row_tiles(const ProductParams& p) {
-    const int lane = threadIdx.x & (kWave - 1);
-    int tiles = 0;
-    for (int e = lane; e < p.num_experts; e += kWave) tiles += (live_rows(p, e) + kRows - 1) / kRows;
-    return __builtin_amdgcn_readlane(wave_scan(tiles), kWave - 1);
-}
+struct RowTiles {
+    int first, rows, tiles, upto;  // lane's expert of the first 64: first row, rows, tiles, tiles up to and with it
+    int total;                     // over all experts
+
+    __device__ __forceinline__ explicit RowTiles(const ProductParams& p) {
+        const int lane = threadIdx.x & (kWave - 1);
+        look(p, lane);
+        int more = 0;
+        for (int e = lane + kWave; e < p.num_experts; e += kWave) more += (live_rows(p, e) + kRows - 1) / kRows;
+        upto = wave_scan(tiles);
+        total = __builtin_amdgcn_readlane(upto, kWave - 1);
+        if (p.num_experts > kWave) total += __builtin_amdgcn_readlane(wave_scan(more), kWave - 1);
+    }
+    __device__ __forceinline__ void look(const ProductParams& p, int e) {
+        rows = e < p.num_experts ? live_rows(p, e) : 0;
+        first = rows > 0 ? p.psum[e] : 0;
+        tiles = (rows + kRows - 1) / kRows;
+    }
+};
 
 // Tile `item` in the order expert, tile of the width, row tile: the row tiles
 // that read the same weights follow each other. Every wavefront finds it for
 // itself.
 template <int kRows>
-__device__ __forceinline__ Tile find_tile(const ProductParams& p, int64_t item) {
+__device__ __forceinline__ Tile find_tile(const ProductParams& p, RowTiles<kRows> at, int64_t item) {
     const int lane = threadIdx.x & (kWave - 1);
     const int target = (int)item / p.n_tiles;  // its row tile if each were taken whole (the same expert)
-    int before = 0;
     Tile t{};
     for (int base = 0; base < p.num_experts; base += kWave) {
-        const int e = base + lane;
-        const int rows = e < p.num_experts ? live_rows(p, e) : 0;
-        const int tiles = (rows + kRows - 1) / kRows;
-        const int upto = before + wave_scan(tiles);
-        const uint64_t past = __ballot(upto > target);
+        if (base > 0) {
+            const int before = __builtin_amdgcn_readlane(at.upto, kWave - 1);
+            at.look(p, base + lane);
+            at.upto = before + wave_scan(at.tiles);
+        }
+        const uint64_t past = __ballot(at.upto > target);
         if (past != 0) {
             const int l = __builtin_ctzll(past);
-            const int mine = __builtin_amdgcn_readlane(tiles, l);
-            const int first = __builtin_amdgcn_readlane(upto, l) - mine;
-            const int live = __builtin_amdgcn_readlane(rows, l);
+            const int mine = __builtin_amdgcn_readlane(at.tiles, l);
+            const int first = __builtin_amdgcn_readlane(at.upto, l) - mine;
+            const int live = __builtin_amdgcn_readlane(at.rows, l);
             const int local = (int)item - first * p.n_tiles;
             // (All uniform; said so, they stay in scalar registers.)
             t.expert = __builtin_amdgcn_readfirstlane(base + l);
             t.n = __builtin_amdgcn_readfirstlane(local / mine);
             const int m = local - t.n * mine;
-            t.row = __builtin_amdgcn_readfirstlane(p.psum[t.expert] + m * kRows);
+            t.row = __builtin_amdgcn_readlane(at.first, l) + m * kRows;
             t.rows = __builtin_amdgcn_readfirstlane(live - m * kRows < kRows ? live - m * kRows : kRows);
             return t;
         }
-        before = __builtin_amdgcn_readlane(upto, kWave - 1);
     }
     return t;  // not reached for item < row tiles * n_tiles: rows = 0
 }
@@ -126,30 +149,109 @@ __device__ __forceinline__ int64_t xcd_item(int64_t b, int64_t total) {
     return (b % kXcds) * run + b / kXcds;
 }
 
-// ------------------------------------------------------ few rows per expert
+// Eight wavefronts compute 256 weight rows x kTokens tokens. Both operands go
+// through LDS in stages of one 128-channel block, loaded straight into it (no
+// registers in between), kStages deep: while one is computed the next ones are
+// on their way. The wavefronts are kRowWaves x kTokenWaves over the tile.
 //
-// With few rows per expert the product reads weights and little else. A wave
-// holds 64 weight rows x 16 * kTokens tokens of sums and walks every kSplit-th
-// block of K, loading the weights straight into the matrix operands: each
-// weight byte is used by one wavefront only, so LDS would add a copy and save
-// nothing. The kSplit wavefronts of the same 64 rows add their sums through
-// LDS at the end, halving their number each time (a fixed order).
-template <int kTokens, bool kSwiglu>
-struct StreamShape {
-    static constexpr int kRowGroups = kSwiglu ? 4 : 1;  // 64 weight rows each
-    static constexpr int kSplit = kSwiglu ? 4 : 8;
-    static constexpr int kWaves = kRowGroups * kSplit;
-    static constexpr int kTileRows = 16 * kTokens;
-    static constexpr int kSliceFloats = 64 * kTileRows;  // one wavefront's sums
-    static constexpr int kLdsFloats = kRowGroups * (kSplit / 2) * kSliceFloats;
+// Many tokens: the fp32 sums fill the registers (vector instructions reach 256
+// of them, so a wavefront's tile is at most 128 x 64) and the LDS reads of a
+// block, 24 KB per wavefront, take about as long as its 32 matrix
+// instructions; two stages of 64 KB leave no room for a third.
+//
+// Few tokens: the product reads weights and little else, and what counts is
+// how many bytes are in flight: three stages of four, 96 KB per CU. (A kernel
+// that loaded the weights straight into the matrix operands, 16 rows x 64 bytes
+// per instruction, took 165 us for 512 rows x 32 experts x 7168 x 2048, this
+// one 91.) With fewer tiles than CUs a tile's K is shared by `parts`
+// workgroups: each leaves its sums in the workspace and takes a ticket; the
+// last one adds them all, in order, and goes on alone.
+//
+// For the SwiGLU product a tile is 128 gate rows and the 128 up rows of the
+// same channels: the first half of the row wavefronts takes the gate rows.
+//
+// A stage's row is 128 bytes, eight 16-byte chunks; chunk c of row r lies at
+// place c ^ (r % 8), so that the 16 rows a read instruction touches at one
+// chunk spread over the banks. Loads into LDS fill it in lane order, so the
+// permutation is applied to the addresses they read from.
+template <int kTokens_, int kRowWaves_, int kStages_>
+struct TileShape {
+    static constexpr int kWaves = 8;
+    static constexpr int kTokens = kTokens_;
+    static constexpr int kStages = kStages_;
+    static constexpr int kRowWaves = kRowWaves_;
+    static constexpr int kTokenWaves = kWaves / kRowWaves;
+    static constexpr int kRows = 256 / kRowWaves;                   // weight rows of a wavefront
+    static constexpr int kF = kRows / 16;                           // fragments of them
+    static constexpr int kM = kTokens / 16 / kTokenWaves;           // fragments of its tokens
+    static constexpr int kWeightBytes = 256 * 128;
+    static constexpr int kStageBytes = kWeightBytes + kTokens * 128;
+    // Loads of a wavefront per stage: 32 weight rows, its eighth of the token
+    // rows (8 per instruction; fewer use part of the lanes).
+    static constexpr int kXLoads = kTokens >= 64 ? kTokens / 64 : 1;
+    static constexpr int kXRows = kTokens / kWaves / kXLoads;       // rows of such a load
+    static constexpr int kLoads = 4 + kXLoads;
+    static constexpr int kScaleBlocks = 8;                          // blocks whose scales are staged at a time
+    static constexpr int kScaleFloats = kScaleBlocks * kTokens;
+    static constexpr int kChunkFloats = kScaleFloats + 2 * kScaleBlocks;
+    static constexpr int kRingBytes = kStages * kStageBytes;
+    static constexpr int kLdsBytes = kRingBytes + 2 * kChunkFloats * 4;
+    static constexpr int kSumFloats = 256 * kTokens;                // a tile's sums
+    // SwiGLU: a wavefront with all 128 channels of a half hands over through
+    // registers, smaller ones through rows of sums in LDS.
+    static constexpr int kSumRow = 256 + 4;
+    static constexpr bool kWholeBlock = kRows == 128;
+    static_assert(kWholeBlock || kTokens * kSumRow * 4 <= kRingBytes, "rows of sums");
+    static_assert(kLdsBytes <= kLdsPerCu, "LDS");
 };
 
-__device__ __forceinline__ i32x8 load_block(const uint8_t* row, int k, int K) {
-    // Chunks k and k + 64 of the row; beyond K (a multiple of 16) zeros.
-    u32x4 lo = {0u, 0u, 0u, 0u}, hi = {0u, 0u, 0u, 0u};
-    if (k < K) lo = *reinterpret_cast<const u32x4*>(row + k);
-    if (k + 64 < K) hi = *reinterpret_cast<const u32x4*>(row + k + 64);
-    return i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+// A raw buffer descriptor in scalar registers.
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ i32x4 descriptor(const void* base, int bytes) {
+    const uint64_t at = reinterpret_cast<uint64_t>(base);
+    return i32x4{__builtin_amdgcn_readfirstlane((int)at), __builtin_amdgcn_readfirstlane((int)(at >> 32) & 0xffff),
+                 __builtin_amdgcn_readfirstlane(bytes), kBufferWord3};
+}
+
+__device__ __forceinline__ int lds_address(const void* at) {
+    return (int)(uintptr_t)(const __attribute__((address_space(3))) void*)at;
+}
+
+// Loads 16 (4) bytes per lane, in lane order, to LDS address dst. Lane offsets past
+// the descriptor's range read as zeros. Written out, as the compiler does not
+// see that the stage being loaded is not the one being read and puts a wait
+// for the load before the reads. It returns nothing (and m0 is the compiler's
+// scratch register for such instructions, set before each use); wait_loads()
+// stands before the barrier that opens the stage.
+__device__ __forceinline__ void load_to_lds(const i32x4& src, int dst, int lane_offset, int k) {
+    asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+                 :
+                 : "v"(lane_offset), "s"(src), "s"(k), "s"(dst)
+                 : "memory");
+}
+
+__device__ __forceinline__ void load_dword_to_lds(const i32x4& src, int dst, int lane_offset, int k) {
+    asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dword %0, %1, %2 offen lds"
+                 :
+                 : "v"(lane_offset), "s"(src), "s"(k), "s"(dst)
+                 : "memory");
+}
+
+// Waits until at most kLeft of this wavefront's loads are outstanding (they
+// arrive in order; loads other than the stages' only make it wait longer).
+template <int kLeft>
+__device__ __forceinline__ void wait_loads() {
+    static_assert(kLeft < 64, "six bits");
+    __builtin_amdgcn_s_waitcnt((kLeft & 15) | (7 << 4) | (15 << 8) | ((kLeft >> 4) << 14));
+}
+
+// A barrier that does not wait for loads into LDS.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+__device__ __forceinline__ i32x8 read_fragment(const uint8_t* at, int lo, int hi) {
+    const u32x4 a = *reinterpret_cast<const u32x4*>(at + lo);
+    const u32x4 b = *reinterpret_cast<const u32x4*>(at + hi);
+    return i32x8{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
 }
 
 __device__ __forceinline__ f32x4 mfma_block(const i32x8& a, const i32x8& b) {
@@ -157,101 +259,213 @@ __device__ __forceinline__ f32x4 mfma_block(const i32x8& a, const i32x8& b) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, zero, 0, 0, 0, 0, 0, 0);
 }
 
-template <int kTokens, bool kSwiglu>
-__global__ void __launch_bounds__((StreamShape<kTokens, kSwiglu>::kWaves * kWave))
-stream_kernel(ProductParams p) {
-    using Shape = StreamShape<kTokens, kSwiglu>;
-    extern __shared__ __align__(16) float lds[];
+template <class Shape, bool kSwiglu>
+__global__ void __launch_bounds__(Shape::kWaves * kWave, 2) product_kernel(ProductParams p) {
+    constexpr int kF = Shape::kF, kM = Shape::kM, kS = Shape::kScaleBlocks, kStages = Shape::kStages;
+    extern __shared__ __align__(16) uint8_t smem[];
+    float* const scales = reinterpret_cast<float*>(smem + Shape::kRingBytes);
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int group = wave % Shape::kRowGroups, split = wave / Shape::kRowGroups;
+    const int row_wave = wave % Shape::kRowWaves, token_wave = wave / Shape::kRowWaves;
     const int col = lane & 15, quad = lane >> 4;
-    const int64_t total = (int64_t)count_row_tiles<Shape::kTileRows>(p) * p.n_tiles;
+    const int64_t tiles = (int64_t)RowTiles<Shape::kTokens>(p).total * p.n_tiles;
+    const int parts = tiles * p.parts <= p.slots ? p.parts : 1;  // more rows than announced: no room to share
+    const int64_t total = tiles * parts;
+    // Reads: this lane's two chunks within the first 16 rows of a fragment.
+    const int read_lo = col * 128 + ((quad ^ (col & 7)) << 4);
+    const int read_hi = read_lo ^ 64;
+    // Loads: this lane's row and chunk.
+    const int load_row = lane >> 3;
+    const int load_k = ((lane & 7) ^ load_row) << 4;
+    const int x_first = wave * (Shape::kTokens / Shape::kWaves);
+    const int x_load_k = ((lane & 7) ^ ((x_first + load_row) & 7)) << 4;
     for (int64_t i = blockIdx.x; i < (total + kXcds - 1) / kXcds * kXcds; i += gridDim.x) {
         const int64_t item = xcd_item(i, total);
         if (item >= total) continue;
-        const Tile t = find_tile<Shape::kTileRows>(p, item);
-        // First weight row of this wavefront: the SwiGLU product's groups 0
-        // and 1 take 128 gate rows, 2 and 3 the up rows of the same channels.
-        const int n0 = kSwiglu ? t.n * 128 + (group & 1) * 64 + (group >> 1) * (p.N / 2) : t.n * 64;
-        const uint8_t* w[4];
-        const uint8_t* x[kTokens];
-        const float* xs[kTokens];
-        const float* ws[4];
+        const int tile = (int)item / parts, part = (int)item - tile * parts;
+        // (Looked up again: kept, they would cost the loop below registers.)
+        const Tile t = find_tile(p, RowTiles<Shape::kTokens>(p), tile);
+        // The part's blocks of K.
+        const int k_first = (int)((int64_t)p.k_blocks * part / parts);
+        const int blocks = (int)((int64_t)p.k_blocks * (part + 1) / parts) - k_first;
+        // Loads of weights: wavefronts 0 to 3 the first 128 rows of the tile,
+        // 4 to 7 the second.
+        const int load_half = wave >> 2, w_first = (wave & 3) * 32;
+        auto half_row = [&](int half) { return kSwiglu ? t.n * 128 + half * (p.N / 2) : t.n * 256 + half * 128; };
+        int n_rows = p.N - half_row(load_half);
+        n_rows = __builtin_amdgcn_readfirstlane(n_rows < 0 ? 0 : (n_rows > 128 ? 128 : n_rows));
+        const int64_t w_row = n_rows > 0 ? (int64_t)t.expert * p.N + half_row(load_half) : 0;
+        const i32x4 w_src = descriptor(p.w + w_row * p.K, n_rows * p.K);
+        const i32x4 x_src = descriptor(p.x + (int64_t)t.row * p.K, t.rows * p.K);
+        // Rows past the last one load that one again; their sums are dropped.
+        int w_offset[4], x_offset[Shape::kXLoads];
 #pragma unroll
-        for (int f = 0; f < 4; ++f) {
-            int n = n0 + f * 16 + col;
-            n = n < p.N ? n : p.N - 1;  // (rows past the end are computed and dropped)
-            w[f] = p.w + ((int64_t)t.expert * p.N + n) * p.K;
-            int nb = (n0 + f * 16) >> 7;
-            nb = nb < p.n_blocks ? nb : p.n_blocks - 1;
-            ws[f] = p.w_sf + ((int64_t)t.expert * p.n_blocks + nb) * p.k_blocks;
+        for (int j = 0; j < 4; ++j) {
+            const int r = w_first + j * 8 + load_row;
+            w_offset[j] = (r < n_rows ? r : (n_rows > 0 ? n_rows - 1 : 0)) * p.K + load_k;
         }
 #pragma unroll
-        for (int m = 0; m < kTokens; ++m) {
-            int r = m * 16 + col;
-            r = r < t.rows ? r : t.rows - 1;
-            x[m] = p.x + (int64_t)(t.row + r) * p.K;
-            xs[m] = p.x_sf + (int64_t)(t.row + r) * p.k_blocks;
+        for (int j = 0; j < Shape::kXLoads; ++j) {
+            const int r = x_first + j * 8 + load_row;
+            x_offset[j] = (r < t.rows ? r : t.rows - 1) * p.K + x_load_k;
         }
-        f32x4 acc[4][kTokens];
+        auto load_stage = [&](int b) {
+            const int stage = lds_address(smem) + b % kStages * Shape::kStageBytes;
+            // Chunks past K (a multiple of 16) are sent out of range.
+            const int k = (k_first + b) * 128;
+            const int out = k + load_k < p.K ? 0 : INT32_MIN;
+            const int x_out = k + x_load_k < p.K ? 0 : INT32_MIN;
 #pragma unroll
-        for (int f = 0; f < 4; ++f)
+            for (int j = 0; j < 4; ++j)
+                load_to_lds(w_src, stage + (load_half * 128 + w_first + j * 8) * 128, w_offset[j] | out, k);
+            if (Shape::kXRows == 8 || load_row < Shape::kXRows) {
 #pragma unroll
-            for (int m = 0; m < kTokens; ++m) acc[f][m] = f32x4{0.f, 0.f, 0.f, 0.f};
-        for (int kb = split; kb < p.k_blocks; kb += Shape::kSplit) {
-            const int k = kb * 128 + quad * 16;
-            i32x8 a[4], b[kTokens];
-            float sx[kTokens];
-#pragma unroll
-            for (int f = 0; f < 4; ++f) a[f] = load_block(w[f], k, p.K);
-#pragma unroll
-            for (int m = 0; m < kTokens; ++m) {
-                b[m] = load_block(x[m], k, p.K);
-                sx[m] = xs[m][kb];
+                for (int j = 0; j < Shape::kXLoads; ++j)
+                    load_to_lds(x_src, stage + Shape::kWeightBytes + (x_first + j * 8) * 128, x_offset[j] | x_out, k);
             }
+        };
+        // Scales, eight blocks at a time, one wavefront for each: a lane per
+        // token, and the first wavefront's 16 lanes for the weights' halves.
+        // (Past the last block the last one is loaded again and not used.)
+        constexpr int kSLoads = (Shape::kTokens + kWave - 1) / kWave;
+        const i32x4 xs_src = descriptor(p.x_sf + (int64_t)t.row * p.k_blocks, t.rows * p.k_blocks * 4);
+        const int64_t ws_first = (int64_t)t.expert * p.n_blocks;
+        const i32x4 ws_src = descriptor(p.w_sf + ws_first * p.k_blocks, p.n_blocks * p.k_blocks * 4);
+        int w_block = half_row((lane / kS) & 1) >> 7;
+        w_block = w_block < p.n_blocks ? w_block : p.n_blocks - 1;
+        auto load_scales = [&](int chunk) {
+            const int dst = lds_address(scales) + (chunk & 1) * Shape::kChunkFloats * 4;
+            int b = chunk * kS + wave;
+            b = k_first + (b < blocks ? b : blocks - 1);
 #pragma unroll
-            for (int f = 0; f < 4; ++f) {
-                const float sw = ws[f][kb];
+            for (int j = 0; j < kSLoads; ++j) {
+                const int r = j * kWave + lane;
+                if (Shape::kTokens >= kWave || lane < Shape::kTokens)
+                    load_dword_to_lds(xs_src, dst + (wave * Shape::kTokens + j * kWave) * 4,
+                                      (r < t.rows ? r : t.rows - 1) * p.k_blocks * 4, b * 4);
+            }
+            if (wave == 0 && lane < 2 * kS) {
+                int l = chunk * kS + (lane % kS);
+                l = k_first + (l < blocks ? l : blocks - 1);
+                load_dword_to_lds(ws_src, dst + Shape::kScaleFloats * 4, (w_block * p.k_blocks + l) * 4, 0);
+            }
+        };
+
+        f32x4 acc[kF][kM];
 #pragma unroll
-                for (int m = 0; m < kTokens; ++m) {
-                    const f32x4 y = mfma_block(a[f], b[m]);
-                    const float s = sx[m] * sw;
+        for (int f = 0; f < kF; ++f)
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) acc[f][m][q] = __builtin_fmaf(s, y[q], acc[f][m][q]);
+            for (int m = 0; m < kM; ++m) acc[f][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+        load_scales(0);
+#pragma unroll
+        for (int b = 0; b < kStages - 1; ++b)
+            if (b < blocks) load_stage(b);
+        for (int b = 0; b < blocks; ++b) {
+            // This wavefront's part of the stage has arrived; past the
+            // barrier everybody's has, and the stage before is free.
+            if (kStages > 2 && b + kStages - 2 < blocks)
+                wait_loads<(kStages - 2) * Shape::kLoads>();
+            else
+                wait_loads<0>();
+            lds_barrier();
+            const int chunk = b / kS, in_chunk = b % kS;
+            if (in_chunk == 0) load_scales(chunk + 1);  // to where nobody reads any more
+            if (b + kStages - 1 < blocks) load_stage(b + kStages - 1);
+            const uint8_t* const stage = smem + b % kStages * Shape::kStageBytes;
+            const uint8_t* const w_at = stage + row_wave * Shape::kRows * 128;
+            const uint8_t* const x_at = stage + Shape::kWeightBytes + token_wave * 16 * kM * 128;
+            const float* const s_chunk = scales + (chunk & 1) * Shape::kChunkFloats;
+            const float* const s_at = s_chunk + in_chunk * Shape::kTokens + token_wave * 16 * kM + col;
+            const float sw = s_chunk[Shape::kScaleFloats + row_wave / (Shape::kRowWaves / 2) * kS + in_chunk];
+            i32x8 x[kM];
+            float s[kM];
+#pragma unroll
+            for (int m = 0; m < kM; ++m) {
+                x[m] = read_fragment(x_at + m * 16 * 128, read_lo, read_hi);
+                s[m] = s_at[m * 16] * sw;
+            }
+            f32x4 y[kM];
+            i32x8 w = read_fragment(w_at, read_lo, read_hi);
+#pragma unroll
+            for (int f = 0; f <= kF; ++f) {
+                // Rows f are multiplied while rows f + 1 are read and the
+                // products of rows f - 1 added. (The barriers to scheduling
+                // keep the steps apart: moved together, their operands no
+                // longer fit the registers.)
+                i32x8 next = w;
+                if (f + 1 < kF) next = read_fragment(w_at + (f + 1) * 16 * 128, read_lo, read_hi);
+#pragma unroll
+                for (int m = 0; m < kM; ++m) {
+                    const f32x4 last = y[m];
+                    if (f < kF) y[m] = mfma_block(w, x[m]);
+                    if (f > 0) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) acc[f - 1][m][q] = __builtin_fmaf(s[m], last[q], acc[f - 1][m][q]);
+                    }
                 }
+                w = next;
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
-        // Sums of the splits, halving their number.
+        if (parts > 1) {
+            // The sums go past the caches that XCDs do not share (sc1 on
+            // stores and loads), so that no cache has to be written back or
+            // invalidated for them: with release and acquire fences instead,
+            // one token's 8 x 4096 x 7168 product took 78 us, unshared 54.
+            constexpr int kSums = Shape::kSumFloats / 4;
+            const int at = (wave * (kF * kM * kWave) + lane) * 16;
+            const auto slot = [&](int q) {
+                return __builtin_amdgcn_make_buffer_rsrc((void*)(p.sums + (int64_t)(item - part + q) * kSums), 0,
+                                                         kSums * 16, kBufferWord3);
+            };
+            const auto mine = slot(part);
 #pragma unroll
-        for (int half = Shape::kSplit / 2; half > 0; half /= 2) {
-            f32x4* slice = reinterpret_cast<f32x4*>(lds) +
-                           (group * (Shape::kSplit / 2) + (split & (half - 1))) * (Shape::kSliceFloats / 4);
-            if (split >= half && split < 2 * half) {
+            for (int f = 0; f < kF; ++f)
 #pragma unroll
-                for (int f = 0; f < 4; ++f)
-#pragma unroll
-                    for (int m = 0; m < kTokens; ++m) slice[(f * kTokens + m) * kWave + lane] = acc[f][m];
+                for (int m = 0; m < kM; ++m)
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[f][m]), mine,
+                                                           at + (f * kM + m) * kWave * 16, 0, kSc1Policy);
+            wait_loads<0>();  // and stores
+            uint32_t* const last = reinterpret_cast<uint32_t*>(scales);
+            lds_barrier();
+            if (threadIdx.x == 0) {
+                const uint32_t before =
+                    __hip_atomic_fetch_add(p.tickets + tile, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                *last = before == (uint32_t)parts - 1;
+                if (before == (uint32_t)parts - 1)
+                    __hip_atomic_store(p.tickets + tile, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             }
-            __syncthreads();
-            if (split < half) {
+            lds_barrier();
+            const bool go_on = *last != 0;
+            lds_barrier();
+            if (!go_on) continue;
 #pragma unroll
-                for (int f = 0; f < 4; ++f)
+            for (int f = 0; f < kF; ++f)
 #pragma unroll
-                    for (int m = 0; m < kTokens; ++m) acc[f][m] += slice[(f * kTokens + m) * kWave + lane];
+                for (int m = 0; m < kM; ++m) acc[f][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int q = 0; q < parts; ++q) {
+                const auto from = slot(q);
+#pragma unroll
+                for (int f = 0; f < kF; ++f)
+#pragma unroll
+                    for (int m = 0; m < kM; ++m)
+                        acc[f][m] += __builtin_bit_cast(
+                            f32x4, __builtin_amdgcn_raw_buffer_load_b128(from, at + (f * kM + m) * kWave * 16, 0,
+                                                                         kSc1Policy));
             }
-            __syncthreads();
         }
+        const int first_token = token_wave * 16 * kM + col;
         if (!kSwiglu) {
-            if (split == 0) {
-                uint16_t* out = static_cast<uint16_t*>(p.out);
+            uint16_t* out = static_cast<uint16_t*>(p.out);
+            const int n0 = t.n * 256 + row_wave * Shape::kRows + quad * 4;
 #pragma unroll
-                for (int f = 0; f < 4; ++f) {
-                    const int n = n0 + f * 16 + quad * 4;
+            for (int m = 0; m < kM; ++m) {
+                const int r = first_token + m * 16;
+                if (r < t.rows) {
 #pragma unroll
-                    for (int m = 0; m < kTokens; ++m) {
-                        const int r = m * 16 + col;
-                        if (r < t.rows && n < p.N) {  // N is a multiple of 8
+                    for (int f = 0; f < kF; ++f) {
+                        const int n = n0 + f * 16;
+                        if (n < p.N) {  // N is a multiple of 8
                             uint2 o;
                             o.x = pack_bf16(acc[f][m][0], acc[f][m][1]);
                             o.y = pack_bf16(acc[f][m][2], acc[f][m][3]);
@@ -260,271 +474,27 @@ stream_kernel(ProductParams p) {
                     }
                 }
             }
-        } else {
-            // [token][256] sums: gate channels, then up channels. A row is
-            // 4 floats longer than that, so that the 16 tokens of a store
-            // fall into different banks.
-            constexpr int kRow = 256 + 4;
-            static_assert(!kSwiglu || Shape::kTileRows * kRow <= Shape::kLdsFloats, "epilogue rows");
-            if (split == 0) {
-#pragma unroll
-                for (int f = 0; f < 4; ++f)
-#pragma unroll
-                    for (int m = 0; m < kTokens; ++m)
-                        *reinterpret_cast<f32x4*>(lds + (m * 16 + col) * kRow + group * 64 + f * 16 + quad * 4) =
-                            acc[f][m];
-            }
-            __syncthreads();
-            const int I = p.N / 2;
-            const int r = threadIdx.x / 16, c = (threadIdx.x & 15) * 8;
-            for (int token = r; token < Shape::kTileRows; token += Shape::kWaves * 4) {
-                if (token < t.rows) {
-                    const float* g = lds + token * kRow + c;
-                    float v[8];
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) v[q] = g[q] * sigmoid(g[q]) * g[128 + q];
-                    uint8_t* dst = static_cast<uint8_t*>(p.out) + (int64_t)(t.row + token) * I + t.n * 128 + c;
-                    quantize8(v, true, c == 0, dst, p.out_sf + (int64_t)(t.row + token) * (I / 128) + t.n);
-                }
-            }
-            __syncthreads();
-        }
-    }
-}
-
-template <int kTokens, bool kSwiglu>
-hipError_t launch_stream(ProductParams p, int64_t max_rows, hipStream_t stream) {
-    using Shape = StreamShape<kTokens, kSwiglu>;
-    p.n_tiles = kSwiglu ? p.N / 256 : (p.N + 63) / 64;
-    // Row tiles at most: one of each expert that has a row may be partial.
-    const int64_t row_tiles = max_rows / Shape::kTileRows + (max_rows < p.num_experts ? max_rows : p.num_experts);
-    int64_t groups = (row_tiles * p.n_tiles + kXcds - 1) / kXcds * kXcds;
-    if (groups > 65536) groups = 65536;  // larger batches loop
-    if (groups < kXcds) groups = kXcds;
-    const size_t shared = Shape::kLdsFloats * sizeof(float);
-    void* args[] = {&p};
-    return hipLaunchKernel((const void*)&stream_kernel<kTokens, kSwiglu>, dim3((unsigned)groups),
-                           dim3(Shape::kWaves * kWave), args, shared, stream);
-}
-
-// ----------------------------------------------------- many rows per expert
-//
-// A workgroup of eight wavefronts computes 256 weight rows x 64 * kMt tokens.
-// Both operands go through LDS in stages of one 128-channel block, loaded
-// straight into it (no registers), two stages deep: while one is computed the
-// next is on its way. Wavefront (h, q) takes weight rows [128 h, 128 h + 128)
-// (for the SwiGLU product h = 0 are gate rows and h = 1 the up rows of the same
-// channels) and the q-th quarter of the tokens: the weights' scale is then one
-// number per wavefront and block. The sums stay in registers: fp32 updates
-// need them among the 256 that vector instructions reach, which is what
-// bounds a wavefront's tile to 128 x 64.
-//
-// A stage's row is 128 bytes, eight 16-byte chunks; chunk c of row r lies at
-// place c ^ (r % 8), so that the 16 rows a read instruction touches at one
-// chunk spread over the banks. Loads into LDS fill it in lane order, so the
-// permutation is applied to the addresses they read from.
-template <int kMt>
-struct TileShape {
-    static constexpr int kWaves = 8;
-    static constexpr int kTokens = 64 * kMt;
-    static constexpr int kWeightBytes = 256 * 128;
-    static constexpr int kStageBytes = kWeightBytes + kTokens * 128;
-    static constexpr int kScaleBlocks = 8;  // blocks whose x scales are staged at a time
-    static constexpr int kScaleFloats = kScaleBlocks * kTokens;
-    static constexpr int kLdsBytes = 2 * kStageBytes + 2 * (kScaleFloats + 2 * kScaleBlocks) * 4;
-};
-
-typedef __attribute__((address_space(3))) void lds_void;
-
-// Loads eight rows of a stage: 1 KB in lane order at dst. Lane offsets past
-// the descriptor's range read as zeros.
-__device__ __forceinline__ void load_rows(__amdgpu_buffer_rsrc_t src, uint8_t* dst, int lane_offset, int k) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (lds_void*)dst, 16, lane_offset, k, 0, 0);
-}
-
-__device__ __forceinline__ i32x8 read_fragment(const uint8_t* at, int lo, int hi) {
-    const u32x4 a = *reinterpret_cast<const u32x4*>(at + lo);
-    const u32x4 b = *reinterpret_cast<const u32x4*>(at + hi);
-    return i32x8{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
-}
-
-template <int kMt, bool kSwiglu>
-__global__ void __launch_bounds__(TileShape<kMt>::kWaves * kWave, 2) tile_kernel(ProductParams p) {
-    using Shape = TileShape<kMt>;
-    extern __shared__ __align__(16) uint8_t smem[];
-    float* const scales = reinterpret_cast<float*>(smem + 2 * Shape::kStageBytes);
-    const int lane = threadIdx.x & (kWave - 1);
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int half = wave & 1, quarter = wave >> 1;
-    const int col = lane & 15, quad = lane >> 4;
-    const int64_t total = (int64_t)count_row_tiles<Shape::kTokens>(p) * p.n_tiles;
-    // Reads: this lane's two chunks within the first 16 rows of a fragment.
-    const int read_lo = col * 128 + ((quad ^ (col & 7)) << 4);
-    const int read_hi = read_lo ^ 64;
-    // Loads: this lane's chunk within 8 rows.
-    const int load_row = lane >> 3;
-    const int load_k = ((lane & 7) ^ load_row) << 4;
-    for (int64_t i = blockIdx.x; i < (total + kXcds - 1) / kXcds * kXcds; i += gridDim.x) {
-        const int64_t item = xcd_item(i, total);
-        if (item >= total) continue;
-        const Tile t = find_tile<Shape::kTokens>(p, item);
-        // Weight rows of this wavefront's half; the other operand's loads are
-        // split over the wavefronts the same way: 32 weight rows and 8 kMt
-        // token rows each.
-        const int n_half = kSwiglu ? t.n * 128 + half * (p.N / 2) : t.n * 256 + half * 128;
-        int n_rows = p.N - n_half;
-        n_rows = __builtin_amdgcn_readfirstlane(n_rows < 0 ? 0 : (n_rows > 128 ? 128 : n_rows));
-        const int64_t w_row = n_rows > 0 ? (int64_t)t.expert * p.N + n_half : 0;
-        const auto w_src = __builtin_amdgcn_make_buffer_rsrc((void*)(p.w + w_row * p.K), 0, n_rows * p.K, kBufferWord3);
-        const auto x_src =
-            __builtin_amdgcn_make_buffer_rsrc((void*)(p.x + (int64_t)t.row * p.K), 0, t.rows * p.K, kBufferWord3);
-        const int w_first = quarter * 32, x_first = wave * 8 * kMt;
-        // Rows past the last one load that one again; their sums are dropped.
-        int w_offset[4], x_offset[kMt];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int r = w_first + j * 8 + load_row;
-            w_offset[j] = (r < n_rows ? r : (n_rows > 0 ? n_rows - 1 : 0)) * p.K + load_k;
-        }
-#pragma unroll
-        for (int j = 0; j < kMt; ++j) {
-            const int r = x_first + j * 8 + load_row;
-            x_offset[j] = (r < t.rows ? r : t.rows - 1) * p.K + load_k;
-        }
-        auto load_stage = [&](int kb) {
-            uint8_t* const stage = smem + (kb & 1) * Shape::kStageBytes;
-            // Chunks past K (a multiple of 16) are sent out of range.
-            const int k = kb * 128;
-            const int out = k + load_k < p.K ? 0 : INT32_MIN;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                load_rows(w_src, stage + (half * 128 + w_first + j * 8) * 128, w_offset[j] | out, k);
-#pragma unroll
-            for (int j = 0; j < kMt; ++j)
-                load_rows(x_src, stage + Shape::kWeightBytes + (x_first + j * 8) * 128, x_offset[j] | out, k);
-        };
-        // Scales, eight blocks at a time: a thread carries kMt blocks of one
-        // token's, the first 16 threads one block of a half's weights. (Past
-        // the last block the last one is loaded again and not used.)
-        constexpr int kS = Shape::kScaleBlocks;
-        const int s_token = threadIdx.x / kS * kMt + (threadIdx.x % kS) / (kS / kMt);
-        const int s_block = (threadIdx.x % (kS / kMt)) * kMt;
-        const int w_half = kSwiglu ? t.n * 128 + ((threadIdx.x / kS) & 1) * (p.N / 2) : t.n * 256 + ((threadIdx.x / kS) & 1) * 128;
-        int w_block = w_half >> 7;
-        w_block = w_block < p.n_blocks ? w_block : p.n_blocks - 1;
-        const float* const s_src =
-            p.x_sf + (int64_t)(t.row + (s_token < t.rows ? s_token : t.rows - 1)) * p.k_blocks;
-        const float* const ws_src = p.w_sf + ((int64_t)t.expert * p.n_blocks + w_block) * p.k_blocks;
-        float s_next[kMt], ws_next;
-        auto load_scales = [&](int chunk) {
-#pragma unroll
-            for (int j = 0; j < kMt; ++j) {
-                const int kb = chunk * kS + s_block + j;
-                s_next[j] = s_src[kb < p.k_blocks ? kb : p.k_blocks - 1];
-            }
-            const int kb = chunk * kS + (int)(threadIdx.x % kS);
-            ws_next = ws_src[kb < p.k_blocks ? kb : p.k_blocks - 1];
-        };
-        auto store_scales = [&](int chunk) {
-            float* const dst = scales + (chunk & 1) * (Shape::kScaleFloats + 2 * kS);
-#pragma unroll
-            for (int j = 0; j < kMt; ++j) dst[(s_block + j) * Shape::kTokens + s_token] = s_next[j];
-            if (threadIdx.x < 2 * kS) dst[Shape::kScaleFloats + threadIdx.x] = ws_next;
-        };
-
-        f32x4 acc[8][kMt];
-#pragma unroll
-        for (int f = 0; f < 8; ++f)
-#pragma unroll
-            for (int m = 0; m < kMt; ++m) acc[f][m] = f32x4{0.f, 0.f, 0.f, 0.f};
-        load_stage(0);
-        load_scales(0);
-        store_scales(0);
-        for (int kb = 0; kb < p.k_blocks; ++kb) {
-            // This wavefront's part of the stage has arrived; past the
-            // barrier everybody's has, and the other stage is free.
-            __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
-            __syncthreads();
-            // The next blocks' scales are loaded at the first block of eight
-            // and stored at the second, when nobody reads their place.
-            const int chunk = kb / kS, in_chunk = kb % kS;
-            if (in_chunk == 1) store_scales(chunk + 1);
-            if (in_chunk == 0) load_scales(chunk + 1);
-            if (kb + 1 < p.k_blocks) load_stage(kb + 1);
-            const uint8_t* const stage = smem + (kb & 1) * Shape::kStageBytes;
-            const uint8_t* const w_at = stage + half * 128 * 128;
-            const uint8_t* const x_at = stage + Shape::kWeightBytes + quarter * 16 * kMt * 128;
-            const float* const s_chunk = scales + (chunk & 1) * (Shape::kScaleFloats + 2 * kS);
-            const float* const s_at = s_chunk + in_chunk * Shape::kTokens + quarter * 16 * kMt + col;
-            const float sw = s_chunk[Shape::kScaleFloats + half * kS + in_chunk];
-            i32x8 b[kMt];
-            float s[kMt];
-#pragma unroll
-            for (int m = 0; m < kMt; ++m) {
-                b[m] = read_fragment(x_at + m * 16 * 128, read_lo, read_hi);
-                s[m] = s_at[m * 16] * sw;
-            }
-            f32x4 y[kMt];
-            i32x8 a = read_fragment(w_at, read_lo, read_hi);
-#pragma unroll
-            for (int f = 0; f < 9; ++f) {
-                // Rows f are multiplied while rows f + 1 are read and the
-                // products of rows f - 1 added. (The barriers to scheduling
-                // keep the steps apart: moved together, their operands no
-                // longer fit the registers.)
-                i32x8 next = a;
-                if (f < 7) next = read_fragment(w_at + (f + 1) * 16 * 128, read_lo, read_hi);
-#pragma unroll
-                for (int m = 0; m < kMt; ++m) {
-                    const f32x4 last = y[m];
-                    if (f < 8) y[m] = mfma_block(a, b[m]);
-                    if (f > 0) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) acc[f - 1][m][q] = __builtin_fmaf(s[m], last[q], acc[f - 1][m][q]);
-                    }
-                }
-                a = next;
-                __builtin_amdgcn_sched_barrier(0);
-            }
-        }
-        if (!kSwiglu) {
-            uint16_t* out = static_cast<uint16_t*>(p.out);
-#pragma unroll
-            for (int m = 0; m < kMt; ++m) {
-                const int r = (quarter * kMt + m) * 16 + col;
-                if (r < t.rows) {
-#pragma unroll
-                    for (int f = 0; f < 8; ++f) {
-                        const int n = f * 16 + quad * 4;
-                        if (n < n_rows) {  // N is a multiple of 8
-                            uint2 o;
-                            o.x = pack_bf16(acc[f][m][0], acc[f][m][1]);
-                            o.y = pack_bf16(acc[f][m][2], acc[f][m][3]);
-                            *reinterpret_cast<uint2*>(out + (int64_t)(t.row + r) * p.N + n_half + n) = o;
-                        }
-                    }
-                }
-            }
-        } else {
+            lds_barrier();  // the ring is free for the next tile
+        } else if (Shape::kWholeBlock) {
             // The up wavefronts hand their sums over through LDS, in the
             // order of their registers.
-            __syncthreads();
-            f32x4* const swap = reinterpret_cast<f32x4*>(smem) + quarter * 8 * kMt * kWave;
-            if (half == 1) {
+            const int I = p.N / 2;
+            lds_barrier();
+            f32x4* const swap = reinterpret_cast<f32x4*>(smem) + token_wave * kF * kM * kWave;
+            if (row_wave == 1) {
 #pragma unroll
-                for (int f = 0; f < 8; ++f)
+                for (int f = 0; f < kF; ++f)
 #pragma unroll
-                    for (int m = 0; m < kMt; ++m) swap[(f * kMt + m) * kWave + lane] = acc[f][m];
+                    for (int m = 0; m < kM; ++m) swap[(f * kM + m) * kWave + lane] = acc[f][m];
             }
-            __syncthreads();
-            if (half == 0) {
-                const int I = p.N / 2;
+            lds_barrier();
+            if (row_wave == 0) {
 #pragma unroll
-                for (int m = 0; m < kMt; ++m) {
+                for (int m = 0; m < kM; ++m) {
                     uint32_t top = __float_as_uint(kAmaxFloor);
 #pragma unroll
-                    for (int f = 0; f < 8; ++f) {
-                        const f32x4 u = swap[(f * kMt + m) * kWave + lane];
+                    for (int f = 0; f < kF; ++f) {
+                        const f32x4 u = swap[(f * kM + m) * kWave + lane];
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             const float g = acc[f][m][q];
@@ -541,11 +511,11 @@ __global__ void __launch_bounds__(TileShape<kMt>::kWaves * kWave, 2) tile_kernel
                     top = top > other ? top : other;
                     const float amax = __uint_as_float(top);
                     const float scale = kFp8Max / amax;
-                    const int r = (quarter * kMt + m) * 16 + col;
+                    const int r = first_token + m * 16;
                     if (r < t.rows) {
                         uint8_t* dst = static_cast<uint8_t*>(p.out) + (int64_t)(t.row + r) * I + t.n * 128 + quad * 4;
 #pragma unroll
-                        for (int f = 0; f < 8; ++f)
+                        for (int f = 0; f < kF; ++f)
                             *reinterpret_cast<uint32_t*>(dst + f * 16) =
                                 pack_fp8(acc[f][m][0] * scale, acc[f][m][1] * scale, acc[f][m][2] * scale,
                                          acc[f][m][3] * scale);
@@ -553,40 +523,117 @@ __global__ void __launch_bounds__(TileShape<kMt>::kWaves * kWave, 2) tile_kernel
                     }
                 }
             }
+            lds_barrier();
+        } else {
+            // [token][256] sums: gate channels, then up channels. A row is
+            // 4 floats longer than that, so that the 16 tokens of a store
+            // fall into different banks.
+            const int I = p.N / 2;
+            float* const sums = reinterpret_cast<float*>(smem);
+            lds_barrier();
+#pragma unroll
+            for (int f = 0; f < kF; ++f)
+#pragma unroll
+                for (int m = 0; m < kM; ++m)
+                    *reinterpret_cast<f32x4*>(sums + (first_token + m * 16) * Shape::kSumRow +
+                                              row_wave * Shape::kRows + f * 16 + quad * 4) = acc[f][m];
+            lds_barrier();
+            const int c = (threadIdx.x & 15) * 8;
+            for (int token = threadIdx.x / 16; token < t.rows; token += Shape::kWaves * 4) {
+                const float* g = sums + token * Shape::kSumRow + c;
+                float v[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) v[q] = g[q] * sigmoid(g[q]) * g[128 + q];
+                uint8_t* dst = static_cast<uint8_t*>(p.out) + (int64_t)(t.row + token) * I + t.n * 128 + c;
+                quantize8(v, true, c == 0, dst, p.out_sf + (int64_t)(t.row + token) * (I / 128) + t.n);
+            }
+            lds_barrier();
         }
-        __syncthreads();
     }
 }
 
-template <int kMt, bool kSwiglu>
-hipError_t launch_tile(ProductParams p, int64_t max_rows, hipStream_t stream) {
-    using Shape = TileShape<kMt>;
-    p.n_tiles = kSwiglu ? p.N / 256 : (p.N + 255) / 256;
-    const int64_t row_tiles =
-        max_rows / Shape::kTokens + (max_rows < p.num_experts ? max_rows : p.num_experts);
-    int64_t groups = (row_tiles * p.n_tiles + kXcds - 1) / kXcds * kXcds;
-    if (groups > 65536) groups = 65536;
+// Row tiles at most: one of each expert that has a row may be partial.
+int64_t most_row_tiles(int64_t max_rows, int32_t num_experts, int tile_rows) {
+    return max_rows / tile_rows + (max_rows < num_experts ? max_rows : num_experts);
+}
+
+// How a product is cut.
+struct ProductPlan {
+    int64_t tiles;  // at most
+    int parts;      // workgroups per tile
+    size_t bytes;   // of workspace: tickets, then sums (0: nothing shared)
+};
+
+constexpr int kMaxParts = 16;
+
+template <class Shape>
+ProductPlan plan_product(int64_t max_rows, int32_t num_experts, int32_t N, int32_t k_blocks) {
+    ProductPlan s;
+    s.tiles = most_row_tiles(max_rows, num_experts, Shape::kTokens) * ((N + 255) / 256);
+    // As many parts as fill the CUs, each left with four blocks of K or more.
+    const int64_t want = kCus / (s.tiles < 1 ? 1 : s.tiles);
+    const int64_t most = k_blocks / 4;
+    const int64_t parts = want < most ? want : most;
+    s.parts = (int)(parts < 1 ? 1 : (parts > kMaxParts ? kMaxParts : parts));
+    s.bytes = s.parts == 1 ? 0 : kTicketBytes + (size_t)(s.tiles * s.parts) * Shape::kSumFloats * sizeof(float);
+    return s;
+}
+
+template <class Shape, bool kSwiglu>
+hipError_t launch_product(ProductParams p, int64_t max_rows, void* workspace, hipStream_t stream) {
+    p.n_tiles = (p.N + 255) / 256;
+    ProductPlan plan = plan_product<Shape>(max_rows, p.num_experts, p.N, p.k_blocks);
+    if (workspace == nullptr) plan.parts = 1;
+    p.parts = plan.parts;
+    p.slots = plan.parts == 1 ? 0 : (int32_t)(plan.tiles * plan.parts);
+    p.tickets = static_cast<uint32_t*>(workspace);
+    p.sums = workspace == nullptr ? nullptr
+                                  : reinterpret_cast<f32x4*>(static_cast<uint8_t*>(workspace) + kTicketBytes);
+    int64_t groups = (plan.tiles * plan.parts + kXcds - 1) / kXcds * kXcds;
+    if (groups > 65536) groups = 65536;  // larger batches loop
     if (groups < kXcds) groups = kXcds;
     void* args[] = {&p};
-    return hipLaunchKernel((const void*)&tile_kernel<kMt, kSwiglu>, dim3((unsigned)groups),
+    return hipLaunchKernel((const void*)&product_kernel<Shape, kSwiglu>, dim3((unsigned)groups),
                            dim3(Shape::kWaves * kWave), args, Shape::kLdsBytes, stream);
 }
 
-template <bool kSwiglu>
-hipError_t launch(const ProductParams& p, int64_t max_rows, hipStream_t stream) {
-    const int64_t mean = max_rows / p.num_experts;
-    if (mean <= 16) return launch_stream<1, kSwiglu>(p, max_rows, stream);
-    if (mean <= 32) return launch_stream<2, kSwiglu>(p, max_rows, stream);
-    if (mean <= 64) return launch_tile<1, kSwiglu>(p, max_rows, stream);
-    if (mean <= 192) return launch_tile<2, kSwiglu>(p, max_rows, stream);
-    return launch_tile<4, kSwiglu>(p, max_rows, stream);
+using Shape16 = TileShape<16, 8, 4>;
+using Shape32 = TileShape<32, 8, 4>;
+using Shape64 = TileShape<64, 4, 3>;
+using Shape128 = TileShape<128, 2, 3>;
+using Shape256 = TileShape<256, 2, 2>;
+
+// The shape by the mean of the rows that an expert gets at most: one tile for
+// most experts, as each tile reads all the weights again.
+template <class F>
+auto with_shape(int64_t max_rows, int32_t num_experts, F f) {
+    const int64_t mean = max_rows / num_experts;
+    if (mean <= 10) return f(Shape16{});
+    if (mean <= 20) return f(Shape32{});
+    if (mean <= 48) return f(Shape64{});
+    if (mean <= 192) return f(Shape128{});
+    return f(Shape256{});
+}
+
+int64_t most_rows(const dispatch_expert_problem_t& p) {
+    return p.max_routed_rows < p.expert_rows ? p.max_routed_rows : p.expert_rows;
 }
 
 }  // namespace
 
+size_t expert_workspace_bytes(const dispatch_expert_problem_t& prob) {
+    const int64_t max_rows = most_rows(prob);
+    return with_shape(max_rows, prob.num_experts, [&](auto shape) {
+        return plan_product<decltype(shape)>(max_rows, prob.num_experts, (int32_t)prob.out_features,
+                                             (int32_t)((prob.in_features + 127) / 128))
+            .bytes;
+    });
+}
+
 hipError_t launch_expert_product(const dispatch_expert_problem_t& prob, const int32_t* expert_psum,
                                  const int32_t* expert_count, const void* x, const float* x_sf, const void* w,
-                                 const float* w_sf, void* out, float* out_sf, hipStream_t stream) {
+                                 const float* w_sf, void* out, float* out_sf, void* workspace,
+                                 hipStream_t stream) {
     if (prob.expert_rows == 0) return hipSuccess;
     ProductParams p{};
     p.psum = expert_psum;
@@ -603,8 +650,12 @@ hipError_t launch_expert_product(const dispatch_expert_problem_t& prob, const in
     p.N = (int32_t)prob.out_features;
     p.k_blocks = (p.K + 127) / 128;
     p.n_blocks = (p.N + 127) / 128;
-    const int64_t max_rows = prob.max_routed_rows < prob.expert_rows ? prob.max_routed_rows : prob.expert_rows;
-    return out_sf != nullptr ? launch<true>(p, max_rows, stream) : launch<false>(p, max_rows, stream);
+    const int64_t max_rows = most_rows(prob);
+    return with_shape(max_rows, prob.num_experts, [&](auto shape) {
+        using Shape = decltype(shape);
+        return out_sf != nullptr ? launch_product<Shape, true>(p, max_rows, workspace, stream)
+                                 : launch_product<Shape, false>(p, max_rows, workspace, stream);
+    });
 }
 
 }  // namespace moe_dispatch

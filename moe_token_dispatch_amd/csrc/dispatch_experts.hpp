@@ -49,8 +49,10 @@ hipError_t launch_quantize(QuantizeSource source, const dispatch_quantize_proble
                            const void* grad, const int32_t* num_valid_rows, void* q, float* sf, hipStream_t stream);
 
 // out_sf: not NULL for the product with the SwiGLU and quantisation behind it.
+// workspace: NULL or of expert_workspace_bytes.
+size_t expert_workspace_bytes(const dispatch_expert_problem_t& p);
 hipError_t launch_expert_product(const dispatch_expert_problem_t& p, const int32_t* expert_psum,
                                  const int32_t* expert_count, const void* x, const float* x_sf, const void* w,
-                                 const float* w_sf, void* out, float* out_sf, hipStream_t stream);
+                                 const float* w_sf, void* out, float* out_sf, void* workspace, hipStream_t stream);
 
 }  // namespace moe_dispatch

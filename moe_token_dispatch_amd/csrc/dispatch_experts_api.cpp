@@ -48,9 +48,7 @@ int check_quantize(const dispatch_quantize_problem_t* p, bool swiglu, int64_t sf
     return DISPATCH_OK;
 }
 
-int expert_product(const dispatch_expert_problem_t* problem, const int32_t* expert_psum, const int32_t* expert_count,
-                   const void* x, const float* x_sf, const void* w, const float* w_sf, void* out, float* out_sf,
-                   bool swiglu, hipStream_t stream) {
+int check_experts(const dispatch_expert_problem_t* problem, bool swiglu) {
     if (problem == nullptr) return DISPATCH_ERR_NULL;
     const dispatch_expert_problem_t& p = *problem;
     if (p.num_experts < 1 || p.num_experts > DISPATCH_MAX_EXPERTS || p.reserved != 0) return DISPATCH_ERR_ARG;
@@ -62,6 +60,15 @@ int expert_product(const dispatch_expert_problem_t* problem, const int32_t* expe
         return DISPATCH_ERR_ALIGN;
     // Tiles (at least 16 rows x 64 channels each) are counted in 32 bits.
     if ((p.expert_rows / 16 + p.num_experts) * ((p.out_features + 63) / 64) > INT32_MAX) return DISPATCH_ERR_ARG;
+    return DISPATCH_OK;
+}
+
+int expert_product(const dispatch_expert_problem_t* problem, const int32_t* expert_psum, const int32_t* expert_count,
+                   const void* x, const float* x_sf, const void* w, const float* w_sf, void* out, float* out_sf,
+                   bool swiglu, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    const int rc = check_experts(problem, swiglu);
+    if (rc != DISPATCH_OK) return rc;
+    const dispatch_expert_problem_t& p = *problem;
     if (!expert_psum || !expert_count || !w || !w_sf) return DISPATCH_ERR_NULL;
     if (p.expert_rows > 0 && (!x || !x_sf || !out || (swiglu && !out_sf))) return DISPATCH_ERR_NULL;
     const void* rows[] = {x, w, out};
@@ -70,8 +77,11 @@ int expert_product(const dispatch_expert_problem_t* problem, const int32_t* expe
     const void* words[] = {expert_psum, expert_count, x_sf, w_sf, out_sf};
     for (const void* q : words)
         if (q && !aligned_to(q, 4)) return DISPATCH_ERR_ALIGN;
+    if (workspace != nullptr &&
+        (!aligned_to(workspace, 256) || workspace_bytes < moe_dispatch::expert_workspace_bytes(p)))
+        return DISPATCH_ERR_WORKSPACE;
     return status_of(moe_dispatch::launch_expert_product(p, expert_psum, expert_count, x, x_sf, w, w_sf, out,
-                                                         swiglu ? out_sf : nullptr, stream));
+                                                         swiglu ? out_sf : nullptr, workspace, stream));
 }
 
 }  // namespace
@@ -153,16 +163,28 @@ int dispatch_swiglu_backward_quantize(const dispatch_quantize_problem_t* problem
                                                    num_valid_rows, q, sf, stream));
 }
 
+int dispatch_expert_workspace_size(const dispatch_expert_problem_t* problem, size_t* bytes) {
+    const int rc = check_experts(problem, false);
+    if (rc != DISPATCH_OK) return rc;
+    if (bytes == nullptr) return DISPATCH_ERR_NULL;
+    *bytes = moe_dispatch::expert_workspace_bytes(*problem);
+    return DISPATCH_OK;
+}
+
 int dispatch_expert_product(const dispatch_expert_problem_t* problem, const int32_t* expert_psum,
                             const int32_t* expert_count, const void* x, const float* x_sf, const void* w,
-                            const float* w_sf, void* out, hipStream_t stream) {
-    return expert_product(problem, expert_psum, expert_count, x, x_sf, w, w_sf, out, nullptr, false, stream);
+                            const float* w_sf, void* out, void* workspace, size_t workspace_bytes,
+                            hipStream_t stream) {
+    return expert_product(problem, expert_psum, expert_count, x, x_sf, w, w_sf, out, nullptr, false, workspace,
+                          workspace_bytes, stream);
 }
 
 int dispatch_expert_product_swiglu(const dispatch_expert_problem_t* problem, const int32_t* expert_psum,
                                    const int32_t* expert_count, const void* x, const float* x_sf, const void* w,
-                                   const float* w_sf, void* out_q, float* out_sf, hipStream_t stream) {
-    return expert_product(problem, expert_psum, expert_count, x, x_sf, w, w_sf, out_q, out_sf, true, stream);
+                                   const float* w_sf, void* out_q, float* out_sf, void* workspace,
+                                   size_t workspace_bytes, hipStream_t stream) {
+    return expert_product(problem, expert_psum, expert_count, x, x_sf, w, w_sf, out_q, out_sf, true, workspace,
+                          workspace_bytes, stream);
 }
 
 }  // extern "C"

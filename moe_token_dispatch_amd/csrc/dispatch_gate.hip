@@ -290,8 +290,11 @@ gate_sum_kernel(const float* partial, int groups, int E, int K, float loss_coef,
     }
     for (int step = kSumExperts / 2; step > 0; step /= 2) mine += __shfl_xor(mine, step);
     if (threadIdx.x != 0) return;
+    // The part goes past the caches that XCDs do not share, and has arrived
+    // before the ticket is taken: no cache has to be written back for it.
     __hip_atomic_store(loss_part + blockIdx.x, mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    const uint32_t before = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    const uint32_t before = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     if (before != gridDim.x - 1) return;
     double total = 0.0;
     for (unsigned i = 0; i < gridDim.x; ++i)

@@ -129,20 +129,33 @@ BAD_EXPERTS = [
 @pytest.mark.parametrize("bad,code", BAD_EXPERTS, ids=str)
 def test_bad_expert_problems(bad, code):
     lib, p = M.load_library(), _experts(**bad)
-    assert lib.dispatch_expert_product(B(p), *[4096] * 7, None) == code
-    assert lib.dispatch_expert_product_swiglu(B(p), *[4096] * 8, None) == code
+    assert lib.dispatch_expert_product(B(p), *[4096] * 7, None, 0, None) == code
+    assert lib.dispatch_expert_product_swiglu(B(p), *[4096] * 8, None, 0, None) == code
 
 
 def test_expert_arguments():
     lib, p = M.load_library(), _experts()
-    assert lib.dispatch_expert_product(None, *[4096] * 7, None) == M.ERR_NULL
+    assert lib.dispatch_expert_product(None, *[4096] * 7, None, 0, None) == M.ERR_NULL
     for swiglu, n in ((False, 7), (True, 8)):
         call = lib.dispatch_expert_product_swiglu if swiglu else lib.dispatch_expert_product
         for i in range(n):
             args = [4096] * n
             args[i] = None
-            assert call(B(p), *args, None) == M.ERR_NULL, i
+            assert call(B(p), *args, None, 0, None) == M.ERR_NULL, i
             args[i] = 4104 if i in (2, 4, 6) else 4098
-            assert call(B(p), *args, None) == M.ERR_ALIGN, i
+            assert call(B(p), *args, None, 0, None) == M.ERR_ALIGN, i
     # Halves of the SwiGLU product are whole blocks.
-    assert lib.dispatch_expert_product_swiglu(B(_experts(out_features=384)), *[4096] * 8, None) == M.ERR_ALIGN
+    assert lib.dispatch_expert_product_swiglu(B(_experts(out_features=384)), *[4096] * 8, None, 0, None) == M.ERR_ALIGN
+
+
+def test_expert_workspace():
+    lib, n = M.load_library(), ctypes.c_size_t(0)
+    assert lib.dispatch_expert_workspace_size(None, B(n)) == M.ERR_NULL
+    assert lib.dispatch_expert_workspace_size(B(_experts()), None) == M.ERR_NULL
+    few, many = _experts(in_features=8192, expert_rows=16, max_routed_rows=8), _experts(expert_rows=4000, max_routed_rows=4000)
+    need = M.dispatch_expert_workspace_size(few)
+    assert need > 0 and M.dispatch_expert_workspace_size(many) == 0
+    for swiglu, ptrs in ((False, 7), (True, 8)):
+        call = lib.dispatch_expert_product_swiglu if swiglu else lib.dispatch_expert_product
+        assert call(B(few), *[4096] * ptrs, 4096 + 128, need, None) == M.ERR_WORKSPACE
+        assert call(B(few), *[4096] * ptrs, 4096, need - 1, None) == M.ERR_WORKSPACE

@@ -145,6 +145,36 @@ def test_any_row_bound_gives_the_same_rows(max_rows):
     _check_swiglu(s, *_run_swiglu(s, max_rows))
 
 
+@pytest.mark.parametrize("counts", [[1], [3, 0, 20], [16, 0, 17, 1, 1, 40]], ids=str)
+@pytest.mark.parametrize("k", [2048, 5008])
+@pytest.mark.parametrize("announced", [None, 1, 60])
+def test_shared_tiles(counts, k, announced):
+    """Few rows with a workspace: workgroups share a tile's K. Twice on one
+    workspace, and with fewer rows announced than there are (then there may be
+    no room to share)."""
+    s = _problem(counts, k, 512, 1, k + len(counts))
+    e, n, _ = s["w"].shape
+    p = M.make_expert_problem(e, k, n, s["rows"], sum(counts) if announced is None else announced)
+    ws = M.alloc_expert_workspace(p, DEV)
+    assert ws is not None or announced == 60
+    ins = _dev(s, "psum_t", "count_t", "x", "x_sf", "w", "w_sf")
+    first = None
+    for _ in range(3):
+        out = torch.full((s["rows"], 2 * n), CANARY, dtype=torch.uint8, device=DEV).view(torch.bfloat16)
+        M.dispatch_expert_product(p, *ins, out, ws)
+        q = torch.full((s["rows"], n // 2), CANARY, dtype=torch.uint8, device=DEV)
+        sf = torch.full((s["rows"], n // 256), -7.0, device=DEV)
+        M.dispatch_expert_product_swiglu(p, *ins, q, sf, ws)
+        torch.cuda.synchronize()
+        got = [out.cpu(), q.cpu(), sf.cpu()]
+        if first is None:
+            _check_product(s, got[0])
+            _check_swiglu(s, *got[1:])
+            first = got
+        # The parts are added in order, whichever workgroup comes last.
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(first, got))
+
+
 def test_rows_outside_the_buffer_are_skipped():
     s = _problem([20, 30], 128, 128, 1, 7, tail=0)
     whole = _run_product(s)
