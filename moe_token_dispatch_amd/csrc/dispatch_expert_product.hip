@@ -17,6 +17,8 @@
 // long as both operands agree (the sum runs over all of them): lane group
 // g = lane / 16 takes the 16-byte chunks g and g + 4, so that one load
 // instruction covers 64 consecutive bytes of 16 rows.
+#include <type_traits>
+
 #include "dispatch_common.hpp"
 #include "dispatch_device.hpp"
 #include "dispatch_experts.hpp"
@@ -297,31 +299,22 @@ __global__ void __launch_bounds__(Shape::kWaves * kWave, 2) product_kernel(Produ
         const int64_t w_row = n_rows > 0 ? (int64_t)t.expert * p.N + half_row(load_half) : 0;
         const i32x4 w_src = descriptor(p.w + w_row * p.K, n_rows * p.K);
         const i32x4 x_src = descriptor(p.x + (int64_t)t.row * p.K, t.rows * p.K);
-        // Rows past the last one load that one again; their sums are dropped.
-        int w_offset[4], x_offset[Shape::kXLoads];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int r = w_first + j * 8 + load_row;
-            w_offset[j] = (r < n_rows ? r : (n_rows > 0 ? n_rows - 1 : 0)) * p.K + load_k;
-        }
-#pragma unroll
-        for (int j = 0; j < Shape::kXLoads; ++j) {
-            const int r = x_first + j * 8 + load_row;
-            x_offset[j] = (r < t.rows ? r : t.rows - 1) * p.K + x_load_k;
-        }
-        auto load_stage = [&](int b) {
+        // Rows past the last one are out of the descriptors' range.
+        const int w_lane = (w_first + load_row) * p.K + load_k;
+        const int x_lane = (x_first + load_row) * p.K + x_load_k;
+        // Load j of stage b; past the last block, and for chunks past K (a
+        // multiple of 16), out of range.
+        auto load_stage = [&](int b, int j) {
             const int stage = lds_address(smem) + b % kStages * Shape::kStageBytes;
-            // Chunks past K (a multiple of 16) are sent out of range.
             const int k = (k_first + b) * 128;
-            const int out = k + load_k < p.K ? 0 : INT32_MIN;
-            const int x_out = k + x_load_k < p.K ? 0 : INT32_MIN;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                load_to_lds(w_src, stage + (load_half * 128 + w_first + j * 8) * 128, w_offset[j] | out, k);
-            if (Shape::kXRows == 8 || load_row < Shape::kXRows) {
-#pragma unroll
-                for (int j = 0; j < Shape::kXLoads; ++j)
-                    load_to_lds(x_src, stage + Shape::kWeightBytes + (x_first + j * 8) * 128, x_offset[j] | x_out, k);
+            const int past = b < blocks ? 0 : INT32_MIN;
+            if (j < 4) {
+                const int out = k + load_k < p.K ? past : INT32_MIN;
+                load_to_lds(w_src, stage + (load_half * 128 + w_first + j * 8) * 128, (w_lane + j * 8 * p.K) | out, k);
+            } else if (Shape::kXRows == 8 || load_row < Shape::kXRows) {
+                const int out = k + x_load_k < p.K ? past : INT32_MIN;
+                load_to_lds(x_src, stage + Shape::kWeightBytes + (x_first + (j - 4) * 8) * 128,
+                            (x_lane + (j - 4) * 8 * p.K) | out, k);
             }
         };
         // Scales, eight blocks at a time, one wavefront for each: a lane per
@@ -359,54 +352,74 @@ __global__ void __launch_bounds__(Shape::kWaves * kWave, 2) product_kernel(Produ
         load_scales(0);
 #pragma unroll
         for (int b = 0; b < kStages - 1; ++b)
-            if (b < blocks) load_stage(b);
+#pragma unroll
+            for (int j = 0; j < Shape::kLoads; ++j) load_stage(b, j);
+        // The blocks, for a tile whose rows fill kLive of each wavefront's
+        // fragments of tokens.
+        auto run = [&](auto live_fragments) {
+        constexpr int kLive = decltype(live_fragments)::value;
         for (int b = 0; b < blocks; ++b) {
             // This wavefront's part of the stage has arrived; past the
             // barrier everybody's has, and the stage before is free.
-            if (kStages > 2 && b + kStages - 2 < blocks)
-                wait_loads<(kStages - 2) * Shape::kLoads>();
-            else
-                wait_loads<0>();
+            wait_loads<(kStages - 2) * Shape::kLoads>();
             lds_barrier();
             const int chunk = b / kS, in_chunk = b % kS;
             if (in_chunk == 0) load_scales(chunk + 1);  // to where nobody reads any more
-            if (b + kStages - 1 < blocks) load_stage(b + kStages - 1);
+            // (All at once: one load a step below arrived later and took
+            // 602 us where this takes 560, 32768 x 7168 x 2048.)
+#pragma unroll
+            for (int j = 0; j < Shape::kLoads; ++j) load_stage(b + kStages - 1, j);
             const uint8_t* const stage = smem + b % kStages * Shape::kStageBytes;
             const uint8_t* const w_at = stage + row_wave * Shape::kRows * 128;
-            const uint8_t* const x_at = stage + Shape::kWeightBytes + token_wave * 16 * kM * 128;
+            const uint8_t* const x_at = stage + Shape::kWeightBytes + token_wave * 16 * 128;
             const float* const s_chunk = scales + (chunk & 1) * Shape::kChunkFloats;
-            const float* const s_at = s_chunk + in_chunk * Shape::kTokens + token_wave * 16 * kM + col;
+            const float* const s_at = s_chunk + in_chunk * Shape::kTokens + token_wave * 16 + col;
             const float sw = s_chunk[Shape::kScaleFloats + row_wave / (Shape::kRowWaves / 2) * kS + in_chunk];
-            i32x8 x[kM];
-            float s[kM];
+            i32x8 x[kLive];
+            float s[kLive];
 #pragma unroll
-            for (int m = 0; m < kM; ++m) {
-                x[m] = read_fragment(x_at + m * 16 * 128, read_lo, read_hi);
-                s[m] = s_at[m * 16] * sw;
+            for (int m = 0; m < kLive; ++m) {
+                x[m] = read_fragment(x_at + m * Shape::kTokenWaves * 16 * 128, read_lo, read_hi);
+                s[m] = s_at[m * Shape::kTokenWaves * 16] * sw;
             }
-            f32x4 y[kM];
+            f32x4 y[kLive];
             i32x8 w = read_fragment(w_at, read_lo, read_hi);
 #pragma unroll
             for (int f = 0; f <= kF; ++f) {
                 // Rows f are multiplied while rows f + 1 are read and the
-                // products of rows f - 1 added. (The barriers to scheduling
-                // keep the steps apart: moved together, their operands no
-                // longer fit the registers.)
+                // products of rows f - 1 added, four additions behind each
+                // matrix instruction, whose 32 cycles they fit into. (Left to
+                // the compiler, additions and matrix instructions came in
+                // separate runs, 5 % slower; and the steps moved together
+                // need more registers than there are.)
                 i32x8 next = w;
                 if (f + 1 < kF) next = read_fragment(w_at + (f + 1) * 16 * 128, read_lo, read_hi);
 #pragma unroll
-                for (int m = 0; m < kM; ++m) {
+                for (int m = 0; m < kLive; ++m) {
                     const f32x4 last = y[m];
                     if (f < kF) y[m] = mfma_block(w, x[m]);
                     if (f > 0) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q) acc[f - 1][m][q] = __builtin_fmaf(s[m], last[q], acc[f - 1][m][q]);
                     }
+                    __builtin_amdgcn_sched_barrier(0);
                 }
                 w = next;
-                __builtin_amdgcn_sched_barrier(0);
             }
         }
+        };
+        // Fragments of tokens go to the token wavefronts in turn, so that a
+        // tile's last rows spread over all of them.
+        const int live = (t.rows + 16 * Shape::kTokenWaves - 1) / (16 * Shape::kTokenWaves);
+        if (kM >= 4 && live == 3)
+            run(std::integral_constant<int, (kM >= 4 ? 3 : kM)>());
+        else if (kM >= 4 && live == 2)
+            run(std::integral_constant<int, (kM >= 4 ? 2 : kM)>());
+        else if (kM >= 2 && live == 1)
+            run(std::integral_constant<int, (kM >= 2 ? 1 : kM)>());
+        else
+            run(std::integral_constant<int, kM>());
+        wait_loads<0>();  // (those past the last block write zeros to the ring)
         if (parts > 1) {
             // The sums go past the caches that XCDs do not share (sc1 on
             // stores and loads), so that no cache has to be written back or
@@ -454,13 +467,13 @@ __global__ void __launch_bounds__(Shape::kWaves * kWave, 2) product_kernel(Produ
                                                                          kSc1Policy));
             }
         }
-        const int first_token = token_wave * 16 * kM + col;
+        const int first_token = token_wave * 16 + col;
         if (!kSwiglu) {
             uint16_t* out = static_cast<uint16_t*>(p.out);
             const int n0 = t.n * 256 + row_wave * Shape::kRows + quad * 4;
 #pragma unroll
             for (int m = 0; m < kM; ++m) {
-                const int r = first_token + m * 16;
+                const int r = first_token + m * Shape::kTokenWaves * 16;
                 if (r < t.rows) {
 #pragma unroll
                     for (int f = 0; f < kF; ++f) {
@@ -511,7 +524,7 @@ __global__ void __launch_bounds__(Shape::kWaves * kWave, 2) product_kernel(Produ
                     top = top > other ? top : other;
                     const float amax = __uint_as_float(top);
                     const float scale = kFp8Max / amax;
-                    const int r = first_token + m * 16;
+                    const int r = first_token + m * Shape::kTokenWaves * 16;
                     if (r < t.rows) {
                         uint8_t* dst = static_cast<uint8_t*>(p.out) + (int64_t)(t.row + r) * I + t.n * 128 + quad * 4;
 #pragma unroll
@@ -535,7 +548,7 @@ __global__ void __launch_bounds__(Shape::kWaves * kWave, 2) product_kernel(Produ
             for (int f = 0; f < kF; ++f)
 #pragma unroll
                 for (int m = 0; m < kM; ++m)
-                    *reinterpret_cast<f32x4*>(sums + (first_token + m * 16) * Shape::kSumRow +
+                    *reinterpret_cast<f32x4*>(sums + (first_token + m * Shape::kTokenWaves * 16) * Shape::kSumRow +
                                               row_wave * Shape::kRows + f * 16 + quad * 4) = acc[f][m];
             lds_barrier();
             const int c = (threadIdx.x & 15) * 8;
