@@ -270,7 +270,8 @@ __global__ void __launch_bounds__(Shape::kWaves * kWave, 2) product_kernel(Produ
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int row_wave = wave % Shape::kRowWaves, token_wave = wave / Shape::kRowWaves;
     const int col = lane & 15, quad = lane >> 4;
-    const int64_t tiles = (int64_t)RowTiles<Shape::kTokens>(p).total * p.n_tiles;
+    RowTiles<Shape::kTokens> row_tiles(p);
+    const int64_t tiles = (int64_t)row_tiles.total * p.n_tiles;
     const int parts = tiles * p.parts <= p.slots ? p.parts : 1;  // more rows than announced: no room to share
     const int64_t total = tiles * parts;
     // Reads: this lane's two chunks within the first 16 rows of a fragment.
@@ -281,12 +282,14 @@ __global__ void __launch_bounds__(Shape::kWaves * kWave, 2) product_kernel(Produ
     const int load_k = ((lane & 7) ^ load_row) << 4;
     const int x_first = wave * (Shape::kTokens / Shape::kWaves);
     const int x_load_k = ((lane & 7) ^ ((x_first + load_row) & 7)) << 4;
-    for (int64_t i = blockIdx.x; i < (total + kXcds - 1) / kXcds * kXcds; i += gridDim.x) {
+    // (The row tiles are looked up again for each further item: kept, they
+    // would cost the loop over the blocks registers.)
+    for (int64_t i = blockIdx.x; i < (total + kXcds - 1) / kXcds * kXcds;
+         i += gridDim.x, row_tiles = RowTiles<Shape::kTokens>(p)) {
         const int64_t item = xcd_item(i, total);
         if (item >= total) continue;
         const int tile = (int)item / parts, part = (int)item - tile * parts;
-        // (Looked up again: kept, they would cost the loop below registers.)
-        const Tile t = find_tile(p, RowTiles<Shape::kTokens>(p), tile);
+        const Tile t = find_tile(p, row_tiles, tile);
         // The part's blocks of K.
         const int k_first = (int)((int64_t)p.k_blocks * part / parts);
         const int blocks = (int)((int64_t)p.k_blocks * (part + 1) / parts) - k_first;
@@ -616,15 +619,25 @@ using Shape64 = TileShape<64, 4, 3>;
 using Shape128 = TileShape<128, 2, 3>;
 using Shape256 = TileShape<256, 2, 2>;
 
-// The shape by the mean of the rows that an expert gets at most: one tile for
-// most experts, as each tile reads all the weights again.
+// The shape by the mean of the rows that an expert gets at most: with fewer
+// tokens per tile more experts need two tiles, which read the weights twice
+// (from L2) and take turns on the CUs; with more, a tile's empty fragments cost
+// their part of the ring and the last round of tiles leaves CUs idle. Measured
+// with 32 experts, us of 2048 -> 7168 channels at mean 4, 8, 16, 32, 48, 64, 96,
+// 128, 192, 384 rows:
+//    16 tokens   87   91  103  140  178  217  288  384  527  965
+//    32          90   88   93  107  133  147  193  235  319  584
+//    64          89   90   92   96  104  124  141  163  222  374
+//   128          93   93   97  100  106  111  123  154  184  318
+//   256         116  117  117  122  131  137  139  151  162  277
+// (7168 -> 4096 channels change over at the same means, give or take one).
 template <class F>
 auto with_shape(int64_t max_rows, int32_t num_experts, F f) {
     const int64_t mean = max_rows / num_experts;
-    if (mean <= 10) return f(Shape16{});
-    if (mean <= 20) return f(Shape32{});
-    if (mean <= 48) return f(Shape64{});
-    if (mean <= 192) return f(Shape128{});
+    if (mean <= 5) return f(Shape16{});
+    if (mean <= 13) return f(Shape32{});
+    if (mean <= 45) return f(Shape64{});
+    if (mean <= 115) return f(Shape128{});
     return f(Shape256{});
 }
 
