@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(Shape::kWaves * kWave, 2) product_kernel(Produ
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             const float g = acc[f][m][q];
-                            const float a = g * sigmoid(g) * u[q];
+                            const float a = g * fast_sigmoid(g) * u[q];
                             acc[f][m][q] = a;
                             const uint32_t mag = __float_as_uint(a) & 0x7fffffffu;
                             top = top > mag ? top : mag;
@@ -559,9 +559,9 @@ __global__ void __launch_bounds__(Shape::kWaves * kWave, 2) product_kernel(Produ
                 const float* g = sums + token * Shape::kSumRow + c;
                 float v[8];
 #pragma unroll
-                for (int q = 0; q < 8; ++q) v[q] = g[q] * sigmoid(g[q]) * g[128 + q];
+                for (int q = 0; q < 8; ++q) v[q] = g[q] * fast_sigmoid(g[q]) * g[128 + q];
                 uint8_t* dst = static_cast<uint8_t*>(p.out) + (int64_t)(t.row + token) * I + t.n * 128 + c;
-                quantize8(v, true, c == 0, dst, p.out_sf + (int64_t)(t.row + token) * (I / 128) + t.n);
+                quantize8<false>(v, true, c == 0, dst, p.out_sf + (int64_t)(t.row + token) * (I / 128) + t.n);
             }
             lds_barrier();
         }

@@ -53,7 +53,10 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v) {
 }
 
 // One block's 8 channels of a lane: quantised to dst, the scale by lane 0.
+// kStream: stored past the caches.
+template <bool kStream>
 __device__ __forceinline__ void quantize8(const float (&v)[8], bool live, bool first, uint8_t* dst, float* sf) {
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
     // The largest magnitude by its bits, which order as the values do, NaN
     // above infinity.
     uint32_t top = __float_as_uint(kAmaxFloor);
@@ -64,10 +67,14 @@ __device__ __forceinline__ void quantize8(const float (&v)[8], bool live, bool f
     }
     const float amax = __uint_as_float(row_max(top));
     const float scale = kFp8Max / amax;
-    uint2 o;
-    o.x = pack_fp8(v[0] * scale, v[1] * scale, v[2] * scale, v[3] * scale);
-    o.y = pack_fp8(v[4] * scale, v[5] * scale, v[6] * scale, v[7] * scale);
-    if (live) *reinterpret_cast<uint2*>(dst) = o;
+    const u32x2 o = {pack_fp8(v[0] * scale, v[1] * scale, v[2] * scale, v[3] * scale),
+                     pack_fp8(v[4] * scale, v[5] * scale, v[6] * scale, v[7] * scale)};
+    if (live) {
+        if (kStream)
+            __builtin_nontemporal_store(o, reinterpret_cast<u32x2*>(dst));
+        else
+            *reinterpret_cast<u32x2*>(dst) = o;
+    }
     if (first) *sf = amax / kFp8Max;
 }
 
@@ -117,7 +124,15 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
     return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
-// 1 / (1 + exp(-z)), the division rounded correctly.
+// 1 / (1 + exp(-z)) from the hardware's exp2 and reciprocal: relative error
+// about (|z| + 4) 2^-24, without which SwiGLU's gradient is bound by
+// arithmetic (expf and a correct division: 113 us for 32777 x 4096 channels,
+// 94 us with these).
+__device__ __forceinline__ float fast_sigmoid(float z) {
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504088896341f * z));
+}
+
+// 1 / (1 + exp(-z)), the division rounded correctly: what the gate compares.
 __device__ __forceinline__ float sigmoid(float z) { return 1.f / (1.f + expf(-z)); }
 
 }  // namespace moe_dispatch
