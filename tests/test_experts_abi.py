@@ -3,6 +3,9 @@ arguments come back as documented codes before any GPU work."""
 
 import ctypes
 import math
+import os
+import shutil
+import subprocess
 
 import pytest
 
@@ -159,3 +162,33 @@ def test_expert_workspace():
         call = lib.dispatch_expert_product_swiglu if swiglu else lib.dispatch_expert_product
         assert call(B(few), *[4096] * ptrs, 4096 + 128, need, None) == M.ERR_WORKSPACE
         assert call(B(few), *[4096] * ptrs, 4096, need - 1, None) == M.ERR_WORKSPACE
+
+
+STRUCTS = {
+    "dispatch_gate_problem_t": M.GateProblem, "dispatch_gate_out_t": M.GateOutPtrs,
+    "dispatch_quantize_problem_t": M.QuantizeProblem, "dispatch_expert_problem_t": M.ExpertProblem,
+}
+
+
+def test_struct_layouts_from_c(tmp_path):
+    """The structs of the header, compiled as C99, against the binding's."""
+    gcc = shutil.which("gcc")
+    if gcc is None or not os.path.isdir("/opt/rocm/include"):
+        pytest.skip("gcc or the ROCm headers are not installed")
+    lines, want = [], []
+    for c_name, py in STRUCTS.items():
+        lines.append(f'printf("%zu\\n", sizeof({c_name}));')
+        want.append(ctypes.sizeof(py))
+        for field, _ in py._fields_:
+            lines.append(f'printf("%zu\\n", offsetof({c_name}, {field}));')
+            want.append(getattr(py, field).offset)
+    src, exe = tmp_path / "probe.c", str(tmp_path / "probe")
+    src.write_text("#include <stddef.h>\n#include <stdio.h>\n#include \"moe_dispatch.h\"\nint main(void) {\n"
+                   + "\n".join(lines) + "\nreturn 0;\n}\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    build = subprocess.run([gcc, "-std=c99", "-Wall", "-Wextra", "-Werror", "-D__HIP_PLATFORM_AMD__", "-I",
+                            "/opt/rocm/include", "-I", os.path.join(root, "include"), str(src), "-o", exe],
+                           capture_output=True, text=True)
+    assert build.returncode == 0, build.stderr
+    got = subprocess.run([exe], capture_output=True, text=True, timeout=60)
+    assert [int(v) for v in got.stdout.split()] == want
