@@ -202,6 +202,9 @@ struct TileShape {
     // SwiGLU: a wavefront with all 128 channels of a half hands over through
     // registers, smaller ones through rows of sums in LDS.
     static constexpr int kSumRow = 256 + 4;
+    // Rows of the bf16 output in LDS, 16 bytes longer than their 256 channels.
+    static constexpr int kOutRow = 512 + 16;
+    static_assert(kTokens * kOutRow <= kLdsBytes, "rows of output");
     static constexpr bool kWholeBlock = kRows == 128;
     static_assert(kWholeBlock || kTokens * kSumRow * 4 <= kRingBytes, "rows of sums");
     static_assert(kLdsBytes <= kLdsPerCu, "LDS");
@@ -471,27 +474,32 @@ __global__ void __launch_bounds__(Shape::kWaves * kWave, 2) product_kernel(Produ
             }
         }
         const int first_token = token_wave * 16 + col;
-        if (!kSwiglu) {
-            uint16_t* out = static_cast<uint16_t*>(p.out);
-            const int n0 = t.n * 256 + row_wave * Shape::kRows + quad * 4;
+        if constexpr (!kSwiglu) {
+            // Through LDS, so that whole rows of 512 bytes leave (4096 x 8192
+            // x 1792 in two rounds of tiles: 68 us; stored straight from the
+            // registers, 32 bytes of each of 16 rows at a time, 84).
+            lds_barrier();
+            const int c0 = (row_wave * Shape::kRows + quad * 4) * 2;
 #pragma unroll
-            for (int m = 0; m < kM; ++m) {
-                const int r = first_token + m * Shape::kTokenWaves * 16;
-                if (r < t.rows) {
+            for (int m = 0; m < kM; ++m)
 #pragma unroll
-                    for (int f = 0; f < kF; ++f) {
-                        const int n = n0 + f * 16;
-                        if (n < p.N) {  // N is a multiple of 8
-                            uint2 o;
-                            o.x = pack_bf16(acc[f][m][0], acc[f][m][1]);
-                            o.y = pack_bf16(acc[f][m][2], acc[f][m][3]);
-                            *reinterpret_cast<uint2*>(out + (int64_t)(t.row + r) * p.N + n) = o;
-                        }
-                    }
+                for (int f = 0; f < kF; ++f) {
+                    uint2 o;
+                    o.x = pack_bf16(acc[f][m][0], acc[f][m][1]);
+                    o.y = pack_bf16(acc[f][m][2], acc[f][m][3]);
+                    *reinterpret_cast<uint2*>(smem + (first_token + m * Shape::kTokenWaves * 16) * Shape::kOutRow + c0 +
+                                              f * 32) = o;
                 }
+            lds_barrier();
+            uint16_t* const out = static_cast<uint16_t*>(p.out);
+            const int n = t.n * 256 + (lane & 31) * 8;
+            if (n < p.N) {  // N is a multiple of 8
+                for (int r = wave * 2 + (lane >> 5); r < t.rows; r += 2 * Shape::kWaves)
+                    *reinterpret_cast<u32x4*>(out + (int64_t)(t.row + r) * p.N + n) =
+                        *reinterpret_cast<const u32x4*>(smem + r * Shape::kOutRow + (lane & 31) * 16);
             }
             lds_barrier();  // the ring is free for the next tile
-        } else if (Shape::kWholeBlock) {
+        } else if constexpr (Shape::kWholeBlock) {
             // The up wavefronts hand their sums over through LDS, in the
             // order of their registers.
             const int I = p.N / 2;
