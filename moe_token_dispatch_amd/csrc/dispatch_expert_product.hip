@@ -17,6 +17,7 @@
 // long as both operands agree (the sum runs over all of them): lane group
 // g = lane / 16 takes the 16-byte chunks g and g + 4, so that one load
 // instruction covers 64 consecutive bytes of 16 rows.
+#include <cmath>
 #include <type_traits>
 
 #include "dispatch_common.hpp"
@@ -153,13 +154,14 @@ __device__ __forceinline__ int64_t xcd_item(int64_t b, int64_t total) {
 
 // Eight wavefronts compute 256 weight rows x kTokens tokens. Both operands go
 // through LDS in stages of one 128-channel block, loaded straight into it (no
-// registers in between), kStages deep: while one is computed the next ones are
+// registers in between), a ring of them deep: while one is computed the next are
 // on their way. The wavefronts are kRowWaves x kTokenWaves over the tile.
 //
 // Many tokens: the fp32 sums fill the registers (vector instructions reach 256
-// of them, so a wavefront's tile is at most 128 x 64) and the LDS reads of a
-// block, 24 KB per wavefront, take about as long as its 32 matrix
-// instructions; two stages of 64 KB leave no room for a third.
+// of them, so a wavefront's tile is at most 128 x 64). Measured with parts of
+// the loop taken out (32768 rows, 7168 -> 2048 channels, 531 us): without the
+// loads 390 us, with loads that always hit L2 500; a third stage of weights
+// (192 tokens) changed nothing. The matrix instructions alone are 250 us.
 //
 // Few tokens: the product reads weights and little else, and what counts is
 // how many bytes are in flight: three stages of four, 96 KB per CU. (A kernel
@@ -186,17 +188,20 @@ struct TileShape {
     static constexpr int kRows = 256 / kRowWaves;                   // weight rows of a wavefront
     static constexpr int kF = kRows / 16;                           // fragments of them
     static constexpr int kM = kTokens / 16 / kTokenWaves;           // fragments of its tokens
-    static constexpr int kWeightBytes = 256 * 128;
-    static constexpr int kStageBytes = kWeightBytes + kTokens * 128;
+    static constexpr int kWBytes = 256 * 128;      // of a stage
+    static constexpr int kXBytes = kTokens * 128;
     // Loads of a wavefront per stage: 32 weight rows, its eighth of the token
     // rows (8 per instruction; fewer use part of the lanes).
     static constexpr int kXLoads = kTokens >= 64 ? kTokens / 64 : 1;
     static constexpr int kXRows = kTokens / kWaves / kXLoads;       // rows of such a load
-    static constexpr int kLoads = 4 + kXLoads;
+    static constexpr int kWLoads = 4;
+    // Loads of a wavefront that may be outstanding when a block starts: all
+    // that were begun after that block's.
+    static constexpr int kAhead = (kStages - 2) * (kWLoads + kXLoads);
     static constexpr int kScaleBlocks = 8;                          // blocks whose scales are staged at a time
     static constexpr int kScaleFloats = kScaleBlocks * kTokens;
     static constexpr int kChunkFloats = kScaleFloats + 2 * kScaleBlocks;
-    static constexpr int kRingBytes = kStages * kStageBytes;
+    static constexpr int kRingBytes = kStages * (kWBytes + kXBytes);
     static constexpr int kLdsBytes = kRingBytes + 2 * kChunkFloats * 4;
     static constexpr int kSumFloats = 256 * kTokens;                // a tile's sums
     // SwiGLU: a wavefront with all 128 channels of a half hands over through
@@ -266,7 +271,7 @@ __device__ __forceinline__ f32x4 mfma_block(const i32x8& a, const i32x8& b) {
 
 template <class Shape, bool kSwiglu>
 __global__ void __launch_bounds__(Shape::kWaves * kWave, 2) product_kernel(ProductParams p) {
-    constexpr int kF = Shape::kF, kM = Shape::kM, kS = Shape::kScaleBlocks, kStages = Shape::kStages;
+    constexpr int kF = Shape::kF, kM = Shape::kM, kS = Shape::kScaleBlocks;
     extern __shared__ __align__(16) uint8_t smem[];
     float* const scales = reinterpret_cast<float*>(smem + Shape::kRingBytes);
     const int lane = threadIdx.x & (kWave - 1);
@@ -308,19 +313,25 @@ __global__ void __launch_bounds__(Shape::kWaves * kWave, 2) product_kernel(Produ
         // Rows past the last one are out of the descriptors' range.
         const int w_lane = (w_first + load_row) * p.K + load_k;
         const int x_lane = (x_first + load_row) * p.K + x_load_k;
-        // Load j of stage b; past the last block, and for chunks past K (a
-        // multiple of 16), out of range.
-        auto load_stage = [&](int b, int j) {
-            const int stage = lds_address(smem) + b % kStages * Shape::kStageBytes;
+        // Loads of block b's weights and tokens; past the last block, and for
+        // chunks past K (a multiple of 16), out of range.
+        auto load_w = [&](int b) {
+            const int dst = lds_address(smem) + b % Shape::kStages * Shape::kWBytes + (load_half * 128 + w_first) * 128;
             const int k = (k_first + b) * 128;
-            const int past = b < blocks ? 0 : INT32_MIN;
-            if (j < 4) {
-                const int out = k + load_k < p.K ? past : INT32_MIN;
-                load_to_lds(w_src, stage + (load_half * 128 + w_first + j * 8) * 128, (w_lane + j * 8 * p.K) | out, k);
-            } else if (Shape::kXRows == 8 || load_row < Shape::kXRows) {
-                const int out = k + x_load_k < p.K ? past : INT32_MIN;
-                load_to_lds(x_src, stage + Shape::kWeightBytes + (x_first + (j - 4) * 8) * 128,
-                            (x_lane + (j - 4) * 8 * p.K) | out, k);
+            const int out = b < blocks && k + load_k < p.K ? 0 : INT32_MIN;
+#pragma unroll
+            for (int j = 0; j < Shape::kWLoads; ++j)
+                load_to_lds(w_src, dst + j * 8 * 128, (w_lane + j * 8 * p.K) | out, k);
+        };
+        auto load_x = [&](int b) {
+            const int dst = lds_address(smem) + Shape::kStages * Shape::kWBytes + b % Shape::kStages * Shape::kXBytes +
+                            x_first * 128;
+            const int k = (k_first + b) * 128;
+            const int out = b < blocks && k + x_load_k < p.K ? 0 : INT32_MIN;
+            if (Shape::kXRows == 8 || load_row < Shape::kXRows) {
+#pragma unroll
+                for (int j = 0; j < Shape::kXLoads; ++j)
+                    load_to_lds(x_src, dst + j * 8 * 128, (x_lane + j * 8 * p.K) | out, k);
             }
         };
         // Scales, eight blocks at a time, one wavefront for each: a lane per
@@ -357,27 +368,28 @@ __global__ void __launch_bounds__(Shape::kWaves * kWave, 2) product_kernel(Produ
             for (int m = 0; m < kM; ++m) acc[f][m] = f32x4{0.f, 0.f, 0.f, 0.f};
         load_scales(0);
 #pragma unroll
-        for (int b = 0; b < kStages - 1; ++b)
-#pragma unroll
-            for (int j = 0; j < Shape::kLoads; ++j) load_stage(b, j);
+        for (int b = 0; b < Shape::kStages - 1; ++b) {
+            load_x(b);
+            load_w(b);
+        }
         // The blocks, for a tile whose rows fill kLive of each wavefront's
         // fragments of tokens.
         auto run = [&](auto live_fragments) {
         constexpr int kLive = decltype(live_fragments)::value;
         for (int b = 0; b < blocks; ++b) {
-            // This wavefront's part of the stage has arrived; past the
-            // barrier everybody's has, and the stage before is free.
-            wait_loads<(kStages - 2) * Shape::kLoads>();
+            // This wavefront's part of the block has arrived; past the
+            // barrier everybody's has, and the block before is done with.
+            wait_loads<Shape::kAhead>();
             lds_barrier();
             const int chunk = b / kS, in_chunk = b % kS;
             if (in_chunk == 0) load_scales(chunk + 1);  // to where nobody reads any more
             // (All at once: one load a step below arrived later and took
             // 602 us where this takes 560, 32768 x 7168 x 2048.)
-#pragma unroll
-            for (int j = 0; j < Shape::kLoads; ++j) load_stage(b + kStages - 1, j);
-            const uint8_t* const stage = smem + b % kStages * Shape::kStageBytes;
-            const uint8_t* const w_at = stage + row_wave * Shape::kRows * 128;
-            const uint8_t* const x_at = stage + Shape::kWeightBytes + token_wave * 16 * 128;
+            load_x(b + Shape::kStages - 1);
+            load_w(b + Shape::kStages - 1);
+            const uint8_t* const w_at = smem + b % Shape::kStages * Shape::kWBytes + row_wave * Shape::kRows * 128;
+            const uint8_t* const x_at = smem + Shape::kStages * Shape::kWBytes + b % Shape::kStages * Shape::kXBytes +
+                                        token_wave * 16 * 128;
             const float* const s_chunk = scales + (chunk & 1) * Shape::kChunkFloats;
             const float* const s_at = s_chunk + in_chunk * Shape::kTokens + token_wave * 16 + col;
             const float sw = s_chunk[Shape::kScaleFloats + row_wave / (Shape::kRowWaves / 2) * kS + in_chunk];
@@ -417,12 +429,12 @@ __global__ void __launch_bounds__(Shape::kWaves * kWave, 2) product_kernel(Produ
         // Fragments of tokens go to the token wavefronts in turn, so that a
         // tile's last rows spread over all of them.
         const int live = (t.rows + 16 * Shape::kTokenWaves - 1) / (16 * Shape::kTokenWaves);
-        if (kM >= 4 && live == 3)
-            run(std::integral_constant<int, (kM >= 4 ? 3 : kM)>());
-        else if (kM >= 4 && live == 2)
-            run(std::integral_constant<int, (kM >= 4 ? 2 : kM)>());
-        else if (kM >= 2 && live == 1)
-            run(std::integral_constant<int, (kM >= 2 ? 1 : kM)>());
+        if (live == 1)
+            run(std::integral_constant<int, 1>());
+        else if (live == 2)
+            run(std::integral_constant<int, (kM < 2 ? kM : 2)>());
+        else if (live == 3)
+            run(std::integral_constant<int, (kM < 3 ? kM : 3)>());
         else
             run(std::integral_constant<int, kM>());
         wait_loads<0>();  // (those past the last block write zeros to the ring)
@@ -625,27 +637,45 @@ using Shape16 = TileShape<16, 8, 4>;
 using Shape32 = TileShape<32, 8, 4>;
 using Shape64 = TileShape<64, 4, 3>;
 using Shape128 = TileShape<128, 2, 3>;
+using Shape192 = TileShape<192, 2, 2>;
 using Shape256 = TileShape<256, 2, 2>;
 
-// The shape by the mean of the rows that an expert gets at most: with fewer
-// tokens per tile more experts need two tiles, which read the weights twice
-// (from L2) and take turns on the CUs; with more, a tile's empty fragments cost
-// their part of the ring and the last round of tiles leaves CUs idle. Measured
-// with 32 experts, us of 2048 -> 7168 channels at mean 4, 8, 16, 32, 48, 64, 96,
-// 128, 192, 384 rows:
-//    16 tokens   87   91  103  140  178  217  288  384  527  965
-//    32          90   88   93  107  133  147  193  235  319  584
-//    64          89   90   92   96  104  124  141  163  222  374
-//   128          93   93   97  100  106  111  123  154  184  318
-//   256         116  117  117  122  131  137  139  151  162  277
+// Few rows: the shape by the mean of the rows that an expert gets at most.
+// With fewer tokens per tile more experts need two tiles, which read the
+// weights twice (from L2) and take turns on the CUs; with more, a tile's empty
+// fragments cost their part of the ring. Measured with 32 experts, us of 2048
+// -> 7168 channels at mean 4, 8, 16, 32, 48, 64, 96 rows:
+//    16 tokens   87   91  103  140  178  217  288
+//    32          90   88   93  107  133  147  193
+//    64          89   90   92   96  104  124  141
+//   128          93   93   97  100  106  111  123
 // (7168 -> 4096 channels change over at the same means, give or take one).
+//
+// Many rows: the shape whose rounds of tiles over the CUs cost least. A round
+// of 128- or 192-token tiles takes 0.66 or 0.86 of one of 256 tokens. An expert
+// has about half a tile more than its rows fill, or one tile if it is well
+// above the mean. Measured, us with 128, 192, 256 tokens (rows of 4096
+// channels, 8 experts, 4096 channels out): 4096 rows 117, 99, 121; 6000 rows
+// 153, 147, 124; 8191 rows 196, 156, 179; 12000 rows 260, 236, 224; the rule
+// took the fastest of the three in 12 of 12 such cases, 2 to 32 experts.
+template <class Shape>
+double rounds_cost(int64_t max_rows, int32_t num_experts, int32_t N, double round) {
+    const double fill = (double)max_rows / num_experts / Shape::kTokens;
+    const double per_expert = num_experts == 1 ? std::ceil(fill) : (fill <= 0.85 ? 1.0 : fill + 0.5);
+    return std::ceil(per_expert * num_experts * ((N + 255) / 256) / kCus) * round;
+}
+
 template <class F>
-auto with_shape(int64_t max_rows, int32_t num_experts, F f) {
+auto with_shape(int64_t max_rows, int32_t num_experts, int32_t N, F f) {
     const int64_t mean = max_rows / num_experts;
     if (mean <= 5) return f(Shape16{});
     if (mean <= 13) return f(Shape32{});
     if (mean <= 45) return f(Shape64{});
-    if (mean <= 115) return f(Shape128{});
+    const double c128 = rounds_cost<Shape128>(max_rows, num_experts, N, 0.66);
+    const double c192 = rounds_cost<Shape192>(max_rows, num_experts, N, 0.86);
+    const double c256 = rounds_cost<Shape256>(max_rows, num_experts, N, 1.0);
+    if (c128 < c192 && c128 < c256) return f(Shape128{});
+    if (c192 < c256) return f(Shape192{});
     return f(Shape256{});
 }
 
@@ -657,7 +687,7 @@ int64_t most_rows(const dispatch_expert_problem_t& p) {
 
 size_t expert_workspace_bytes(const dispatch_expert_problem_t& prob) {
     const int64_t max_rows = most_rows(prob);
-    return with_shape(max_rows, prob.num_experts, [&](auto shape) {
+    return with_shape(max_rows, prob.num_experts, (int32_t)prob.out_features, [&](auto shape) {
         return plan_product<decltype(shape)>(max_rows, prob.num_experts, (int32_t)prob.out_features,
                                              (int32_t)((prob.in_features + 127) / 128))
             .bytes;
@@ -685,7 +715,7 @@ hipError_t launch_expert_product(const dispatch_expert_problem_t& prob, const in
     p.k_blocks = (p.K + 127) / 128;
     p.n_blocks = (p.N + 127) / 128;
     const int64_t max_rows = most_rows(prob);
-    return with_shape(max_rows, prob.num_experts, [&](auto shape) {
+    return with_shape(max_rows, prob.num_experts, p.N, [&](auto shape) {
         using Shape = decltype(shape);
         return out_sf != nullptr ? launch_product<Shape, true>(p, max_rows, workspace, stream)
                                  : launch_product<Shape, false>(p, max_rows, workspace, stream);

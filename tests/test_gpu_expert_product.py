@@ -145,6 +145,15 @@ def test_any_row_bound_gives_the_same_rows(max_rows):
     _check_swiglu(s, *_run_swiglu(s, max_rows))
 
 
+# Announced rows that take the tiles of 16, 32, 64, 128, 192 and 256 tokens.
+@pytest.mark.parametrize("announced", [8, 20, 60, 200, 20000, 28000])
+@pytest.mark.parametrize("counts", [[700, 129], [1, 255]], ids=str)
+def test_every_tile_shape(announced, counts):
+    s = _problem(counts, 400, 512, 1, announced, tail=28000)
+    _check_product(s, _run_product(s, announced))
+    _check_swiglu(s, *_run_swiglu(s, announced))
+
+
 @pytest.mark.parametrize("counts", [[1], [3, 0, 20], [16, 0, 17, 1, 1, 40]], ids=str)
 @pytest.mark.parametrize("k", [2048, 5008])
 @pytest.mark.parametrize("announced", [None, 1, 60])
