@@ -1,15 +1,29 @@
 // The gate on gfx950: router logits to the routing table and its weights, the
 // per-expert counts and the balance loss, and the gradient of the logits.
 //
-// One wavefront per token. Lane l holds the logits of experts l, l + 64, ...,
-// V = ceil(E / 64) of them in registers, so a row is read once, and a row of
-// scores, its sums and its choice never leave the wavefront.
+// One wavefront per token, V = ceil(E / 64) experts per lane (rounded up to a
+// power of two) in registers: a row is read once, and its scores, sums and
+// choice never leave the wavefront. A lane holds pairs of neighbouring
+// experts, which arrive as one load. The next token's row is on its way while
+// this one's is worked on; it is widened when its turn comes, so that no load
+// is waited for early, but before this one's results are stored, so that it
+// does not wait for those either (with single loads, widened as they came,
+// 4096 tokens of 256 experts with gradients took 21.1 us, with pairs 17.8).
 //
-// Choice: K rounds of a wave maximum over what is left. Selection compares
-// the fp32 values themselves (for softmax the logits, whose order the scores
-// share), so ties are exact ties and go to the lowest expert. They are
-// compared as unsigned integers that order as the values do: an integer
-// maximum takes one instruction where a float maximum also has to quiet NaN.
+// Choice: K rounds of a wave maximum. Selection compares the fp32 values
+// themselves (for softmax the logits, whose order the scores share), so ties
+// are exact ties and go to the lowest expert. They are compared as unsigned
+// integers that order as the values do: an integer maximum takes one
+// instruction where a float maximum also has to quiet NaN. A lane orders each
+// pair once; a round then looks at the pairs' first keys alone: the lowest
+// pair and lane that hold the maximum are the lowest expert that does.
+//
+// What bounds it, at 65536 tokens of 256 experts, top-8, fp32: the forward
+// kernel takes 46 us for 71 MB, of which the rounds are 3.3 us each: 16 vector
+// and about 24 scalar instructions a token, and a SIMD has 64 tokens. The
+// gradient's kernel has no rounds and takes 25.6 us for 140 MB (5.5 TB/s, as a
+// large copy). Small batches are bound by the launch, 4.1 us for a call of 333
+// tokens.
 //
 // Balance: a wavefront keeps prob_sum of its lanes' experts in registers over
 // all its tokens; a workgroup adds its wavefronts in order and leaves one
@@ -36,7 +50,6 @@ struct GateParams {
     int64_t num_tokens;
     int32_t num_experts;
     int32_t num_topk;
-    int32_t logits_bytes;
     int32_t idx_bytes;
     uint32_t flags;
     float route_scale;
@@ -47,39 +60,155 @@ struct GateParams {
 template <int V>
 constexpr int kGateWaves = V <= 8 ? 16 : (V == 16 ? 8 : 4);
 
-// Lane's logits of row t, -inf past the last expert.
+// A lane's V experts are pairs of neighbours, pair j of lane l from expert
+// 2 (64 j + l) (with up to 64 experts a lane has one). With an odd number of
+// experts the last pair is moved back to end with them, and its first expert,
+// which the pair before has, does not count there; nor does a pair that starts
+// past the end.
 template <int V>
-__device__ __forceinline__ void load_row(const void* logits, int32_t bytes, int64_t t, int32_t E, int lane,
-                                         float (&z)[V]) {
-    if (bytes == 2) {
-        const uint16_t* row = static_cast<const uint16_t*>(logits) + t * E;
+constexpr int kPair = V < 2 ? V : 2;
+
+template <int V>
+struct Pair {
+    int start, first;  // where it starts, where it is moved to
+    __device__ __forceinline__ Pair(int lane, int v, int32_t E) {
+        constexpr int R = kPair<V>;
+        start = (v / R * kWave + lane) * R;
+        // (E > 32 V if V > 1: the first half of the pairs is whole.)
+        first = R * kWave * (v / R + 1) <= 32 * V || start < E - R ? start : E - R;
+    }
+};
+
+// Expert v of the lane, and whether it counts.
+template <int V>
+__device__ __forceinline__ int expert_of(int lane, int v, int32_t E) {
+    return Pair<V>(lane, v, E).first + v % kPair<V>;
+}
+template <int V>
+__device__ __forceinline__ bool counts(int lane, int v, int32_t E) {
+    const Pair<V> pair(lane, v, E);
+    return pair.first + v % kPair<V> >= pair.start;
+}
+
+// A pair as one access, of rows that start wherever their type may (global
+// memory takes accesses of any alignment).
+typedef uint32_t Halves2 __attribute__((aligned(2)));
+typedef uint32_t Floats2 __attribute__((ext_vector_type(2), aligned(4)));
+
+// Lane's logits of row t as they are in memory, a bf16 pair in one word.
+template <int V, bool kHalf>
+__device__ __forceinline__ void load_row(const void* logits, int64_t t, int32_t E, int lane, uint32_t (&w)[V]) {
+    constexpr int R = kPair<V>;
+    const uint16_t* half = static_cast<const uint16_t*>(logits) + t * E;
+    const uint32_t* full = static_cast<const uint32_t*>(logits) + t * E;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int e = v * kWave + lane;
-            z[v] = e < E ? bf16_low(row[e]) : kNone;
-        }
-    } else {
-        const float* row = static_cast<const float*>(logits) + t * E;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int e = v * kWave + lane;
-            z[v] = e < E ? row[e] : kNone;
+    for (int v = 0; v < V; v += R) {
+        const int first = Pair<V>(lane, v, E).first;
+        if constexpr (kHalf) {
+            if constexpr (R == 2)
+                w[v] = *reinterpret_cast<const Halves2*>(half + first);
+            else
+                w[v] = half[first];
+        } else if constexpr (R == 2) {
+            const Floats2 x = *reinterpret_cast<const Floats2*>(full + first);
+            w[v] = x.x, w[v + 1] = x.y;
+        } else {
+            w[v] = full[first];
         }
     }
+}
+
+// The loaded row as floats, -inf for what does not count.
+template <int V, bool kHalf>
+__device__ __forceinline__ void widen_row(const uint32_t (&w)[V], int32_t E, int lane, float (&z)[V]) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        if (kHalf)
+            z[v] = v % 2 == 0 ? bf16_low(w[v]) : bf16_high(w[v - v % 2]);
+        else
+            z[v] = __uint_as_float(w[v]);
+        z[v] = counts<V>(lane, v, E) ? z[v] : kNone;
+    }
+}
+
+// The gradient of row t's logits.
+template <int V, bool kHalf>
+__device__ __forceinline__ void store_row(void* grad, int64_t t, int32_t E, int lane, const float (&s)[V]) {
+    constexpr int R = kPair<V>;
+    uint16_t* const half = static_cast<uint16_t*>(grad) + t * E;
+    float* const full = static_cast<float*>(grad) + t * E;
+#pragma unroll
+    for (int v = 0; v < V; v += R) {
+        const Pair<V> pair(lane, v, E);
+        const bool whole = pair.first == pair.start;
+        const bool second = !whole && counts<V>(lane, v + R - 1, E);  // of a pair that was moved
+        if constexpr (kHalf) {
+            const uint32_t x = pack_bf16(s[v], s[v + R - 1]);
+            uint16_t* const at = half + pair.first;
+            if constexpr (R == 2) {
+                if (whole) *reinterpret_cast<Halves2*>(at) = x;
+                if (second) at[1] = (uint16_t)(x >> 16);
+            } else {
+                if (whole) *at = (uint16_t)x;
+            }
+        } else {
+            float* const at = full + pair.first;
+            if constexpr (R == 2) {
+                const Floats2 x = {__float_as_uint(s[v]), __float_as_uint(s[v + 1])};
+                if (whole) *reinterpret_cast<Floats2*>(at) = x;
+                if (second) at[1] = s[v + 1];
+            } else {
+                if (whole) *at = s[v];
+            }
+        }
+    }
+}
+
+// A row of the lanes' floats in LDS, each pair at the place it would have
+// without being moved. slot_of: where expert e's is;
+// expert_at: whose a slot is.
+template <int V>
+__device__ __forceinline__ int lane_slot(int lane, int v) {
+    return (v / kPair<V> * kWave + lane) * kPair<V> + v % kPair<V>;
+}
+template <int V>
+__device__ __forceinline__ int slot_of(int e, int32_t E) {
+    return kPair<V> == 2 && (E & 1) != 0 && e == E - 1 ? E : e;
+}
+template <int V>
+__device__ __forceinline__ int expert_at(int slot, int32_t E) {
+    return kPair<V> == 2 && slot == E ? E - 1 : slot;
+}
+template <int V>
+__device__ __forceinline__ void write_slots(float* row, int lane, const float (&s)[V]) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) row[lane_slot<V>(lane, v)] = s[v];
 }
 
 // A value as an unsigned integer of the same order, both zeros alike. What is
 // never taken, NaN and -inf, gets kNoKey, below every other value's.
 constexpr uint32_t kNoKey = 0x007fffffu;
 __device__ __forceinline__ uint32_t order_key(float c) {
-    const uint32_t u = __float_as_uint(fmaxf(c, kNone) + 0.f);  // (fmaxf drops NaN)
+    const uint32_t u = __float_as_uint(fmaxf(c + 0.f, kNone));  // (fmaxf drops NaN)
     return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+
+// The value of an order key, -inf of kNoKey.
+__device__ __forceinline__ float key_value(uint32_t key) {
+    return __uint_as_float((int32_t)key < 0 ? key ^ 0x80000000u : ~key);
 }
 
 // exp(x) for x <= 0 from the hardware's exp2: the argument's rounding leaves a
 // relative error of |x| 2^-24, far from where exp(x) counts in a sum with 1.
 __device__ __forceinline__ float exp_nonpositive(float x) {
     return __builtin_amdgcn_exp2f(x * 1.44269504088896341f);
+}
+
+// 1 / x within 1 ulp, exact for 1, for x in [2^-126, 2^126]: the hardware's
+// reciprocal and one Newton step, 3 instructions where a division takes 11.
+__device__ __forceinline__ float reciprocal(float x) {
+    const float r = __builtin_amdgcn_rcpf(x);
+    return __builtin_fmaf(__builtin_fmaf(-x, r, 1.f), r, r);
 }
 
 // A row's sum of scores (before softmax divides by it) and its reciprocal, 0
@@ -94,41 +223,91 @@ struct RowSum {
     }
 };
 
-// Scores of a row in place of its logits (softmax scores are shares already).
+// Scores of a row in place of its logits, whose largest has the key top
+// (softmax scores are shares already: their sum is at least 1, or the row has
+// nothing).
 template <int V, bool kSigmoid>
-__device__ __forceinline__ RowSum scores(float (&z)[V]) {
+__device__ __forceinline__ RowSum scores(float (&z)[V], uint32_t top) {
+    const float high = top == kNoKey ? 0.f : key_value(top);
     float sum = 0.f;
-    if (kSigmoid) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            z[v] = z[v] == kNone ? 0.f : sigmoid(z[v]);
-            sum += z[v];
-        }
-        sum = wave_sum(sum);
-        return {sum, sum == 0.f ? 0.f : 1.f / sum};
-    }
-    float top = kNone;
-#pragma unroll
-    for (int v = 0; v < V; ++v) top = fmaxf(top, z[v]);
-    top = wave_max(top);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        z[v] = z[v] == kNone ? 0.f : exp_nonpositive(z[v] - top);
+        if (kSigmoid)
+            z[v] = z[v] == kNone ? 0.f : sigmoid(z[v]);
+        else
+            z[v] = exp_nonpositive(z[v] - high);
         sum += z[v];
     }
     sum = wave_sum(sum);
-    const RowSum r{sum, sum == 0.f ? 0.f : 1.f / sum};
+    const RowSum r{sum, sum == 0.f ? 0.f : (kSigmoid ? 1.f / sum : reciprocal(sum))};
+    if (!kSigmoid) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) z[v] *= r.inv;
+        for (int v = 0; v < V; ++v) z[v] *= r.inv;
+    }
     return r;
 }
 
-template <int V, bool kSigmoid, bool kBalance>
+// A lane's pairs of keys, the larger one of each first, of equal ones the
+// lower expert's. A mask bit per lane says whose pairs have changed places:
+// a removal then costs two vector instructions a pair, the rest is scalar.
+template <int V>
+struct Pairs {
+    static constexpr int R = kPair<V>, kPairs = V / R;
+    uint32_t key[V];
+    uint64_t swapped[kPairs];
+
+    __device__ __forceinline__ void sort() {
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+            swapped[j] = 0;
+            if constexpr (R == 2) {
+                const uint32_t a = key[2 * j], b = key[2 * j + 1];
+                swapped[j] = __ballot(b > a);
+                key[2 * j] = a > b ? a : b;
+                key[2 * j + 1] = a > b ? b : a;
+            }
+        }
+    }
+    // The largest key of the wavefront.
+    __device__ __forceinline__ uint32_t top() const {
+        uint32_t m = key[0];
+#pragma unroll
+        for (int j = 1; j < kPairs; ++j) m = m > key[j * R] ? m : key[j * R];
+        return wave_max(m);
+    }
+    // Takes the lowest expert whose key is m, the largest, out: its slot.
+    __device__ __forceinline__ int take(uint32_t m) {
+        uint64_t hit = __ballot(key[0] == m), out[kPairs];
+        int pair = 0;
+#pragma unroll
+        for (int j = 1; j < kPairs; ++j) {
+            const uint64_t here = __ballot(key[j * R] == m);
+            pair = hit == 0 ? j : pair;
+            hit = hit == 0 ? here : hit;
+        }
+        const int l = __builtin_ctzll(hit);
+        const uint64_t bit = uint64_t(1) << l;
+        uint64_t order = 0;
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+            const bool here = kPairs == 1 || pair == j;
+            out[j] = here ? bit : 0;
+            order = here ? swapped[j] : order;
+            swapped[j] ^= out[j];
+            const bool mine = __builtin_amdgcn_inverse_ballot_w64(out[j]);
+            if constexpr (R == 2) key[j * R] = mine ? key[j * R + 1] : key[j * R];
+            key[j * R + R - 1] = mine ? kNoKey : key[j * R + R - 1];
+        }
+        return (pair * kWave + l) * R + (R == 2 ? (int)(order >> l) & 1 : 0);
+    }
+};
+
+template <int V, bool kHalf, bool kSigmoid, bool kBalance>
 __global__ void __launch_bounds__(kGateWaves<V> * kWave) gate_kernel(GateParams p) {
     // A row of scores per wavefront, then with kBalance the workgroup's
     // counts [E] and live tokens [1].
     extern __shared__ float lds[];
-    const int W = blockDim.x / kWave;
+    const int W = kBalance ? kGateWaves<V> : (int)blockDim.x / kWave;
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int E = p.num_experts, K = p.num_topk;
@@ -145,54 +324,74 @@ __global__ void __launch_bounds__(kGateWaves<V> * kWave) gate_kernel(GateParams 
     }
     const int64_t stride = (int64_t)gridDim.x * W;
     int64_t t = (int64_t)blockIdx.x * W + wave;
-    // The next token's row is loaded while this one's is worked on.
-    float next[V];
-    if (t < p.num_tokens) load_row<V>(p.logits, p.logits_bytes, t, E, lane, next);
+    uint32_t next[V];
+    int next_live = 1;
+    const auto load = [&](int64_t row) {
+        load_row<V, kHalf>(p.logits, row, E, lane, next);
+        if (p.mask != nullptr) next_live = p.mask[row];
+    };
+    // The loaded row becomes the current one before the last one's results are
+    // stored, so that it does not wait for them.
+    float s[V];
+    bool taken = false;
+    const auto arrive = [&] {
+        widen_row<V, kHalf>(next, E, lane, s);
+        taken = __builtin_amdgcn_readfirstlane(next_live) != 0;
+    };
+    if (t < p.num_tokens) load(t);
+    const auto bias_of = [&](int v) { return p.bias != nullptr ? p.bias[expert_of<V>(lane, v, E)] : 0.f; };
+    // Kept in registers where there are enough of them.
+    constexpr bool kKeepBias = kSigmoid && V <= 16;
+    float bias[kKeepBias ? V : 1];
+    if constexpr (kKeepBias) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) bias[v] = bias_of(v);
+    }
+    if (t < p.num_tokens) arrive();
     for (; t < p.num_tokens; t += stride) {
-        int picked = -1;     // lane k: entry k's expert
+        int picked = -1;     // lane k: entry k's slot, then its expert
         float weight = 0.f;  // lane k: its score
-        float s[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) s[v] = next[v];
-        if (t + stride < p.num_tokens) load_row<V>(p.logits, p.logits_bytes, t + stride, E, lane, next);
-        if (p.mask == nullptr || p.mask[t] != 0) {
-            uint32_t c[V];
-#pragma unroll
-            for (int v = 0; v < V; ++v) c[v] = order_key(s[v]);
-            const RowSum row_sum = scores<V, kSigmoid>(s);
+        if (t + stride < p.num_tokens) load(t + stride);
+        if (taken) {
+            Pairs<V> pairs;
+            RowSum row_sum;
+            uint32_t m;
             if (kSigmoid) {
+                bool never[V];
+#pragma unroll
+                for (int v = 0; v < V; ++v) never[v] = !(s[v] > kNone);
+                row_sum = scores<V, true>(s, kNoKey);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    const int e = v * kWave + lane;
-                    const float b = p.bias != nullptr && e < E ? p.bias[e] : 0.f;
-                    c[v] = c[v] == kNoKey ? kNoKey : order_key(s[v] + b);
+                    const float b = kKeepBias ? bias[kKeepBias ? v : 0] : bias_of(v);
+                    pairs.key[v] = never[v] ? kNoKey : order_key(s[v] + b);
                 }
+                pairs.sort();
+                m = pairs.top();
+            } else {
+#pragma unroll
+                for (int v = 0; v < V; ++v) pairs.key[v] = order_key(s[v]);
+                pairs.sort();
+                m = pairs.top();
+                row_sum = scores<V, false>(s, m);
             }
-#pragma unroll
-            for (int v = 0; v < V; ++v) score_row[v * kWave + lane] = s[v];
-            for (int k = 0; k < K; ++k) {
-                uint32_t m = c[0];
-#pragma unroll
-                for (int v = 1; v < V; ++v) m = m > c[v] ? m : c[v];
-                m = wave_max(m);
-                if (m == kNoKey) break;
-                int e = -1;
-#pragma unroll
-                for (int v = V - 1; v >= 0; --v) {
-                    const uint64_t hit = __ballot(c[v] == m);
-                    if (hit != 0) e = v * kWave + __builtin_ctzll(hit);
-                }
-                const bool here = lane == (e & (kWave - 1));
-#pragma unroll
-                for (int v = 0; v < V; ++v) c[v] = here && (e / kWave) == v ? kNoKey : c[v];
-                picked = lane == k ? e : picked;
+            write_slots<V>(score_row, lane, s);
+            for (int k = 0; m != kNoKey;) {
+                const int slot = pairs.take(m);
+                picked = lane == k ? slot : picked;
+                if (++k == K) break;
+                m = pairs.top();
             }
             __builtin_amdgcn_wave_barrier();
             if (picked >= 0) weight = score_row[picked];
+            picked = expert_at<V>(picked, E);
             __builtin_amdgcn_wave_barrier();
             if (p.flags & DISPATCH_GATE_NORMALIZE) {
                 const float total = wave_sum(weight);
-                weight = total == 0.f ? 0.f : p.route_scale * weight / total;
+                // (A softmax row's largest share is at least 1 / E.)
+                weight = total == 0.f ? 0.f
+                         : kSigmoid   ? p.route_scale * weight / total
+                                      : p.route_scale * weight * reciprocal(total);
             } else {
                 weight *= p.route_scale;
             }
@@ -203,6 +402,7 @@ __global__ void __launch_bounds__(kGateWaves<V> * kWave) gate_kernel(GateParams 
                 if (picked >= 0) atomicAdd(counts + picked, 1);
             }
         }
+        if (t + stride < p.num_tokens) arrive();
         if (lane < K) {
             const int64_t at = t * K + lane;
             if (p.idx_bytes == 8)
@@ -215,16 +415,17 @@ __global__ void __launch_bounds__(kGateWaves<V> * kWave) gate_kernel(GateParams 
     if (!kBalance) return;
     // Each wavefront leaves its sums in its row; a thread adds an expert's
     // over the rows, in order.
-#pragma unroll
-    for (int v = 0; v < V; ++v) score_row[v * kWave + lane] = prob_sum[v];
+    write_slots<V>(score_row, lane, prob_sum);
     if (lane == 0) atomicAdd(counts + E, live);
     __syncthreads();
     float* const out = p.partial + (int64_t)blockIdx.x * (2 * E + 1);
     for (int i = threadIdx.x; i < 2 * E + 1; i += W * kWave) {
         float x = __int_as_float(counts[i - E < 0 ? 0 : i - E]);
         if (i < E) {
-            x = lds[i];
-            for (int w = 1; w < W; ++w) x += lds[w * V * kWave + i];
+            const float* at = lds + slot_of<V>(i, E);
+            x = at[0];
+#pragma unroll
+            for (int w = 1; w < kGateWaves<V>; ++w) x += at[w * V * kWave];
         }
         out[i] = x;
     }
@@ -251,9 +452,22 @@ gate_sum_kernel(const float* partial, int groups, int E, int K, float loss_coef,
     float s = 0.f;
     int n = 0;
     if (e < E) {
-        for (int g = g0; g < groups; g += kSumGroups) {
-            s += partial[g * stride + e];
-            n += __float_as_int(partial[g * stride + E + e]);
+        // Eight rows on their way at once (past the last: its own, not added).
+        constexpr int kAtOnce = 8;
+        for (int g = g0; g < groups; g += kAtOnce * kSumGroups) {
+            float a[kAtOnce];
+            int b[kAtOnce];
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                const int row = g + i * kSumGroups < groups ? g + i * kSumGroups : groups - 1;
+                a[i] = partial[row * stride + e];
+                b[i] = __float_as_int(partial[row * stride + E + e]);
+            }
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                s += g + i * kSumGroups < groups ? a[i] : 0.f;
+                n += g + i * kSumGroups < groups ? b[i] : 0;
+            }
         }
     }
     // The four groups of a wavefront, then the wavefronts in order.
@@ -270,7 +484,12 @@ gate_sum_kernel(const float* partial, int groups, int E, int K, float loss_coef,
     // workgroup needs them, but it would wait for them).
     int live = 0;
     if (threadIdx.x < kWave) {
-        for (int g = lane; g < groups; g += kWave) live += __float_as_int(partial[g * stride + 2 * E]);
+#pragma unroll
+        for (int i = 0; i < kGateMaxGroups / kWave; ++i) {
+            const int g = i * kWave + lane;
+            const int here = __float_as_int(partial[(g < groups ? g : groups - 1) * stride + 2 * E]);
+            live += g < groups ? here : 0;
+        }
         for (int step = kWave / 2; step > 0; step /= 2) live += __shfl_xor(live, step);
     }
     __syncthreads();
@@ -315,7 +534,6 @@ struct GateBackwardParams {
     int64_t num_tokens;
     int32_t num_experts;
     int32_t num_topk;
-    int32_t logits_bytes;
     int32_t idx_bytes;
     uint32_t flags;
     float route_scale;
@@ -325,8 +543,9 @@ struct GateBackwardParams {
 // Gradient of the logits. The row is read again and its scores computed
 // again, which is cheaper than storing them. Lane k holds entry k: its
 // score's gradient goes through the wavefront's row in LDS to the lane that
-// holds the expert.
-template <int V, bool kSigmoid>
+// holds the expert. The row and its entries are loaded before anything is
+// waited for.
+template <int V, bool kHalf, bool kSigmoid>
 __global__ void __launch_bounds__(kGateWaves<V> * kWave) gate_backward_kernel(GateBackwardParams p) {
     constexpr int W = kGateWaves<V>;
     extern __shared__ float lds[];  // [W][V * 64] score gradients, zero between tokens
@@ -334,6 +553,40 @@ __global__ void __launch_bounds__(kGateWaves<V> * kWave) gate_backward_kernel(Ga
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int E = p.num_experts, K = p.num_topk;
     float* const row = lds + wave * V * kWave;
+    const int64_t stride = (int64_t)gridDim.x * W;
+    int64_t t = (int64_t)blockIdx.x * W + wave;
+    uint32_t next[V];
+    int next_live = 1;
+    uint64_t next_id = 0;
+    float next_dw = 0.f;
+    const int entry = lane < K ? lane : K - 1;
+    const auto load = [&](int64_t token) {
+        load_row<V, kHalf>(p.logits, token, E, lane, next);
+        if (p.mask != nullptr) next_live = p.mask[token];
+        if (p.grad_weights != nullptr) {
+            const int64_t at = token * K + entry;
+            uint64_t id;
+            if (p.idx_bytes == 8)
+                id = static_cast<const uint64_t*>(p.topk_idx)[at];
+            else
+                id = static_cast<const uint32_t*>(p.topk_idx)[at];
+            next_id = id;
+            next_dw = p.grad_weights[at];
+        }
+    };
+    if (t < p.num_tokens) load(t);
+    // As in the forward kernel.
+    float z[V];
+    bool taken = false;
+    int e = -1;  // lane k: entry k's expert
+    float dw = 0.f;
+    const auto arrive = [&] {
+        widen_row<V, kHalf>(next, E, lane, z);
+        taken = __builtin_amdgcn_readfirstlane(next_live) != 0;
+        const bool any = p.grad_weights != nullptr && lane < K && next_id < (uint64_t)E;
+        e = any ? (int)next_id : -1;
+        dw = any ? next_dw : 0.f;
+    };
     float dp[V];  // the loss's gradient of this lane's experts' p: the same for every token
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -345,33 +598,28 @@ __global__ void __launch_bounds__(kGateWaves<V> * kWave) gate_backward_kernel(Ga
         const float unit = n == 0.f ? 0.f : *p.grad_loss * (p.loss_coef * (float)E / ((float)K * n * n));
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int e = v * kWave + lane;
-            if (e < E) dp[v] = unit * (float)p.expert_count[e];
+            if (counts<V>(lane, v, E)) dp[v] = unit * (float)p.expert_count[expert_of<V>(lane, v, E)];
         }
     }
-    for (int64_t t = (int64_t)blockIdx.x * W + wave; t < p.num_tokens; t += (int64_t)gridDim.x * W) {
+    if (t < p.num_tokens) arrive();
+    for (; t < p.num_tokens; t += stride) {
         float s[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) s[v] = 0.f;
-        if (p.mask == nullptr || p.mask[t] != 0) {
-            int e = -1;
-            float dw = 0.f;
-            if (lane < K && p.grad_weights != nullptr) {
-                const int64_t at = t * K + lane;
-                const int64_t id = p.idx_bytes == 8 ? static_cast<const int64_t*>(p.topk_idx)[at]
-                                                    : (int64_t)static_cast<const int32_t*>(p.topk_idx)[at];
-                if (id >= 0 && id < E) {
-                    e = (int)id;
-                    dw = p.grad_weights[at];
-                }
-            }
-            load_row<V>(p.logits, p.logits_bytes, t, E, lane, s);
-            const RowSum row_sum = scores<V, kSigmoid>(s);
-            // The scores of the taken experts, through the row in LDS.
+        for (int v = 0; v < V; ++v) s[v] = z[v];
+        if (t + stride < p.num_tokens) load(t + stride);
+        if (taken) {
+            uint32_t top = kNoKey;
+            if (!kSigmoid) {
+                float high = s[0];
 #pragma unroll
-            for (int v = 0; v < V; ++v) row[v * kWave + lane] = s[v];
+                for (int v = 1; v < V; ++v) high = fmaxf(high, s[v]);
+                top = wave_max(order_key(high));
+            }
+            const RowSum row_sum = scores<V, kSigmoid>(s, top);
+            // The scores of the taken experts, through the row in LDS.
+            write_slots<V>(row, lane, s);
             __builtin_amdgcn_wave_barrier();
-            const float mine = e >= 0 ? row[e] : 0.f;
+            const float mine = e >= 0 ? row[slot_of<V>(e, E)] : 0.f;
             __builtin_amdgcn_wave_barrier();
             float ds = p.route_scale * dw;
             if (p.flags & DISPATCH_GATE_NORMALIZE) {
@@ -379,16 +627,16 @@ __global__ void __launch_bounds__(kGateWaves<V> * kWave) gate_backward_kernel(Ga
                 const float mean = wave_sum(dw * mine);
                 ds = total == 0.f ? 0.f : p.route_scale / total * (dw - mean / total);
             }
-#pragma unroll
-            for (int v = 0; v < V; ++v) row[v * kWave + lane] = 0.f;
+            const float zero[V] = {};
+            write_slots<V>(row, lane, zero);
             __builtin_amdgcn_wave_barrier();
-            if (e >= 0) row[e] = ds;
+            if (e >= 0) row[slot_of<V>(e, E)] = ds;
             __builtin_amdgcn_wave_barrier();
             float d[V];
             float mean = 0.f;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                d[v] = row[v * kWave + lane];
+                d[v] = row[lane_slot<V>(lane, v)];
                 if (kSigmoid) {
                     mean += row_sum.share(s[v]) * dp[v];
                 } else {
@@ -401,23 +649,30 @@ __global__ void __launch_bounds__(kGateWaves<V> * kWave) gate_backward_kernel(Ga
 #pragma unroll
             for (int v = 0; v < V; ++v)
                 s[v] = kSigmoid ? (d[v] + (dp[v] - mean) * row_sum.inv) * s[v] * (1.f - s[v]) : s[v] * (d[v] - mean);
-        }
-        if (p.logits_bytes == 2) {
-            uint16_t* out = static_cast<uint16_t*>(p.grad_logits) + t * E;
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int e = v * kWave + lane;
-                if (e < E) out[e] = (uint16_t)pack_bf16(s[v], 0.f);
-            }
         } else {
-            float* out = static_cast<float*>(p.grad_logits) + t * E;
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int e = v * kWave + lane;
-                if (e < E) out[e] = s[v];
-            }
+            for (int v = 0; v < V; ++v) s[v] = 0.f;
         }
+        if (t + stride < p.num_tokens) arrive();
+        store_row<V, kHalf>(p.grad_logits, t, E, lane, s);
     }
+}
+
+template <int V, bool kHalf>
+const void* gate_kernel_of(bool sigmoid, bool balance) {
+    if (sigmoid)
+        return balance ? (const void*)&gate_kernel<V, kHalf, true, true> : (const void*)&gate_kernel<V, kHalf, true, false>;
+    return balance ? (const void*)&gate_kernel<V, kHalf, false, true> : (const void*)&gate_kernel<V, kHalf, false, false>;
+}
+template <int V>
+const void* gate_kernel_of(bool half, bool sigmoid, bool balance) {
+    return half ? gate_kernel_of<V, true>(sigmoid, balance) : gate_kernel_of<V, false>(sigmoid, balance);
+}
+template <int V>
+const void* gate_backward_of(bool half, bool sigmoid) {
+    if (half)
+        return sigmoid ? (const void*)&gate_backward_kernel<V, true, true> : (const void*)&gate_backward_kernel<V, true, false>;
+    return sigmoid ? (const void*)&gate_backward_kernel<V, false, true> : (const void*)&gate_backward_kernel<V, false, false>;
 }
 
 // f<V> for the fewest V of 1, 2, 4, ..., 64 that hold E experts in 64 lanes.
@@ -449,16 +704,13 @@ hipError_t launch_gate(const dispatch_gate_problem_t& prob, const void* logits, 
     p.num_tokens = prob.num_tokens;
     p.num_experts = prob.num_experts;
     p.num_topk = prob.num_topk;
-    p.logits_bytes = prob.logits_bytes;
     p.idx_bytes = prob.topk_idx_bytes;
     p.flags = prob.flags;
     p.route_scale = prob.route_scale;
-    const bool sig = prob.scoring == DISPATCH_GATE_SIGMOID;
+    const bool sig = prob.scoring == DISPATCH_GATE_SIGMOID, half = prob.logits_bytes == 2;
     const bool balance = out.loss != nullptr;
     if (prob.num_tokens == 0 && !balance) return hipSuccess;
-#define DISPATCH_F(V)                                                                           \
-    (sig ? (balance ? (const void*)&gate_kernel<V, true, true> : (const void*)&gate_kernel<V, true, false>)     \
-         : (balance ? (const void*)&gate_kernel<V, false, true> : (const void*)&gate_kernel<V, false, false>))
+#define DISPATCH_F(V) gate_kernel_of<V>(half, sig, balance)
     const void* kernel = DISPATCH_GATE_BY_V(E, DISPATCH_F);
 #undef DISPATCH_F
 #define DISPATCH_F(V) kGateWaves<V>
@@ -510,14 +762,13 @@ hipError_t launch_gate_backward(const dispatch_gate_problem_t& prob, const void*
     p.num_tokens = prob.num_tokens;
     p.num_experts = prob.num_experts;
     p.num_topk = prob.num_topk;
-    p.logits_bytes = prob.logits_bytes;
     p.idx_bytes = prob.topk_idx_bytes;
     p.flags = prob.flags;
     p.route_scale = prob.route_scale;
     p.loss_coef = prob.loss_coef;
-    const bool sig = prob.scoring == DISPATCH_GATE_SIGMOID;
+    const bool sig = prob.scoring == DISPATCH_GATE_SIGMOID, half = prob.logits_bytes == 2;
     const int E = prob.num_experts;
-#define DISPATCH_F(V) (sig ? (const void*)&gate_backward_kernel<V, true> : (const void*)&gate_backward_kernel<V, false>)
+#define DISPATCH_F(V) gate_backward_of<V>(half, sig)
     const void* kernel = DISPATCH_GATE_BY_V(E, DISPATCH_F);
 #undef DISPATCH_F
 #define DISPATCH_F(V) kGateWaves<V>

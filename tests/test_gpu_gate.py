@@ -302,3 +302,39 @@ def test_binding_refuses_wrong_tensors():
         M.dispatch_gate(soft, z, out, ws, select_bias=torch.zeros(20, device=DEV))
     with pytest.raises(ValueError, match="bfloat16 or float32"):
         M.make_gate_problem(1, 2, 1, logits_dtype=torch.float16)
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("e", [63, 65, 127, 129, 255, 257, 511, 999, 2047, 2049])
+def test_odd_expert_counts_at_any_alignment(sigmoid, dtype, e):
+    """Rows of an odd length, their first element one past an aligned address; nothing beside them is written."""
+    t, k = 19, 8
+    g = torch.Generator().manual_seed(e)
+    z = torch.randint(-3, 4, (t, e), generator=g).to(dtype)  # many ties
+    z[4, : e - 1] = -math.inf   # one expert, the last
+    z[5, 0] = z[5, e - 1] = 9.0
+    p = M.make_gate_problem(t, e, k, M.GATE_SIGMOID if sigmoid else M.GATE_SOFTMAX, dtype, True, 2.0, 0.5, 8)
+    out = M.alloc_gate(p, DEV)
+    flat = torch.full((t * e + 2,), math.nan, dtype=dtype, device=DEV)
+    rows = flat[1:-1].view(t, e)
+    rows.copy_(z)
+    M.dispatch_gate(p, rows, out, M.alloc_gate_workspace(p, DEV))
+    torch.cuda.synchronize()
+    ref = R.gate(z, k, sigmoid, True, 2.0, 0.5, None, None)
+    idx, count = out.topk_idx.cpu().long(), out.expert_count.cpu()
+    assert torch.equal(idx, ref["idx"]) and torch.equal(count.long(), ref["count"])
+    assert torch.all((out.topk_weights.cpu().double() - ref["weights"]).abs() <= REL * (ref["weights"] + 2.0 ** -20))
+    assert torch.all((out.prob_sum.cpu().double() - ref["prob_sum"]).abs() <= REL * (ref["prob_sum"] + 2.0 ** -60))
+    dw = torch.randn((t, k), generator=g)
+    dloss = torch.tensor([1.7])
+    grad = torch.full((t * e + 2,), 77.0, dtype=dtype, device=DEV)
+    M.dispatch_gate_backward(p, rows, out, dw.to(DEV), dloss.to(DEV), grad[1:-1].view(t, e))
+    torch.cuda.synchronize()
+    grad = grad.cpu().double()
+    assert grad[0] == 77 and grad[-1] == 77
+    want = R.gate_gradient(z, idx, count, sigmoid, True, 2.0, 0.5, dw, dloss, None)
+    rel = REL + (BF16 if dtype == torch.bfloat16 else 0)
+    size = 2.0 * dw.abs().amax() + want.abs().amax()
+    got = grad[1:-1].view(t, e)
+    assert torch.all((got - want).abs() <= rel * want.abs() + 8 * REL * size), (got - want).abs().max()
