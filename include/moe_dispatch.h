@@ -19,6 +19,11 @@
  * and deterministic. The (token, rank) slot is held by the highest k of that
  * rank in the token (the page's dedup "master lane", section 4.2).
  *
+ * It also holds the expert layer around the dispatch (last part of this file):
+ * the gate that makes topk_idx and its weights, with the balance loss and the
+ * logits' gradient; rows to fp8 with a scale per 128 channels; and the experts'
+ * fp8 product over recv_x.
+ *
  * Conventions for every entry point:
  *   - Ownership: all buffer pointers are device pointers allocated and owned by
  *     the caller. The library allocates, frees and retains no memory.

@@ -2,9 +2,10 @@
 
 Layout (Count -> Prefix Sum -> stable slots) and row scatter of a token batch
 into a rank-contiguous buffer and an expert-major buffer, as hand-written HIP
-kernels for gfx950 behind a C ABI (``include/moe_dispatch.h``). This package is
-the thin Python binding: it marshals torch device tensors and the current
-stream into the C calls.
+kernels for gfx950 behind a C ABI (``include/moe_dispatch.h``); the combine; and
+the expert layer around them: the gate with its balance loss and gradient, rows
+to fp8, and the experts' fp8 product. This package is the thin Python binding:
+it marshals torch device tensors and the current stream into the C calls.
 """
 
 from ._binding import (  # noqa: F401

@@ -1,6 +1,6 @@
 """ctypes binding of the dispatch C ABI (``include/moe_dispatch.h``).
 
-Argument marshalling only: every step of dispatch runs in the HIP kernels of
+Argument marshalling only: every operator runs in the HIP kernels of
 ``libmoe_dispatch.so``. torch supplies device memory and the current stream.
 The library must have been built (``python -m moe_token_dispatch_amd.build``);
 loading fails loudly otherwise, and there is no fallback path.

