@@ -18,9 +18,10 @@
 // pair once; a round then looks at the pairs' first keys alone: the lowest
 // pair and lane that hold the maximum are the lowest expert that does.
 //
-// What bounds it, at 65536 tokens of 256 experts, top-8, fp32: the forward
-// kernel takes 46 us for 71 MB, of which the rounds are 3.3 us each: 16 vector
-// and about 24 scalar instructions a token, and a SIMD has 64 tokens. The
+// What bounds it: the rounds, 16 vector and about 24 scalar instructions a
+// token, 3.3 us each for 65536 tokens of 256 experts. Many tokens with up to
+// 256 experts therefore take a form of their own (gate_rows_kernel): 65536
+// tokens, top-8, fp32, 28 us for 71 MB on the trace, where this one takes 46. The
 // gradient's kernel has no rounds and takes 25.6 us for 140 MB (5.5 TB/s, as a
 // large copy). Small batches are bound by the launch, 4.1 us for a call of 333
 // tokens.
@@ -431,6 +432,264 @@ __global__ void __launch_bounds__(kGateWaves<V> * kWave) gate_kernel(GateParams 
     }
 }
 
+// The forward pass of many tokens and up to 256 experts: four tokens per
+// wavefront, 16 lanes for each, V = 8 or 16 experts per lane in runs of four
+// neighbours (run j of lane c from expert 4 (16 j + c); a run that would pass
+// the last expert is moved back, as a pair above).
+//
+// Choice of up to eight: a key and its expert are one number, key * 256 + 255
+// - expert, exact in a double (2^52 is added, so that its bits are put together
+// by two instructions), and all differ: a maximum and a minimum, one full-rate
+// instruction each, order two of them with no tie to look at. A lane sorts its
+// numbers, and four times lanes join their best eight with a partner's: the
+// larger of each and the partner's opposite are the best eight of both, in a
+// bitonic order that three steps sort. What is done once a token above (sums,
+// divisions, stores) is done once for four.
+//
+// Measured against the form above, us without and with balance outputs, 256
+// experts, top-8, softmax of fp32: 4096 tokens 4.6 and 12.7 (above 5.0, 12.3),
+// 8192 4.7 and 13.1 (7.1, 15.2), 65536 21.9 and 34.0 (38.2, 51.0); sigmoid of
+// bf16 with balance: 4096 15.6 (13.3), 8192 16.0 (16.9), 65536 46.9 (58.8). Its
+// time does not depend on k, a round above takes 3.3 us of 65536 tokens: even at
+// three rounds, four with sigmoid.
+constexpr int kBest = 8;
+constexpr int kFewestRounds = 4;
+constexpr int64_t kManyTokens = 8192;
+constexpr int kRowLanes = 16;
+constexpr int kRowTokens = kWave / kRowLanes;
+constexpr int kRowWaves = 8;
+
+template <int V>
+struct Quad {
+    int start, first;  // as of Pair
+    __device__ __forceinline__ Quad(int c, int v, int32_t E) {
+        start = (v / 4 * kRowLanes + c) * 4;
+        // (E > 8 V: the first half is whole.)
+        first = 4 * kRowLanes * (v / 4 + 1) <= 8 * V || start < E - 4 ? start : E - 4;
+    }
+};
+
+typedef uint32_t Halves4 __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t Floats4 __attribute__((ext_vector_type(4), aligned(4)));
+
+__device__ __forceinline__ double larger(double a, double b) { return __builtin_fmax(a, b); }
+__device__ __forceinline__ double smaller(double a, double b) { return __builtin_fmin(a, b); }
+
+__device__ __forceinline__ double numbered(uint32_t key, int expert) {
+    const uint64_t bits = (uint64_t)(0x43300000u | key >> 24) << 32 | (key << 8 | (uint32_t)(255 - expert));
+    return __builtin_bit_cast(double, bits);
+}
+
+__device__ __forceinline__ void order(double (&x)[kBest], int i, int j) {
+    const double a = larger(x[i], x[j]), b = smaller(x[i], x[j]);
+    x[i] = a, x[j] = b;
+}
+// Largest first: Batcher's network of 19 exchanges.
+__device__ __forceinline__ void sort(double (&x)[kBest]) {
+    order(x, 0, 1), order(x, 2, 3), order(x, 4, 5), order(x, 6, 7);
+    order(x, 0, 2), order(x, 1, 3), order(x, 4, 6), order(x, 5, 7);
+    order(x, 1, 2), order(x, 5, 6);
+    order(x, 0, 4), order(x, 1, 5), order(x, 2, 6), order(x, 3, 7);
+    order(x, 2, 4), order(x, 3, 5);
+    order(x, 1, 2), order(x, 3, 4), order(x, 5, 6);
+}
+// The best eight of two sorted lists.
+__device__ __forceinline__ void join(double (&x)[kBest], const double (&y)[kBest]) {
+#pragma unroll
+    for (int i = 0; i < kBest; ++i) x[i] = larger(x[i], y[kBest - 1 - i]);
+    order(x, 0, 4), order(x, 1, 5), order(x, 2, 6), order(x, 3, 7);
+    order(x, 0, 2), order(x, 1, 3), order(x, 4, 6), order(x, 5, 7);
+    order(x, 0, 1), order(x, 2, 3), order(x, 4, 5), order(x, 6, 7);
+}
+// With the lane that kCtrl pairs this one with.
+template <int kCtrl>
+__device__ __forceinline__ void join_lanes(double (&x)[kBest]) {
+    double y[kBest];
+#pragma unroll
+    for (int i = 0; i < kBest; ++i) {
+        const uint64_t bits = __builtin_bit_cast(uint64_t, x[i]);
+        const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)bits, kCtrl, 0xf, 0xf, true);
+        const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(bits >> 32), kCtrl, 0xf, 0xf, true);
+        y[i] = __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+    }
+    join(x, y);
+}
+
+// Where expert e is in a row of runs.
+__device__ __forceinline__ int quad_slot(int e, int32_t E) {
+    const int past = E % 4;
+    return past == 0 || e < E - past ? e : e + 4 - past;
+}
+
+template <int V, bool kHalf, bool kSigmoid, bool kBalance>
+__global__ void __launch_bounds__(kRowWaves * kWave, 4) gate_rows_kernel(GateParams p) {
+    // Sigmoid: the wavefront's rows of scores; balance: its sums; then of the
+    // workgroup, sigmoid: a row of the selection bias; balance: counts [E] and
+    // live tokens [1].
+    constexpr int kWaveFloats = (kSigmoid ? kRowTokens : 1) * V * kRowLanes;
+    extern __shared__ float lds[];
+    const int lane = threadIdx.x & (kWave - 1), c = lane % kRowLanes;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int E = p.num_experts, K = p.num_topk;
+    float* const mine = lds + wave * kWaveFloats;
+    float* const bias = lds + kRowWaves * kWaveFloats;
+    int* const counts = reinterpret_cast<int*>(bias + (kSigmoid ? V * kRowLanes : 0));
+    float prob_sum[V];
+    int live = 0;
+    if (kBalance) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) *p.ticket = 0;
+        for (int i = threadIdx.x; i < E + 1; i += kRowWaves * kWave) counts[i] = 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) prob_sum[v] = 0.f;
+    }
+    if (kSigmoid)
+        for (int e = threadIdx.x; e < E; e += kRowWaves * kWave)
+            bias[quad_slot(e, E)] = p.bias != nullptr ? p.bias[e] : 0.f;
+    if (kBalance || kSigmoid) __syncthreads();
+    const int64_t stride = (int64_t)gridDim.x * kRowWaves * kRowTokens;
+    int64_t t0 = ((int64_t)blockIdx.x * kRowWaves + wave) * kRowTokens;  // the wavefront's first token
+    constexpr int kWords = kHalf ? V / 2 : V;
+    uint32_t next[kWords];
+    int next_live = 0;
+    const auto load = [&](int64_t first) {
+        const int64_t mine_t = first + lane / kRowLanes;
+        const int64_t t = mine_t < p.num_tokens ? mine_t : p.num_tokens - 1;
+#pragma unroll
+        for (int v = 0; v < V; v += 4) {
+            const int64_t at = t * E + Quad<V>(c, v, E).first;
+            if constexpr (kHalf) {
+                const Halves4 x = *reinterpret_cast<const Halves4*>(static_cast<const uint16_t*>(p.logits) + at);
+                next[v / 2] = x.x, next[v / 2 + 1] = x.y;
+            } else {
+                const Floats4 x = *reinterpret_cast<const Floats4*>(static_cast<const uint32_t*>(p.logits) + at);
+                next[v] = x.x, next[v + 1] = x.y, next[v + 2] = x.z, next[v + 3] = x.w;
+            }
+        }
+        const int on = p.mask != nullptr ? p.mask[t] : 1;
+        next_live = mine_t < p.num_tokens ? on : 0;
+    };
+    float s[V];
+    bool taken = false;
+    // A token that is masked or past the last has no logit that counts.
+    const auto arrive = [&] {
+        taken = next_live != 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const Quad<V> quad(c, v, E);
+            const float z = !kHalf        ? __uint_as_float(next[kHalf ? 0 : v])
+                            : v % 2 == 0 ? bf16_low(next[v / 2])
+                                         : bf16_high(next[v / 2]);
+            s[v] = taken && quad.first + v % 4 >= quad.start ? z : kNone;
+        }
+    };
+    if (t0 < p.num_tokens) load(t0);
+    if (t0 < p.num_tokens) arrive();
+    for (; t0 < p.num_tokens; t0 += stride) {
+        if (t0 + stride < p.num_tokens) load(t0 + stride);
+        const bool now = taken;
+        float sum = 0.f;
+        double best[kBest], more[kBest];
+        const auto place = [&](int v, uint32_t key) {
+            (v < kBest ? best : more)[v % kBest] = numbered(key, Quad<V>(c, v, E).first + v % 4);
+        };
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            if constexpr (kSigmoid) {
+                const bool never = !(s[v] > kNone);
+                s[v] = s[v] == kNone ? 0.f : sigmoid(s[v]);
+                sum += s[v];
+                place(v, never ? kNoKey : order_key(s[v] + bias[(v / 4 * kRowLanes + c) * 4 + v % 4]));
+            } else {
+                place(v, order_key(s[v]));
+            }
+        }
+        sort(best);
+        if constexpr (V > kBest) {
+            sort(more);
+            join(best, more);
+        }
+        join_lanes<kDppQuadXor1>(best);
+        join_lanes<kDppQuadXor2>(best);
+        join_lanes<kDppRowHalfMirror>(best);
+        join_lanes<kDppRowMirror>(best);
+        const auto key_of = [](double x) { return (uint32_t)(__builtin_bit_cast(uint64_t, x) >> 8); };
+        const uint32_t top = key_of(best[0]);
+        const float high = top == kNoKey ? 0.f : key_value(top);
+        if constexpr (!kSigmoid) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                s[v] = exp_nonpositive(s[v] - high);
+                sum += s[v];
+            }
+        }
+        sum = row_sum(sum);
+        const RowSum all{sum, sum == 0.f ? 0.f : (kSigmoid ? 1.f / sum : reciprocal(sum))};
+        // Lane c of the token's 16 takes entry c.
+        double entry = best[0];
+#pragma unroll
+        for (int k = 1; k < kBest; ++k) entry = c == k ? best[k] : entry;
+        const uint32_t key = key_of(entry);
+        const int expert = 255 - (int)((uint32_t)__builtin_bit_cast(uint64_t, entry) & 0xff);
+        const int picked = c < K && key != kNoKey ? expert : -1;
+        float weight = 0.f;
+        if constexpr (kSigmoid) {
+            float* const row = mine + lane / kRowLanes * V * kRowLanes;
+#pragma unroll
+            for (int v = 0; v < V; ++v) row[(v / 4 * kRowLanes + c) * 4 + v % 4] = s[v];
+            __builtin_amdgcn_wave_barrier();
+            if (picked >= 0) weight = row[quad_slot(picked, E)];
+            __builtin_amdgcn_wave_barrier();
+        } else {
+            weight = picked >= 0 ? exp_nonpositive(key_value(key) - high) * all.inv : 0.f;
+        }
+        if (p.flags & DISPATCH_GATE_NORMALIZE) {
+            const float total = row_sum(weight);
+            weight = total == 0.f ? 0.f
+                     : kSigmoid   ? p.route_scale * weight / total
+                                  : p.route_scale * weight * reciprocal(total);
+        } else {
+            weight *= p.route_scale;
+        }
+        if (kBalance) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) prob_sum[v] += kSigmoid ? all.share(s[v]) : s[v] * all.inv;
+            live += now && c == 0 ? 1 : 0;
+            if (picked >= 0) atomicAdd(counts + picked, 1);
+        }
+        if (t0 + stride < p.num_tokens) arrive();
+        const int64_t t = t0 + lane / kRowLanes;
+        if (c < K && t < p.num_tokens) {
+            const int64_t at = t * K + c;
+            if (p.idx_bytes == 8)
+                static_cast<int64_t*>(p.topk_idx)[at] = picked;
+            else
+                static_cast<int32_t*>(p.topk_idx)[at] = picked;
+            p.topk_weights[at] = weight;
+        }
+    }
+    if (!kBalance) return;
+    // The wavefront's four rows, then as above.
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        prob_sum[v] += __shfl_xor(prob_sum[v], 16);
+        prob_sum[v] += __shfl_xor(prob_sum[v], 32);
+        if (lane < kRowLanes) mine[(v / 4 * kRowLanes + c) * 4 + v % 4] = prob_sum[v];
+    }
+    if (c == 0) atomicAdd(counts + E, live);
+    __syncthreads();
+    float* const out = p.partial + (int64_t)blockIdx.x * (2 * E + 1);
+    for (int i = threadIdx.x; i < 2 * E + 1; i += kRowWaves * kWave) {
+        float x = __int_as_float(counts[i - E < 0 ? 0 : i - E]);
+        if (i < E) {
+            const float* at = lds + quad_slot(i, E);
+            x = at[0];
+#pragma unroll
+            for (int w = 1; w < kRowWaves; ++w) x += at[w * kWaveFloats];
+        }
+        out[i] = x;
+    }
+}
+
 // Adds the partial rows. A workgroup takes 16 experts: its 64 groups of 16
 // threads add every 64th row, then the groups are added in order. Its part of
 // the loss goes to the workspace, and the workgroup that finds itself the last
@@ -668,6 +927,19 @@ template <int V>
 const void* gate_kernel_of(bool half, bool sigmoid, bool balance) {
     return half ? gate_kernel_of<V, true>(sigmoid, balance) : gate_kernel_of<V, false>(sigmoid, balance);
 }
+template <int V, bool kHalf>
+const void* gate_rows_of(bool sigmoid, bool balance) {
+    if (sigmoid)
+        return balance ? (const void*)&gate_rows_kernel<V, kHalf, true, true>
+                       : (const void*)&gate_rows_kernel<V, kHalf, true, false>;
+    return balance ? (const void*)&gate_rows_kernel<V, kHalf, false, true>
+                   : (const void*)&gate_rows_kernel<V, kHalf, false, false>;
+}
+template <int V>
+const void* gate_rows_of(bool half, bool sigmoid, bool balance) {
+    return half ? gate_rows_of<V, true>(sigmoid, balance) : gate_rows_of<V, false>(sigmoid, balance);
+}
+
 template <int V>
 const void* gate_backward_of(bool half, bool sigmoid) {
     if (half)
@@ -710,24 +982,37 @@ hipError_t launch_gate(const dispatch_gate_problem_t& prob, const void* logits, 
     const bool sig = prob.scoring == DISPATCH_GATE_SIGMOID, half = prob.logits_bytes == 2;
     const bool balance = out.loss != nullptr;
     if (prob.num_tokens == 0 && !balance) return hipSuccess;
+    const void* kernel;
+    // Wavefronts of a workgroup, their tokens, the floats in LDS of each and of all.
+    int waves, per_wave, row, extra = 0;
+    if (E > 64 && E <= 256 && prob.num_topk >= kFewestRounds && prob.num_topk <= kBest &&
+        prob.num_tokens >= kManyTokens) {
+        waves = kRowWaves, per_wave = kRowTokens;
+        const int v = E <= 128 ? 8 : 16;
+        kernel = v == 8 ? gate_rows_of<8>(half, sig, balance) : gate_rows_of<16>(half, sig, balance);
+        row = (sig ? kRowTokens : 1) * v * kRowLanes;
+        extra = sig ? v * kRowLanes : 0;
+    } else {
+        per_wave = 1;
 #define DISPATCH_F(V) gate_kernel_of<V>(half, sig, balance)
-    const void* kernel = DISPATCH_GATE_BY_V(E, DISPATCH_F);
+        kernel = DISPATCH_GATE_BY_V(E, DISPATCH_F);
 #undef DISPATCH_F
 #define DISPATCH_F(V) kGateWaves<V>
-    int waves = DISPATCH_GATE_BY_V(E, DISPATCH_F);
+        waves = DISPATCH_GATE_BY_V(E, DISPATCH_F);
 #undef DISPATCH_F
-    // Small workgroups start sooner and spread over more CUs (16 or 1000
-    // tokens: 4.7 and 4.5 us, 6.1 and 5.8 with 16 wavefronts); with balance
-    // outputs each workgroup leaves a partial row, so there they are large.
-    if (!balance) waves = 4;
+#define DISPATCH_F(V) (V * kWave)
+        row = DISPATCH_GATE_BY_V(E, DISPATCH_F);
+#undef DISPATCH_F
+        // Small workgroups start sooner and spread over more CUs (16 or 1000
+        // tokens: 4.7 and 4.5 us, 6.1 and 5.8 with 16 wavefronts); with balance
+        // outputs each workgroup leaves a partial row, so there they are large.
+        if (!balance) waves = 4;
+    }
     // Without balance outputs nothing crosses workgroups and the grid may be
     // as large as the batch.
-    const int64_t all = (prob.num_tokens + waves - 1) / waves;
-    const int groups = balance ? gate_groups(prob.num_tokens, waves) : (int)(all < 65536 ? all : 65536);
-#define DISPATCH_F(V) (V * kWave)
-    const int row = DISPATCH_GATE_BY_V(E, DISPATCH_F);
-#undef DISPATCH_F
-    const size_t shared = ((size_t)waves * row + (balance ? E + 1 : 0)) * sizeof(float);
+    const int64_t all = (prob.num_tokens + waves * per_wave - 1) / (waves * per_wave);
+    const int groups = balance ? gate_groups(prob.num_tokens, waves * per_wave) : (int)(all < 65536 ? all : 65536);
+    const size_t shared = ((size_t)waves * row + extra + (balance ? E + 1 : 0)) * sizeof(float);
     void* args[] = {&p};
     hipError_t err = hipLaunchKernel(kernel, dim3(groups), dim3(waves * kWave), args, shared, stream);
     if (err != hipSuccess || !balance) return err;

@@ -32,6 +32,12 @@ __device__ __forceinline__ uint32_t pack_fp8(float a, float b, float c, float d)
 // row's last lane into the following rows.
 constexpr int kDppRowShr = 0x110;
 constexpr int kDppRowRor = 0x120;
+// (also: a lane's neighbour and next but one in its four, its mirror image in
+// its eight and in its row.)
+constexpr int kDppQuadXor1 = 0xb1;
+constexpr int kDppQuadXor2 = 0x4e;
+constexpr int kDppRowHalfMirror = 0x141;
+constexpr int kDppRowMirror = 0x140;
 constexpr int kDppBcast15 = 0x142;
 constexpr int kDppBcast31 = 0x143;
 
@@ -50,6 +56,16 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v) {
     v = v > o ? v : o;
     o = dpp_ror<kDppRowRor + 8>(v);
     return v > o ? v : o;
+}
+
+// Sum of the 16 lanes of a row, in every lane of the row: the same bits, as
+// each step adds a pair of sums that both its lanes have.
+__device__ __forceinline__ float row_sum(float v) {
+    v += __uint_as_float(dpp_ror<kDppRowRor + 8>(__float_as_uint(v)));
+    v += __uint_as_float(dpp_ror<kDppRowRor + 4>(__float_as_uint(v)));
+    v += __uint_as_float(dpp_ror<kDppRowRor + 2>(__float_as_uint(v)));
+    v += __uint_as_float(dpp_ror<kDppRowRor + 1>(__float_as_uint(v)));
+    return v;
 }
 
 // One block's 8 channels of a lane: quantised to dst, the scale by lane 0.

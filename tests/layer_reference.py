@@ -50,6 +50,35 @@ def gate(z, topk, sigmoid, normalize, scale, coef, bias=None, mask=None):
     return dict(idx=idx, weights=weights, prob_sum=prob_sum, count=count, live=n, loss=loss, order=order)
 
 
+def gate_table(z, topk, sigmoid, normalize, scale, coef, bias=None, mask=None):
+    """gate() for many tokens at once: a stable sort in place of a loop over them."""
+    z = z.double()
+    t, e = z.shape
+    live = torch.ones(t, dtype=torch.bool) if mask is None else mask.bool()
+    nothing = torch.isneginf(z)
+    if sigmoid:
+        score = torch.where(nothing, 0.0, torch.sigmoid(z))
+        order = torch.where(nothing, -math.inf, score + (0.0 if bias is None else bias.double()))
+    else:
+        score = torch.where(nothing.all(1, keepdim=True), 0.0, torch.softmax(z, dim=1))
+        order = z.clone()
+    order = torch.where(torch.isnan(order), -math.inf, order)
+    best, idx = (x[:, :topk] for x in torch.sort(order, dim=1, descending=True, stable=True))
+    idx = torch.where(torch.isneginf(best) | ~live[:, None], -1, idx)
+    picked = torch.where(idx >= 0, score.gather(1, idx.clamp_min(0)), 0.0)
+    total = picked.sum(1, keepdim=True)
+    weights = scale * picked
+    if normalize:
+        weights = torch.where(total == 0, 0.0, weights / torch.where(total == 0, 1.0, total))
+    denom = score.sum(1, keepdim=True)
+    share = torch.where(denom == 0, 0.0, score / torch.where(denom == 0, 1.0, denom))
+    n = int(live.sum())
+    prob_sum = share[live].sum(0)
+    count = torch.bincount(idx[idx >= 0], minlength=e)
+    loss = coef * e / (topk * n * n) * float((count.double() * prob_sum).sum()) if n else 0.0
+    return dict(idx=idx, weights=weights, prob_sum=prob_sum, count=count, live=n, loss=loss, order=order)
+
+
 def gate_gradient(z, idx, count, sigmoid, normalize, scale, coef, dw, dloss, mask=None):
     """By automatic differentiation of the definition, the choice and the counts fixed."""
     z = z.double().clone().requires_grad_(True)

@@ -8,8 +8,10 @@ import shutil
 import subprocess
 
 import pytest
+import torch
 
 import moe_token_dispatch_amd as M
+from tests import layer_reference as R
 from tests.test_abi import _defines
 
 B = ctypes.byref
@@ -192,3 +194,21 @@ def test_struct_layouts_from_c(tmp_path):
     assert build.returncode == 0, build.stderr
     got = subprocess.run([exe], capture_output=True, text=True, timeout=60)
     assert [int(v) for v in got.stdout.split()] == want
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_references_of_the_gate_agree(sigmoid):
+    g = torch.Generator().manual_seed(1)
+    z = torch.randint(-3, 4, (40, 21), generator=g).float()
+    z[0] = -math.inf
+    z[1, 2:] = -math.inf
+    z[2, 3] = math.nan
+    mask = torch.rand((40,), generator=g) > 0.2
+    bias = torch.randn((21,), generator=g) if sigmoid else None
+    z2 = z.clone()
+    z2[2, 3] = 0.0  # (NaN shows in sums: the choice alone is compared with it)
+    for x, names in ((z, ("idx", "count")), (z2, ("idx", "weights", "prob_sum", "count", "live", "loss", "order"))):
+        a = R.gate(x, 4, sigmoid, True, 1.5, 0.1, bias, mask)
+        b = R.gate_table(x, 4, sigmoid, True, 1.5, 0.1, bias, mask)
+        for name in names:
+            assert torch.equal(torch.as_tensor(a[name]), torch.as_tensor(b[name])), name

@@ -338,3 +338,80 @@ def test_odd_expert_counts_at_any_alignment(sigmoid, dtype, e):
     size = 2.0 * dw.abs().amax() + want.abs().amax()
     got = grad[1:-1].view(t, e)
     assert torch.all((got - want).abs() <= rel * want.abs() + 8 * REL * size), (got - want).abs().max()
+
+
+def _many(t, e, k, dtype, sigmoid, seed, ties=False):
+    g = torch.Generator().manual_seed(seed)
+    z = torch.randint(-3, 4, (t, e), generator=g).to(dtype) if ties else _logits(t, e, dtype, seed)
+    z[1] = -math.inf                      # nothing to take
+    z[2, 3:] = -math.inf                  # three of k
+    z[3, : e - 1] = -math.inf             # the last alone
+    z[4] = 0.0                            # all equal
+    z[4, ::2] = -0.0
+    z[t - 1] = torch.arange(e).to(dtype) / 16
+    mask = torch.rand((t,), generator=g) > 0.1
+    mask[:5] = True
+    mask[t - 1] = True
+    return z, mask
+
+
+@pytest.mark.parametrize("e,k", [(65, 4), (66, 8), (67, 5), (97, 8), (128, 8), (129, 6), (130, 8), (191, 7), (255, 8), (256, 8)])
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_many_tokens(e, k, sigmoid, dtype, monkeypatch):
+    monkeypatch.setattr(R, "gate", R.gate_table)
+    t = 8192 + e  # not a multiple of a wavefront's or a workgroup's tokens
+    z, mask = _many(t, e, k, dtype, sigmoid, e, ties=True)
+    # (The last row's largest sigmoids are equal in fp32, though not in fp64.)
+    _, out, _ = _check(z, k, sigmoid, scale=2.5, mask=mask, exact_choice=not sigmoid)
+    if sigmoid:
+        fp32 = 1.0 / (1.0 + torch.exp(-z.to(DEV).float()))
+        want = torch.sort(fp32, dim=1, descending=True, stable=True).indices[:, :k]
+        rows = mask.to(DEV)
+        rows[:4] = False  # (rows with fewer than k to take)
+        assert torch.equal(out.topk_idx[rows], want[rows])
+    z, mask = _many(t, e, k, dtype, sigmoid, e + 1)
+    bias = torch.randn((e,), generator=torch.Generator().manual_seed(e)) if sigmoid else None
+    _check(z, k, sigmoid, normalize=False, mask=mask, bias=bias, idx_bytes=4, exact_choice=not sigmoid)
+
+
+@pytest.mark.parametrize("t", [8191, 8192, 8195, 65539])
+def test_many_tokens_at_any_alignment(t):
+    """The choice on both sides of the change of form and past one pass, from rows at odd addresses; without balance alike."""
+    e, k = 129, 8
+    z, mask = _many(t, e, k, torch.bfloat16, False, t, ties=True)
+    flat = torch.full((t * e + 2,), math.nan, dtype=torch.bfloat16, device=DEV)
+    rows = flat[1:-1].view(t, e)
+    rows.copy_(z)
+    p = M.make_gate_problem(t, e, k, M.GATE_SOFTMAX, torch.bfloat16, True, 1.0, 0.5, 8)
+    ref = R.gate_table(z, k, False, True, 1.0, 0.5, None, mask)
+    tables = []
+    for balance in (True, False, True):
+        out = M.alloc_gate(p, DEV, balance=balance)
+        M.dispatch_gate(p, rows, out, M.alloc_gate_workspace(p, DEV), token_mask=mask.to(DEV))
+        torch.cuda.synchronize()
+        assert torch.equal(out.topk_idx.cpu().long(), ref["idx"])
+        if balance:
+            assert torch.equal(out.expert_count.cpu().long(), ref["count"]) and int(out.live_tokens) == ref["live"]
+        tables.append(out)
+    assert torch.equal(tables[0].topk_weights, tables[1].topk_weights)
+    for name in ("topk_weights", "prob_sum", "loss"):
+        assert torch.equal(getattr(tables[0], name), getattr(tables[2], name))  # bit for bit
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_many_tokens_nan_and_infinity(sigmoid):
+    t, e, k = 8200, 200, 8
+    z, _ = _many(t, e, k, torch.float32, sigmoid, 11)
+    z[10, 5] = math.nan
+    z[11] = math.nan
+    z[12, 7] = math.inf
+    few, many = z[:64].contiguous(), z
+    _, a = _run(few, k, sigmoid)
+    _, b = _run(many, k, sigmoid)
+    # The same choice as in the form of few tokens; NaN shows in the same places.
+    assert torch.equal(a.topk_idx, b.topk_idx[:64])
+    wa, wb = a.topk_weights, b.topk_weights[:64]
+    assert torch.equal(torch.isnan(wa), torch.isnan(wb))
+    assert torch.all(((wa - wb).abs() <= REL * wa.abs()) | torch.isnan(wa))
+    assert not torch.any(b.topk_idx[10] == 5) and torch.all(b.topk_idx[11] == -1)
