@@ -608,12 +608,14 @@ struct ProductPlan {
 constexpr int kMaxParts = 16;
 
 template <class Shape>
-ProductPlan plan_product(int64_t max_rows, int32_t num_experts, int32_t N, int32_t k_blocks) {
+ProductPlan plan_product(int64_t max_rows, int32_t num_experts, int32_t N, int32_t k_blocks, bool workspace) {
     ProductPlan s;
     s.tiles = most_row_tiles(max_rows, num_experts, Shape::kTokens) * ((N + 255) / 256);
     // As many parts as fill the CUs, each left with four blocks of K or more.
+    // (Not of tiles of 128 tokens and more: their sums take the workgroup that
+    // adds them 30 us a MB, and smaller tiles were faster in all of 28 problems.)
     const int64_t want = kCus / (s.tiles < 1 ? 1 : s.tiles);
-    const int64_t most = k_blocks / 4;
+    const int64_t most = workspace && Shape::kTokens <= 64 ? k_blocks / 4 : 1;
     const int64_t parts = want < most ? want : most;
     s.parts = (int)(parts < 1 ? 1 : (parts > kMaxParts ? kMaxParts : parts));
     s.bytes = s.parts == 1 ? 0 : kTicketBytes + (size_t)(s.tiles * s.parts) * Shape::kSumFloats * sizeof(float);
@@ -623,8 +625,7 @@ ProductPlan plan_product(int64_t max_rows, int32_t num_experts, int32_t N, int32
 template <class Shape, bool kSwiglu>
 hipError_t launch_product(ProductParams p, int64_t max_rows, void* workspace, hipStream_t stream) {
     p.n_tiles = (p.N + 255) / 256;
-    ProductPlan plan = plan_product<Shape>(max_rows, p.num_experts, p.N, p.k_blocks);
-    if (workspace == nullptr) plan.parts = 1;
+    const ProductPlan plan = plan_product<Shape>(max_rows, p.num_experts, p.N, p.k_blocks, workspace != nullptr);
     p.parts = plan.parts;
     p.slots = plan.parts == 1 ? 0 : (int32_t)(plan.tiles * plan.parts);
     p.tickets = static_cast<uint32_t*>(workspace);
@@ -645,43 +646,84 @@ using Shape128 = TileShape<128, 2, 3>;
 using Shape192 = TileShape<192, 2, 2>;
 using Shape256 = TileShape<256, 2, 2>;
 
-// Few rows: the shape by the mean of the rows that an expert gets at most.
-// With fewer tokens per tile more experts need two tiles, which read the
-// weights twice (from L2) and take turns on the CUs; with more, a tile's empty
-// fragments cost their part of the ring. Measured with 32 experts, us of 2048
-// -> 7168 channels at mean 4, 8, 16, 32, 48, 64, 96 rows:
-//    16 tokens   87   91  103  140  178  217  288
-//    32          90   88   93  107  133  147  193
-//    64          89   90   92   96  104  124  141
-//   128          93   93   97  100  106  111  123
-// (7168 -> 4096 channels change over at the same means, give or take one).
+// The shape whose tiles take least time by this estimate: rounds of tiles over
+// the CUs, each with its blocks of K and what a tile costs beside them
+// (beginning, epilogue, its output), and the sums of tiles that share their K.
+// The times are measured ones, us, of the full chip. An expert has about half
+// a tile more than its rows fill, fewer where its count (give or take its root)
+// fits a few tiles. Weights' bytes cost all shapes alike and are left out.
 //
-// Many rows: the shape whose rounds of tiles over the CUs cost least. A round
-// of 128- or 192-token tiles takes 0.66 or 0.86 of one of 256 tokens. An expert
-// has about half a tile more than its rows fill, or one tile if it is well
-// above the mean. Measured, us with 128, 192, 256 tokens (rows of 4096
-// channels, 8 experts, 4096 channels out): 4096 rows 117, 99, 121; 6000 rows
-// 153, 147, 124; 8191 rows 196, 156, 179; 12000 rows 260, 236, 224; the rule
-// took the fastest of the three in 12 of 12 such cases, 2 to 32 experts.
+// Measured over 28 problems of 1 to 60 experts, 19 to 18847 rows, 272 to 8192 x 336
+// to 8192 channels: the choice is within 8 % of the fastest shape each time (a rule
+// by the mean of rows alone took up to 3.6 times that). Some of them, us by
+// tokens of a tile:
+//                                        16    32    64   128   192   256
+//   836 rows on 3, 2656 -> 336           13    12    14    27    31    38
+//   2000 rows on 8, 1024 -> 1024         21    17    11    14    15    19
+//   6175 rows on 45, 1856 -> 1536       143    89    62    55    65    67
+//   4096 rows on 8, 1024 -> 4096        128    77    52    44    39    44
+//   2562 rows on 6, 1280 -> 5376        115    73    51    36    42    30
+// and where the weights' bytes bound it, 32 experts, 2048 -> 7168, at mean 4, 16, 32
+// and 64 rows: 16 tokens 87, 103, 140, 217; 32: 90, 93, 107, 147; 64: 89, 92, 96, 124; 128:
+// 93, 97, 100, 111.
+struct TileTimes {
+    double tile, block;
+};
+constexpr TileTimes tile_times(int tokens) {
+    switch (tokens) {
+        case 16: return {3.1, 0.60};
+        case 32: return {4.7, 0.65};
+        case 64: return {5.7, 0.76};
+        case 128: return {7.7, 1.12};
+        case 192: return {9.9, 1.46};
+        default: return {11.0, 1.70};
+    }
+}
+
 template <class Shape>
-double rounds_cost(int64_t max_rows, int32_t num_experts, int32_t N, double round) {
-    const double fill = (double)max_rows / num_experts / Shape::kTokens;
-    const double per_expert = num_experts == 1 ? std::ceil(fill) : (fill <= 0.85 ? 1.0 : fill + 0.5);
-    return std::ceil(per_expert * num_experts * ((N + 255) / 256) / kCus) * round;
+double product_time(int64_t max_rows, int32_t num_experts, int32_t N, int32_t k_blocks, bool workspace) {
+    const ProductPlan plan = plan_product<Shape>(max_rows, num_experts, N, k_blocks, workspace);
+    const double experts = max_rows < num_experts ? (double)max_rows : (double)num_experts;
+    const double mean = max_rows / experts, fill = mean / Shape::kTokens;
+    double per_expert = fill + 0.5;
+    if (num_experts == 1) {
+        per_expert = std::ceil(fill);
+    } else if (fill < 3) {
+        const double spread = std::sqrt(mean) / Shape::kTokens;
+        const double around = (std::ceil(fill - spread) + std::ceil(fill + spread)) / 2;
+        per_expert = around < per_expert ? around : per_expert;
+        per_expert = per_expert < 1 ? 1 : per_expert;
+    }
+    const double tiles = per_expert * experts * ((N + 255) / 256);
+    constexpr TileTimes times = tile_times(Shape::kTokens);
+    double us = std::ceil(tiles * plan.parts / kCus) * (times.tile + times.block * k_blocks / plan.parts);
+    if (plan.parts > 1) {
+        // The last workgroup's reading, and everybody's writing and reading.
+        const double kb = plan.parts * Shape::kSumFloats * 4e-3;
+        us += 2.5 + 0.012 * kb + tiles * kb * 2 / 5.2e3;
+    }
+    return us;
 }
 
 template <class F>
-auto with_shape(int64_t max_rows, int32_t num_experts, int32_t N, F f) {
-    const int64_t mean = max_rows / num_experts;
-    if (mean <= 5) return f(Shape16{});
-    if (mean <= 13) return f(Shape32{});
-    if (mean <= 45) return f(Shape64{});
-    const double c128 = rounds_cost<Shape128>(max_rows, num_experts, N, 0.66);
-    const double c192 = rounds_cost<Shape192>(max_rows, num_experts, N, 0.86);
-    const double c256 = rounds_cost<Shape256>(max_rows, num_experts, N, 1.0);
-    if (c128 < c192 && c128 < c256) return f(Shape128{});
-    if (c192 < c256) return f(Shape192{});
-    return f(Shape256{});
+auto with_shape(int64_t max_rows, int32_t num_experts, int32_t N, int32_t k_blocks, bool workspace, F f) {
+    if (max_rows <= 0) return f(Shape16{});
+    const auto time = [&](auto shape) {
+        return product_time<decltype(shape)>(max_rows, num_experts, N, k_blocks, workspace);
+    };
+    const double us[] = {time(Shape16{}),  time(Shape32{}),  time(Shape64{}),
+                         time(Shape128{}), time(Shape192{}), time(Shape256{})};
+    int best = 0;
+    for (int i = 1; i < 6; ++i)
+        if (us[i] < us[best]) best = i;
+    switch (best) {
+        case 0: return f(Shape16{});
+        case 1: return f(Shape32{});
+        case 2: return f(Shape64{});
+        case 3: return f(Shape128{});
+        case 4: return f(Shape192{});
+        default: return f(Shape256{});
+    }
 }
 
 int64_t most_rows(const dispatch_expert_problem_t& p) {
@@ -692,10 +734,9 @@ int64_t most_rows(const dispatch_expert_problem_t& p) {
 
 size_t expert_workspace_bytes(const dispatch_expert_problem_t& prob) {
     const int64_t max_rows = most_rows(prob);
-    return with_shape(max_rows, prob.num_experts, (int32_t)prob.out_features, [&](auto shape) {
-        return plan_product<decltype(shape)>(max_rows, prob.num_experts, (int32_t)prob.out_features,
-                                             (int32_t)((prob.in_features + 127) / 128))
-            .bytes;
+    const int32_t N = (int32_t)prob.out_features, k_blocks = (int32_t)((prob.in_features + 127) / 128);
+    return with_shape(max_rows, prob.num_experts, N, k_blocks, true, [&](auto shape) {
+        return plan_product<decltype(shape)>(max_rows, prob.num_experts, N, k_blocks, true).bytes;
     });
 }
 
@@ -720,7 +761,7 @@ hipError_t launch_expert_product(const dispatch_expert_problem_t& prob, const in
     p.k_blocks = (p.K + 127) / 128;
     p.n_blocks = (p.N + 127) / 128;
     const int64_t max_rows = most_rows(prob);
-    return with_shape(max_rows, prob.num_experts, p.N, [&](auto shape) {
+    return with_shape(max_rows, prob.num_experts, p.N, p.k_blocks, workspace != nullptr, [&](auto shape) {
         using Shape = decltype(shape);
         return out_sf != nullptr ? launch_product<Shape, true>(p, max_rows, workspace, stream)
                                  : launch_product<Shape, false>(p, max_rows, workspace, stream);

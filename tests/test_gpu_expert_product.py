@@ -145,7 +145,7 @@ def test_any_row_bound_gives_the_same_rows(max_rows):
     _check_swiglu(s, *_run_swiglu(s, max_rows))
 
 
-# Announced rows that take the tiles of 16, 32, 64, 128, 192 and 256 tokens.
+# Announced rows from few to many.
 @pytest.mark.parametrize("announced", [8, 20, 60, 200, 20000, 28000])
 @pytest.mark.parametrize("counts", [[700, 129], [1, 255]], ids=str)
 def test_every_tile_shape(announced, counts):
@@ -330,3 +330,41 @@ def test_binding_refuses_wrong_tensors():
     q, sf = torch.zeros((s["rows"], 64), dtype=R.FP8, device=DEV), torch.zeros((s["rows"], 1), device=DEV)
     with pytest.raises(ValueError, match="out_q"):
         M.dispatch_expert_product_swiglu(p, *ins, q, sf)
+
+
+# Announced rows for which two or three experts with 512 output channels take
+# tiles of 16, 32, 64, 128, 192 and 256 tokens.
+@pytest.mark.parametrize("announced", [200, 4000, 8000, 12000, 20000, 28000])
+@pytest.mark.parametrize("counts,k,n", [([300, 1], 16, 512), ([257, 15, 64], 400, 512), ([0, 513], 144, 264),
+                                        ([1, 0, 2], 1040, 512), ([130, 65, 193], 128, 512), ([17, 33], 272, 504)], ids=str)
+def test_rows_in_every_tile(announced, counts, k, n):
+    s = _problem(counts, k, n, 1, announced + k, tail=28000)
+    _check_product(s, _run_product(s, announced))
+    if n % 256 == 0:
+        _check_swiglu(s, *_run_swiglu(s, announced))
+
+
+# The same for shared tiles: of 16, 32 and 64 tokens.
+@pytest.mark.parametrize("announced", [100, 800, 2500])
+@pytest.mark.parametrize("counts", [[3, 0], [130, 70], [1, 65, 17]], ids=str)
+def test_shared_tiles_of_every_size(announced, counts):
+    s = _problem(counts, 5008, 512, 1, announced, tail=2500)
+    e, n, k = s["w"].shape
+    p = M.make_expert_problem(e, k, n, s["rows"], announced)
+    ws = M.alloc_expert_workspace(p, DEV)
+    assert ws is not None
+    ins = _dev(s, "psum_t", "count_t", "x", "x_sf", "w", "w_sf")
+    first = None
+    for _ in range(3):
+        out = torch.full((s["rows"], 2 * n), CANARY, dtype=torch.uint8, device=DEV).view(torch.bfloat16)
+        M.dispatch_expert_product(p, *ins, out, ws)
+        q = torch.full((s["rows"], n // 2), CANARY, dtype=torch.uint8, device=DEV)
+        sf = torch.full((s["rows"], n // 256), -7.0, device=DEV)
+        M.dispatch_expert_product_swiglu(p, *ins, q, sf, ws)
+        torch.cuda.synchronize()
+        got = [out.cpu(), q.cpu(), sf.cpu()]
+        if first is None:
+            _check_product(s, got[0])
+            _check_swiglu(s, *got[1:])
+            first = got
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(first, got))
