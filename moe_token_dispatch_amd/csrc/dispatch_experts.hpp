@@ -14,11 +14,14 @@ constexpr int kGateMaxGroups = 512;  // workgroups of a gate forward with balanc
 // Workgroups of a gate forward with balance outputs: each leaves one partial
 // row of E probability sums, E counts and its live tokens.
 inline int gate_groups(int64_t num_tokens, int waves) {
+    // One workgroup up to two tokens per wavefront: it needs no second kernel
+    // (256 experts: 16 tokens 6.2 us, 32 8.9, against 11.3; 48 would take 11.8).
     // One token per wavefront up to 256 workgroups, one per CU; a second one
     // per CU (better hidden latencies, but twice the partial rows) where each
     // wavefront still gets two tokens.
+    if (num_tokens <= 2 * waves) return 1;
     const int64_t g = (num_tokens + waves - 1) / waves;
-    if (g <= kGateMaxGroups / 2) return g < 1 ? 1 : (int)g;
+    if (g <= kGateMaxGroups / 2) return (int)g;
     return g < 2 * kGateMaxGroups ? kGateMaxGroups / 2 : kGateMaxGroups;
 }
 inline size_t gate_partial_words(int32_t num_experts) { return 2 * (size_t)num_experts + 1; }

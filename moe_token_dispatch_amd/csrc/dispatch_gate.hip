@@ -48,6 +48,11 @@ struct GateParams {
     float* topk_weights;
     float* partial;    // [groups][2E + 1]: prob sums, counts and live tokens (as integer bits)
     uint32_t* ticket;  // cleared here for the kernel that adds the partial rows
+    int32_t* expert_count;  // these by a lone workgroup
+    float* prob_sum;
+    int32_t* live_tokens;
+    float* loss;
+    float loss_coef;
     int64_t num_tokens;
     int32_t num_experts;
     int32_t num_topk;
@@ -303,6 +308,11 @@ struct Pairs {
     }
 };
 
+// From the sum of counts times probability sums.
+__device__ __forceinline__ float balance_loss(float coef, int E, int K, int live, double sum) {
+    return live == 0 ? 0.f : (float)((double)coef * E / ((double)K * live * live) * sum);
+}
+
 template <int V, bool kHalf, bool kSigmoid, bool kBalance>
 __global__ void __launch_bounds__(kGateWaves<V> * kWave) gate_kernel(GateParams p) {
     // A row of scores per wavefront, then with kBalance the workgroup's
@@ -419,6 +429,30 @@ __global__ void __launch_bounds__(kGateWaves<V> * kWave) gate_kernel(GateParams 
     write_slots<V>(score_row, lane, prob_sum);
     if (lane == 0) atomicAdd(counts + E, live);
     __syncthreads();
+    if (gridDim.x == 1) {
+        // A lone workgroup has it all.
+        double part = 0.0;
+        for (int i = threadIdx.x; i < E; i += W * kWave) {
+            const float* at = lds + slot_of<V>(i, E);
+            float x = at[0];
+#pragma unroll
+            for (int w = 1; w < kGateWaves<V>; ++w) x += at[w * V * kWave];
+            p.prob_sum[i] = x;
+            p.expert_count[i] = counts[i];
+            part += (double)counts[i] * (double)x;
+        }
+        for (int step = kWave / 2; step > 0; step /= 2) part += __shfl_xor(part, step);
+        __syncthreads();
+        double* const parts = reinterpret_cast<double*>(lds);
+        if (lane == 0) parts[wave] = part;
+        __syncthreads();
+        if (threadIdx.x != 0) return;
+        for (int w = 1; w < W; ++w) part += parts[w];
+        const int n = counts[E];
+        *p.live_tokens = n;
+        *p.loss = balance_loss(p.loss_coef, E, K, n, part);
+        return;
+    }
     float* const out = p.partial + (int64_t)blockIdx.x * (2 * E + 1);
     for (int i = threadIdx.x; i < 2 * E + 1; i += W * kWave) {
         float x = __int_as_float(counts[i - E < 0 ? 0 : i - E]);
@@ -778,7 +812,7 @@ gate_sum_kernel(const float* partial, int groups, int E, int K, float loss_coef,
     for (unsigned i = 0; i < gridDim.x; ++i)
         total += __hip_atomic_load(loss_part + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     *live_tokens = live;
-    *loss = live == 0 ? 0.f : (float)((double)loss_coef * E / ((double)K * live * live) * total);
+    *loss = balance_loss(loss_coef, E, K, live, total);
 }
 
 struct GateBackwardParams {
@@ -969,6 +1003,11 @@ hipError_t launch_gate(const dispatch_gate_problem_t& prob, const void* logits, 
     p.mask = token_mask;
     p.topk_idx = out.topk_idx;
     p.topk_weights = out.topk_weights;
+    p.expert_count = out.expert_count;
+    p.prob_sum = out.prob_sum;
+    p.live_tokens = out.live_tokens;
+    p.loss = out.loss;
+    p.loss_coef = prob.loss_coef;
     const GateWorkspace ws = gate_workspace(E);
     uint8_t* const base = static_cast<uint8_t*>(workspace);
     p.partial = reinterpret_cast<float*>(base);
@@ -1015,7 +1054,7 @@ hipError_t launch_gate(const dispatch_gate_problem_t& prob, const void* logits, 
     const size_t shared = ((size_t)waves * row + extra + (balance ? E + 1 : 0)) * sizeof(float);
     void* args[] = {&p};
     hipError_t err = hipLaunchKernel(kernel, dim3(groups), dim3(waves * kWave), args, shared, stream);
-    if (err != hipSuccess || !balance) return err;
+    if (err != hipSuccess || !balance || groups == 1) return err;
     const float* partial = p.partial;
     int n = groups, k = prob.num_topk, e = E;
     float coef = prob.loss_coef;

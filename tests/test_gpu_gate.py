@@ -415,3 +415,11 @@ def test_many_tokens_nan_and_infinity(sigmoid):
     assert torch.equal(torch.isnan(wa), torch.isnan(wb))
     assert torch.all(((wa - wb).abs() <= REL * wa.abs()) | torch.isnan(wa))
     assert not torch.any(b.topk_idx[10] == 5) and torch.all(b.topk_idx[11] == -1)
+
+
+@pytest.mark.parametrize("e", [7, 65, 256, 600, 2049])
+@pytest.mark.parametrize("t", [1, 2, 8, 9, 16, 17, 31, 32, 33, 64, 65])
+def test_balance_of_few_tokens(t, e):
+    """Either side of the batches that one workgroup finishes alone."""
+    mask = torch.rand((t,), generator=torch.Generator().manual_seed(t)) > 0.3
+    _check(_logits(t, e, torch.float32, t + e), min(e, 8), False, mask=mask, coef=0.5)
