@@ -801,16 +801,21 @@ gate_sum_kernel(const float* partial, int groups, int E, int K, float loss_coef,
         mine = (double)n * (double)s;
     }
     for (int step = kSumExperts / 2; step > 0; step /= 2) mine += __shfl_xor(mine, step);
-    if (threadIdx.x != 0) return;
     // The part goes past the caches that XCDs do not share, and has arrived
     // before the ticket is taken: no cache has to be written back for it.
-    __hip_atomic_store(loss_part + blockIdx.x, mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    const uint32_t before = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    if (before != gridDim.x - 1) return;
+    uint32_t before = 0;
+    if (lane == 0) {
+        __hip_atomic_store(loss_part + blockIdx.x, mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        before = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    if ((uint32_t)__builtin_amdgcn_readfirstlane((int)before) != gridDim.x - 1) return;
+    // A lane for each part (one lane for all of them: 16 loads in turn).
     double total = 0.0;
-    for (unsigned i = 0; i < gridDim.x; ++i)
+    for (unsigned i = lane; i < gridDim.x; i += kWave)
         total += __hip_atomic_load(loss_part + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    for (int step = kWave / 2; step > 0; step /= 2) total += __shfl_xor(total, step);
+    if (lane != 0) return;
     *live_tokens = live;
     *loss = balance_loss(loss_coef, E, K, live, total);
 }
