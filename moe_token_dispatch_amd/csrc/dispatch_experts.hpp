@@ -15,7 +15,7 @@ constexpr int kGateMaxGroups = 512;  // workgroups of a gate forward with balanc
 // row of E probability sums, E counts and its live tokens.
 inline int gate_groups(int64_t num_tokens, int waves) {
     // One workgroup up to two tokens per wavefront: it needs no second kernel
-    // (256 experts: 16 tokens 6.2 us, 32 8.9, against 11.3; 48 would take 11.8).
+    // (256 experts: 16 tokens 6.2 us, 32 8.9, against 10.0; 48 would take 11.8).
     // One token per wavefront up to 256 workgroups, one per CU; a second one
     // per CU (better hidden latencies, but twice the partial rows) where each
     // wavefront still gets two tokens.

@@ -423,3 +423,15 @@ def test_balance_of_few_tokens(t, e):
     """Either side of the batches that one workgroup finishes alone."""
     mask = torch.rand((t,), generator=torch.Generator().manual_seed(t)) > 0.3
     _check(_logits(t, e, torch.float32, t + e), min(e, 8), False, mask=mask, coef=0.5)
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_lone_weight_has_no_gradient(sigmoid):
+    """One entry, normalised: its weight is constant, and only the loss has a gradient."""
+    t, e = 300, 40
+    z = _logits(t, e, torch.float32, 3)
+    p, out = _run(z, 1, sigmoid, True, 2.5, 0.01)
+    dw = 10 * torch.randn((t, 1), generator=torch.Generator().manual_seed(4))
+    assert torch.all(_gradient(p, z, out, dw, None) == 0)
+    loss = torch.tensor([1.0])
+    assert torch.equal(_gradient(p, z, out, dw, loss), _gradient(p, z, out, None, loss))
