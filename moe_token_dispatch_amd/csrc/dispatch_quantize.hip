@@ -7,7 +7,7 @@
 // goes through LDS, so the kernel is bound by HBM: 2 bytes read and 1 written
 // per channel (4 and 1 for SwiGLU, 6 and 2 for its gradient).
 // Measured: 4096 x 7168 rows 16.4 us (5.4 TB/s), SwiGLU's gradient of 32777 rows
-// of 2048 84.8 us (6.4 TB/s; a large copy reaches 5.0 to 5.3); 8 rows of 2048
+// of 2048 87.9 us (6.2 TB/s; a large copy reaches 5.0 to 5.3); 8 rows of 2048
 // through SwiGLU 3.9 us, which is the launch.
 #include "dispatch_common.hpp"
 #include "dispatch_device.hpp"
@@ -74,14 +74,14 @@ __global__ void __launch_bounds__(kQuantizeThreads) quantize_kernel(QuantizePara
             widen(uw, u);
             if (kSource == QuantizeSource::kSwiglu) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) g[i] = g[i] * fast_sigmoid(g[i]) * u[i];
+                for (int i = 0; i < 8; ++i) g[i] = g[i] * near_sigmoid(g[i]) * u[i];
                 quantize8<kStream>(g, true, lane == 0, p.q + row * p.width + c, p.sf + b);
             } else {
                 float d[8];
                 widen(load8<kStream>(p.grad + row * p.width + c), d);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float s = fast_sigmoid(g[i]);
+                    const float s = near_sigmoid(g[i]);
                     const float du = d[i] * g[i] * s;
                     g[i] = d[i] * u[i] * s * (1.f + g[i] * (1.f - s));
                     u[i] = du;
