@@ -7,7 +7,7 @@
 // goes through LDS, so the kernel is bound by HBM: 2 bytes read and 1 written
 // per channel (4 and 1 for SwiGLU, 6 and 2 for its gradient).
 // Measured: 4096 x 7168 rows 16.4 us (5.4 TB/s), SwiGLU's gradient of 32777 rows
-// of 2048 87.9 us (6.2 TB/s; a large copy reaches 5.0 to 5.3); 8 rows of 2048
+// of 2048 89.4 us (6.05 TB/s; a large copy reaches 5.0 to 5.3); 8 rows of 2048
 // through SwiGLU 3.9 us, which is the launch.
 #include "dispatch_common.hpp"
 #include "dispatch_device.hpp"

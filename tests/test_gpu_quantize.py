@@ -181,3 +181,43 @@ def test_binding_refuses_wrong_tensors():
         M.dispatch_quantize(x[:, :8].contiguous(), q, sf)         # not a multiple of 16
     with pytest.raises(M.DispatchError):
         M.dispatch_swiglu_quantize(x[:, :96].contiguous(), q, sf)  # halves of 48
+
+
+def _every_gate():
+    """Every finite bf16 value once as the first channel of a block whose other gates are -2..2, the up values 1."""
+    bits = torch.arange(-32768, 32768, dtype=torch.int32).to(torch.int16)
+    z = bits.view(torch.bfloat16)
+    z = z[torch.isfinite(z)]
+    h = torch.ones((z.numel(), 256), dtype=torch.bfloat16)
+    h[:, :128] = torch.linspace(-2, 2, 128).to(torch.bfloat16)
+    h[:, 0] = z
+    return h
+
+
+def test_swiglu_of_every_finite_gate():
+    """The sigmoid is 0 or 1 far out, whatever the size of z; nothing finite becomes NaN."""
+    h = _every_gate()
+    q, sf = _out(h.shape[0], 128)
+    M.dispatch_swiglu_quantize(h.to(DEV), q, sf)
+    # As test_swiglu; the values of gates below -87 are under 2^-119, the floor of a block is 2^-100.
+    R.assert_quantised(_values(q), sf.cpu(), R.swiglu(h), 16 * EPS)
+
+
+def test_swiglu_gradient_of_every_finite_gate():
+    h = _every_gate()
+    d = torch.ones((h.shape[0], 128), dtype=torch.bfloat16)
+    q, sf = _out(h.shape[0], 256)
+    M.dispatch_swiglu_backward_quantize(h.to(DEV), d.to(DEV), q, sf)
+    # g (1 - s) has up to 17.3 times the sigmoid's error of 3 units (from there on s is 1), and a few roundings.
+    R.assert_quantised(_values(q), sf.cpu(), R.swiglu_gradient(h, d), 64 * EPS)
+
+
+def test_swiglu_of_infinite_gates():
+    """g / (1 + exp(-g)): infinity stays, -infinity has no value; other blocks keep theirs."""
+    h = torch.ones((2, 512), dtype=torch.bfloat16)
+    h[0, 3], h[1, 3] = math.inf, -math.inf
+    q, sf = _out(2, 256)
+    M.dispatch_swiglu_quantize(h.to(DEV), q, sf)
+    v, s = _values(q), sf.cpu()
+    assert math.isinf(float(s[0, 0])) and math.isnan(float(v[0, 3])) and math.isnan(float(s[1, 0]))
+    R.assert_quantised(v[:, 128:], s[:, 1:], R.swiglu(h)[:, 128:], 16 * EPS)
