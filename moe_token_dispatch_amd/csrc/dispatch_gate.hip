@@ -921,9 +921,13 @@ __global__ void __launch_bounds__(kGateWaves<V> * kWave) gate_backward_kernel(Ga
             __builtin_amdgcn_wave_barrier();
             float ds = p.route_scale * dw;
             if (p.flags & DISPATCH_GATE_NORMALIZE) {
-                // (Less the first entry's gradient, which changes nothing: a
-                // lone entry's weight is constant, and its gradient exactly 0.)
-                dw -= __int_as_float(__builtin_amdgcn_readlane(__float_as_int(dw), 0));
+                // (Less the gradient of the entry with the largest score, which
+                // changes nothing: a lone entry's weight is constant, and its
+                // gradient exactly 0. Another entry's gradient may be far larger
+                // than all that comes of it, and its rounding would stay.)
+                const uint32_t largest = wave_max(__float_as_uint(mine));
+                const int from = __builtin_ctzll(__ballot(__float_as_uint(mine) == largest));
+                dw -= __int_as_float(__builtin_amdgcn_readlane(__float_as_int(dw), from));
                 const float total = wave_sum(mine);
                 const float mean = wave_sum(dw * mine);
                 ds = total == 0.f ? 0.f : p.route_scale / total * (dw - mean / total);

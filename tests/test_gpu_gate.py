@@ -435,3 +435,28 @@ def test_lone_weight_has_no_gradient(sigmoid):
     assert torch.all(_gradient(p, z, out, dw, None) == 0)
     loss = torch.tensor([1.0])
     assert torch.equal(_gradient(p, z, out, dw, loss), _gradient(p, z, out, None, loss))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_gradient_beside_a_large_one_of_a_small_share(dtype):
+    """A selection bias puts an expert of a tiny score first; its weight's gradient is large, and tiny in all others'."""
+    t, e, k = 33, 20, 4
+    z = _logits(t, e, torch.float32, 71, 0.5)
+    z[:, 7] = -20.0
+    z = z.to(dtype)
+    bias = torch.zeros(e)
+    bias[7] = 5.0
+    p, out = _run(z, k, True, True, 2.0, 0.5, bias)
+    idx, count = out.topk_idx.cpu(), out.expert_count.cpu()
+    assert torch.all(idx[:, 0] == 7)
+    dw = torch.randn((t, k), generator=torch.Generator().manual_seed(5))
+    dw[:, 0] *= 1e6
+    got = _gradient(p, z, out, dw, None)
+    want = R.gate_gradient(z, idx, count, True, True, 2.0, 0.5, dw, None)
+    # A weight's gradient and the mean of all, each with a few roundings of
+    # what it is added up from: shares times gradients, no more.
+    score = torch.sigmoid(z.double()).gather(1, idx)
+    share = score / score.sum(1, keepdim=True)
+    mean = (share * dw.double().abs()).sum(1, keepdim=True)
+    bound = torch.zeros_like(want).scatter_(1, idx, REL * 2.0 * share * (dw.double().abs() + mean))
+    assert torch.all((got - want).abs() <= bound + (BF16 if dtype == torch.bfloat16 else 0) * want.abs())
