@@ -218,7 +218,9 @@ __device__ __forceinline__ float reciprocal(float x) {
 }
 
 // A row's sum of scores (before softmax divides by it) and its reciprocal, 0
-// for a row whose scores are all 0.
+// for a row whose scores are all 0. (The smallest sigmoid that is not 0, of the
+// last fp32 number before exp(-z) is infinite, is 2^-128 (1 + 2^-17): its
+// reciprocal is finite, that times another number may not be.)
 struct RowSum {
     float sum, inv;
     // s / sum, the product's rounding corrected: a lone score's share is 1, so
@@ -399,9 +401,10 @@ __global__ void __launch_bounds__(kGateWaves<V> * kWave) gate_kernel(GateParams 
             __builtin_amdgcn_wave_barrier();
             if (p.flags & DISPATCH_GATE_NORMALIZE) {
                 const float total = wave_sum(weight);
-                // (A softmax row's largest share is at least 1 / E.)
+                // (A softmax row's largest share is at least 1 / E. Sigmoid
+                // scores may be as small as numbers are: divided first.)
                 weight = total == 0.f ? 0.f
-                         : kSigmoid   ? p.route_scale * weight / total
+                         : kSigmoid   ? p.route_scale * (weight / total)
                                       : p.route_scale * weight * reciprocal(total);
             } else {
                 weight *= p.route_scale;
@@ -679,7 +682,7 @@ __global__ void __launch_bounds__(kRowWaves * kWave, 4) gate_rows_kernel(GatePar
         if (p.flags & DISPATCH_GATE_NORMALIZE) {
             const float total = row_sum(weight);
             weight = total == 0.f ? 0.f
-                     : kSigmoid   ? p.route_scale * weight / total
+                     : kSigmoid   ? p.route_scale * (weight / total)
                                   : p.route_scale * weight * reciprocal(total);
         } else {
             weight *= p.route_scale;
@@ -919,7 +922,10 @@ __global__ void __launch_bounds__(kGateWaves<V> * kWave) gate_backward_kernel(Ga
             __builtin_amdgcn_wave_barrier();
             const float mine = e >= 0 ? row[slot_of<V>(e, E)] : 0.f;
             __builtin_amdgcn_wave_barrier();
+            // The entry's score's gradient; with sigmoid, times the score,
+            // which may be too small a number to be divided by.
             float ds = p.route_scale * dw;
+            if (kSigmoid) ds *= mine;
             if (p.flags & DISPATCH_GATE_NORMALIZE) {
                 // (Less the gradient of the entry with the largest score, which
                 // changes nothing: a lone entry's weight is constant, and its
@@ -929,8 +935,13 @@ __global__ void __launch_bounds__(kGateWaves<V> * kWave) gate_backward_kernel(Ga
                 const int from = __builtin_ctzll(__ballot(__float_as_uint(mine) == largest));
                 dw -= __int_as_float(__builtin_amdgcn_readlane(__float_as_int(dw), from));
                 const float total = wave_sum(mine);
-                const float mean = wave_sum(dw * mine);
-                ds = total == 0.f ? 0.f : p.route_scale / total * (dw - mean / total);
+                if (kSigmoid) {
+                    const float part = total == 0.f ? 0.f : mine / total;
+                    ds = p.route_scale * part * (dw - wave_sum(dw * part));
+                } else {
+                    const float mean = wave_sum(dw * mine);
+                    ds = total == 0.f ? 0.f : p.route_scale / total * (dw - mean / total);
+                }
             }
             const float zero[V] = {};
             write_slots<V>(row, lane, zero);
@@ -953,7 +964,7 @@ __global__ void __launch_bounds__(kGateWaves<V> * kWave) gate_backward_kernel(Ga
             mean = wave_sum(mean);
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                s[v] = kSigmoid ? (d[v] + (dp[v] - mean) * row_sum.inv) * s[v] * (1.f - s[v]) : s[v] * (d[v] - mean);
+                s[v] = kSigmoid ? (d[v] + (dp[v] - mean) * (s[v] * row_sum.inv)) * (1.f - s[v]) : s[v] * (d[v] - mean);
         } else {
 #pragma unroll
             for (int v = 0; v < V; ++v) s[v] = 0.f;

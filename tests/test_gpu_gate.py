@@ -460,3 +460,61 @@ def test_gradient_beside_a_large_one_of_a_small_share(dtype):
     mean = (share * dw.double().abs()).sum(1, keepdim=True)
     bound = torch.zeros_like(want).scatter_(1, idx, REL * 2.0 * share * (dw.double().abs() + mean))
     assert torch.all((got - want).abs() <= bound + (BF16 if dtype == torch.bfloat16 else 0) * want.abs())
+
+
+def _smallest(t, e):
+    """fp32 sigmoid logits whose scores are 2^-115 to 2^-128, the smallest that are not 0: all of a row's, or one alone."""
+    z = -88.7228 + 9.0 * torch.rand((t, e), generator=torch.Generator().manual_seed(t + e))
+    z[1] = -88.72283  # the last fp32 number whose exp(-z) is finite
+    z[2] = -math.inf
+    z[2, e // 2] = -88.72283
+    return z
+
+
+# A score of 2^-128 has 21 bits: half a unit of them, and as much again from exp,
+# in a share, its sum and the products that they enter.
+SMALLEST = 8 * 2.0 ** -21
+
+
+@pytest.mark.parametrize("e,k", [(1, 1), (7, 1), (7, 3), (70, 8)])
+@pytest.mark.parametrize("scale", [2.5, 1e-3])
+def test_smallest_sigmoid_scores(e, k, scale):
+    """Shares of scores whose reciprocals are past fp32's range, in the weights, the loss and both gradients."""
+    t = 33
+    z = _smallest(t, e)
+    p, out = _run(z, k, True, True, scale, 0.5)
+    idx, count = out.topk_idx.cpu(), out.expert_count.cpu()
+    took = idx >= 0
+    score = torch.sigmoid(z.double())
+    picked = torch.where(took, score.gather(1, idx.clamp_min(0)), 0.0)
+    share = picked / picked.sum(1, keepdim=True)
+    got = out.topk_weights.cpu().double()
+    assert torch.all((got - scale * share).abs() <= SMALLEST * scale * share)
+    prob_sum = (score / score.sum(1, keepdim=True)).sum(0)
+    assert torch.all((out.prob_sum.cpu().double() - prob_sum).abs() <= SMALLEST * prob_sum)
+    loss = 0.5 * e / (k * t * t) * float((count.double() * prob_sum).sum())
+    assert abs(float(out.loss) - loss) <= SMALLEST * loss
+    dw, dloss = torch.randn((t, k), generator=torch.Generator().manual_seed(6)), torch.tensor([1.7])
+    for a, b in ((dw, None), (None, dloss), (dw, dloss)):
+        want = R.gate_gradient(z, idx, count, True, True, scale, 0.5, a, b)
+        # Each gradient's terms: an entry's share times its own and the mean gradient, the same of the shares of all.
+        size = (scale * dw.abs().max() if a is not None else 0.0) + \
+            (2 * 1.7 * 0.5 * e / (k * t * t) * float(count.max()) if b is not None else 0.0)
+        assert torch.all((_gradient(p, z, out, a, b) - want).abs() <= 2 * SMALLEST * size)
+    # Not normalised, the weights' gradient is in fp32's smallest numbers, the loss's as before.
+    p, out = _run(z, k, True, False, scale, 0.5)
+    got = _gradient(p, z, out, dw, None)
+    want = R.gate_gradient(z, idx, count, True, False, scale, 0.5, dw, None)
+    assert torch.all((got - want).abs() <= SMALLEST * want.abs() + 2.0 ** -147)
+
+
+def test_smallest_sigmoid_scores_of_many_tokens():
+    t, e, k = 8229, 130, 8
+    z = _smallest(t, e)
+    p, out = _run(z, k, True, True, 2.5, 0.5)
+    few, b = _run(z[:64].contiguous(), k, True, True, 2.5, 0.5)
+    assert torch.equal(out.topk_idx[:64], b.topk_idx)
+    assert torch.all((out.topk_weights[:64] - b.topk_weights).abs() <= SMALLEST * b.topk_weights)
+    score = torch.sigmoid(z.double())
+    prob_sum = (score / score.sum(1, keepdim=True)).sum(0)
+    assert torch.all((out.prob_sum.cpu().double() - prob_sum).abs() <= SMALLEST * prob_sum)
