@@ -466,8 +466,11 @@ int dispatch_swiglu_backward_quantize(const dispatch_quantize_problem_t* problem
  * each of its rows r in [expert_psum[e], expert_psum[e] + expert_count[e]),
  *   y[r, n] = sum_b x_sf[r, b] * w_sf[e, n / 128, b]
  *                   * sum_{k in block b} x[r, k] * w[e, n, k]
- * with fp8 (e4m3) x and w, blocks of 128 channels (the last may be short),
- * the fp8 matrix instruction's sum within a block and fp32 sums across them.
+ * with fp8 (e4m3) x and w, blocks of 128 channels (the last may be short) and
+ * fp32 sums across them. Within a block the sum is the fp8 matrix
+ * instruction's, which drops what is below about 2^-14 of a run's largest
+ * product; the SwiGLU product of few rows (at most 16 an expert announced)
+ * adds in fp32 there too.
  * Pad rows and rows beyond the totals are neither read nor
  * written. The rows' gradient of a product with weights w[E, N, K] is this
  * product with the weights laid out as [E, K, N] and their scales as

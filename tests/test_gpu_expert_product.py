@@ -368,3 +368,49 @@ def test_shared_tiles_of_every_size(announced, counts):
             _check_swiglu(s, *got[1:])
             first = got
         assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(first, got))
+
+
+@pytest.mark.parametrize("k", [128, 4096])
+def test_few_rows_keep_what_cancels_leaves(k):
+    """448 * 448 - 448 * 448 + 2 * 2 within 16 channels, before an activation: 4, in tiles that share K and alone."""
+    counts, n = [1, 0, 3], 256
+    rows = sum(counts)
+    x, w = torch.zeros((rows, k)), torch.zeros((3, n, k))
+    at = k - 100  # in the last block
+    x[:, at:at + 3] = torch.tensor([448.0, 448.0, 2.0])
+    w[:, :128, at:at + 3] = torch.tensor([448.0, -448.0, 2.0])
+    w[:, 128:, at] = 1.0
+    p = M.make_expert_problem(3, k, n, rows)
+    ins = [v.to(DEV) for v in (torch.tensor([0, 1, 1, 4], dtype=torch.int32), torch.tensor(counts, dtype=torch.int32),
+                               x.to(R.FP8), torch.ones((rows, k // 128)), w.to(R.FP8), torch.ones((3, 2, k // 128)))]
+    want = 4.0 * torch.sigmoid(torch.tensor(4.0, dtype=torch.float64)) * 448.0
+    for ws in (None, M.alloc_expert_workspace(p, DEV)):
+        q, sf = torch.zeros((rows, 128), dtype=R.FP8, device=DEV), torch.zeros((rows, 1), device=DEV)
+        M.dispatch_expert_product_swiglu(p, *ins, q, sf, ws)
+        assert torch.all((sf.cpu().double() - want / 448.0).abs() <= 16 * EPS * want / 448.0)
+        assert torch.all(q.float() == 448.0)
+
+
+@pytest.mark.parametrize("counts,k", [([1], 1040), ([3, 0, 20], 4096), ([16, 17, 1, 1, 40, 5], 7168), ([0, 2], 144)], ids=str)
+def test_swiglu_of_few_rows_in_fp32(counts, k):
+    """As _check_swiglu, with no allowance for bits dropped within a block."""
+    s = _problem(counts, k, 512, 16, k + 7)
+    e, n = s["w"].shape[:2]
+    p = M.make_expert_problem(e, k, n, s["rows"], sum(counts))
+    y, mag, _ = R.product(s["x"], s["x_sf"], s["w"], s["w_sf"], s["psum"], s["counts"])
+    live = s["live"]
+    y, mag = y[live], mag[live]
+    a, g, u = R.swiglu(y), y[:, :256], y[:, 256:]
+    # A block's 128 products and the blocks' sums: a few dozen roundings of the sum of magnitudes.
+    eps = (32 + _blocks(k)) * EPS
+    err = eps * (1.1 * mag[:, :256] * u.abs() + mag[:, 256:] * g.abs() + a.abs())
+    top = a.abs().view(-1, 2, 128).amax(2, keepdim=True)
+    rel = float((err.view(-1, 2, 128) / top).amax()) + 16 * EPS
+    assert rel < 2.0 ** -10, "the inputs say too little"
+    for ws in (None, M.alloc_expert_workspace(p, DEV)):
+        q = torch.full((s["rows"], 256), CANARY, dtype=torch.uint8, device=DEV)
+        sf = torch.full((s["rows"], 2), -7.0, device=DEV)
+        M.dispatch_expert_product_swiglu(p, *_dev(s, "psum_t", "count_t", "x", "x_sf", "w", "w_sf"), q, sf, ws)
+        q, sf = q.cpu(), sf.cpu()
+        assert torch.all(q[~live] == CANARY) and torch.all(sf[~live] == -7.0)
+        R.assert_quantised(q[live].view(R.FP8).float(), sf[live], a, rel)
