@@ -483,7 +483,7 @@ typedef struct dispatch_expert_problem {
     uint32_t reserved;        /* must be 0 */
     int64_t in_features;      /* K: channels of x, a multiple of 16, 16..2^20 */
     int64_t out_features;     /* N: rows of an expert's weights, a multiple of 8, 8..2^20 */
-    int64_t expert_rows;      /* rows of x and of the output, <= 2^31 - 1 (and their 16 x 64 tiles of
+    int64_t expert_rows;      /* rows of x and of the output, <= 2^31 - 1 (and their 16 x 256 tiles of
                                  the output too); rows outside are skipped */
     int64_t max_routed_rows;  /* about how many rows are routed at most (T * K); picks the kernel and
                                  its grid, more rows are computed all the same */

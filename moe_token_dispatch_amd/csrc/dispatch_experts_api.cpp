@@ -58,8 +58,8 @@ int check_experts(const dispatch_expert_problem_t* problem, bool swiglu) {
     if (p.expert_rows < 0 || p.expert_rows > INT32_MAX || p.max_routed_rows < 0) return DISPATCH_ERR_ARG;
     if (p.in_features % 16 != 0 || p.out_features % (swiglu ? 2 * DISPATCH_SF_BLOCK : 8) != 0)
         return DISPATCH_ERR_ALIGN;
-    // Tiles (at least 16 rows x 64 channels each) are counted in 32 bits.
-    if ((p.expert_rows / 16 + p.num_experts) * ((p.out_features + 63) / 64) > INT32_MAX) return DISPATCH_ERR_ARG;
+    // Tiles (at least 16 rows x 256 channels each) are counted in 32 bits.
+    if ((p.expert_rows / 16 + p.num_experts) * ((p.out_features + 255) / 256) > INT32_MAX) return DISPATCH_ERR_ARG;
     return DISPATCH_OK;
 }
 

@@ -212,3 +212,15 @@ def test_references_of_the_gate_agree(sigmoid):
         b = R.gate_table(x, 4, sigmoid, True, 1.5, 0.1, bias, mask)
         for name in names:
             assert torch.equal(torch.as_tensor(a[name]), torch.as_tensor(b[name])), name
+
+
+@pytest.mark.parametrize("width", [8, 256, 264, 1 << 20])
+def test_largest_expert_problems(width):
+    """The output's tiles of 16 rows x 256 channels are counted in 32 bits; what they hold is taken."""
+    lib, n = M.load_library(), ctypes.c_size_t(0)
+    most = min((1 << 31) - 1, ((((1 << 31) - 1) // -(-width // 256)) - 4) * 16 + 15)
+    assert lib.dispatch_expert_workspace_size(B(_experts(out_features=width, expert_rows=most)), B(n)) == M.OK
+    if most < (1 << 31) - 1:
+        p = _experts(out_features=width, expert_rows=most + 1)
+        assert lib.dispatch_expert_workspace_size(B(p), B(n)) == M.ERR_ARG
+        assert lib.dispatch_expert_product(B(p), *[4096] * 7, None, 0, None) == M.ERR_ARG
