@@ -1062,6 +1062,12 @@ def _sf_blocks(width: int) -> int:
     return (width + SF_BLOCK - 1) // SF_BLOCK
 
 
+def _check_grad(grad: Optional[torch.Tensor]) -> None:
+    """SwiGLU's gradient needs one (None stands for the calls that have none)."""
+    if grad is None:
+        raise ValueError("grad must be a device tensor")
+
+
 def _quantize_args(x, grad, q, sf, num_valid_rows, halves_in: int, halves_out: int, stream):
     """halves_in, halves_out: x's and q's channels in units of the problem's width."""
     _check_device_tensor(x, "x", torch.bfloat16)
@@ -1104,6 +1110,7 @@ def dispatch_swiglu_backward_quantize(h: torch.Tensor, grad: torch.Tensor, q: to
                                       stream: Optional[torch.cuda.Stream] = None) -> None:
     """Enqueue SwiGLU's gradient with respect to h [R, 2I], from grad [R, I],
     to fp8 q [R, 2I] and scales sf [R, 2I / 128]."""
+    _check_grad(grad)
     args, _keep = _quantize_args(h, grad, q, sf, num_valid_rows, 2, 2, stream)
     rc = load_library().dispatch_swiglu_backward_quantize(*args)
     if rc:
@@ -1143,8 +1150,7 @@ class SwigluBackwardQuantizePlan(QuantizePlan):
 
     def __init__(self, h: torch.Tensor, grad: torch.Tensor, q: torch.Tensor, sf: torch.Tensor,
                  num_valid_rows: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
-        if grad is None:
-            raise ValueError("grad must be a device tensor")
+        _check_grad(grad)
         self._prepare(h, grad, q, sf, num_valid_rows, stream)
 
 

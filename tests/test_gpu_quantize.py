@@ -221,3 +221,11 @@ def test_swiglu_of_infinite_gates():
     v, s = _values(q), sf.cpu()
     assert math.isinf(float(s[0, 0])) and math.isnan(float(v[0, 3])) and math.isnan(float(s[1, 0]))
     R.assert_quantised(v[:, 128:], s[:, 1:], R.swiglu(h)[:, 128:], 16 * EPS)
+
+
+def test_swiglu_gradient_needs_a_gradient():
+    h = torch.zeros((4, 512), dtype=torch.bfloat16, device=DEV)
+    q, sf = _out(4, 512)
+    for call in (M.dispatch_swiglu_backward_quantize, M.SwigluBackwardQuantizePlan):
+        with pytest.raises(ValueError, match="grad"):
+            call(h, None, q, sf)
