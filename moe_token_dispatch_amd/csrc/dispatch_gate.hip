@@ -849,7 +849,7 @@ struct GateBackwardParams {
 template <int V, bool kHalf, bool kSigmoid>
 __global__ void __launch_bounds__(kGateWaves<V> * kWave) gate_backward_kernel(GateBackwardParams p) {
     constexpr int W = kGateWaves<V>;
-    extern __shared__ float lds[];  // [W][V * 64] score gradients, zero between tokens
+    extern __shared__ float lds[];  // [W][V * 64]: a token's scores, then their gradients
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int E = p.num_experts, K = p.num_topk;
@@ -890,10 +890,7 @@ __global__ void __launch_bounds__(kGateWaves<V> * kWave) gate_backward_kernel(Ga
     };
     float dp[V];  // the loss's gradient of this lane's experts' p: the same for every token
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        row[v * kWave + lane] = 0.f;
-        dp[v] = 0.f;
-    }
+    for (int v = 0; v < V; ++v) dp[v] = 0.f;
     if (p.grad_loss != nullptr) {
         const float n = (float)*p.live_tokens;
         const float unit = n == 0.f ? 0.f : *p.grad_loss * (p.loss_coef * (float)E / ((float)K * n * n));

@@ -110,18 +110,6 @@ __device__ __forceinline__ float wave_sum(float v) {
     v += dpp_float<kDppBcast31, 0xc>(0.f, v);
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
-// NaN is ignored (every lane's value may be NaN: then the result is -inf).
-__device__ __forceinline__ float wave_max(float v) {
-    const float low = -__builtin_inff();
-    v = fmaxf(v, low);
-    v = fmaxf(v, dpp_float<kDppRowShr + 1, 0xf>(low, v));
-    v = fmaxf(v, dpp_float<kDppRowShr + 2, 0xf>(low, v));
-    v = fmaxf(v, dpp_float<kDppRowShr + 4, 0xf>(low, v));
-    v = fmaxf(v, dpp_float<kDppRowShr + 8, 0xf>(low, v));
-    v = fmaxf(v, dpp_float<kDppBcast15, 0xa>(low, v));
-    v = fmaxf(v, dpp_float<kDppBcast31, 0xc>(low, v));
-    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
-}
 
 // Largest of the 64 lanes, uniform.
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
