@@ -518,3 +518,33 @@ def test_smallest_sigmoid_scores_of_many_tokens():
     score = torch.sigmoid(z.double())
     prob_sum = (score / score.sum(1, keepdim=True)).sum(0)
     assert torch.all((out.prob_sum.cpu().double() - prob_sum).abs() <= SMALLEST * prob_sum)
+
+
+# Tokens past one for each wavefront of the gradient's grid (512 workgroups of
+# 16, 8 and 4 wavefronts, by the number of experts), not a multiple of anything.
+@pytest.mark.parametrize("t,e,k", [(8192 + 37, 64, 8), (20011, 129, 8), (8192 + 37, 512, 5), (4096 + 45, 601, 8),
+                                   (2048 + 77, 1100, 32)])
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_gradient_of_many_tokens(t, e, k, sigmoid, dtype):
+    """A wavefront's later tokens: the same rows in calls of at most 300, with the same counts, have the same bits."""
+    z, mask = _many(t, e, k, dtype, sigmoid, e)
+    p, out = _run(z, k, sigmoid, True, 2.5, 0.5, None, mask)
+    g = torch.Generator().manual_seed(t)
+    dw, dloss = torch.randn((t, k), generator=g).to(DEV), torch.tensor([1.7], device=DEV)
+    zd, md = z.to(DEV), mask.to(DEV)
+    for a, b, m in ((dw, dloss, md), (None, dloss, md), (dw, None, None)):
+        got = torch.full_like(zd, 77.0)
+        M.dispatch_gate_backward(p, zd, out, a, b, got, token_mask=m)
+        want = torch.full_like(zd, 78.0)
+        for first in range(0, t, 300):
+            part = slice(first, min(first + 300, t))
+            n = part.stop - first
+            few = M.make_gate_problem(n, e, k, M.GATE_SIGMOID if sigmoid else M.GATE_SOFTMAX, dtype, True, 2.5, 0.5)
+            rows = M.GateTensors(out.topk_idx[part], out.topk_weights[part], out.expert_count, out.prob_sum,
+                                 out.live_tokens, out.loss)
+            M.dispatch_gate_backward(few, zd[part], rows, None if a is None else a[part], b, want[part],
+                                     token_mask=None if m is None else m[part])
+        bits = torch.int16 if dtype == torch.bfloat16 else torch.int32
+        assert torch.equal(got.view(bits), want.view(bits))
+        assert m is None or torch.all(got[~md] == 0)

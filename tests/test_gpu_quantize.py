@@ -229,3 +229,29 @@ def test_swiglu_gradient_needs_a_gradient():
     for call in (M.dispatch_swiglu_backward_quantize, M.SwigluBackwardQuantizePlan):
         with pytest.raises(ValueError, match="grad"):
             call(h, None, q, sf)
+
+
+# Buffers past the Infinity Cache (256 MB read and written) take another form of
+# the kernel: its first, middle and last rows against the same rows by themselves.
+@pytest.mark.parametrize("name,r,w", [("rows", 12500, 7168), ("swiglu", 26300, 2048), ("swiglu_gradient", 16500, 2048)])
+def test_large_buffers(name, r, w):
+    g = torch.Generator(device=DEV).manual_seed(r)
+    normal = lambda width: torch.randn((r, width), generator=g, device=DEV, dtype=torch.bfloat16)  # noqa: E731
+    ins = {"rows": [w], "swiglu": [2 * w], "swiglu_gradient": [2 * w, w]}[name]
+    ins = [normal(width) for width in ins]
+    call, width, channel_bytes = {"rows": (M.dispatch_quantize, w, 3), "swiglu": (M.dispatch_swiglu_quantize, w, 5),
+                                  "swiglu_gradient": (M.dispatch_swiglu_backward_quantize, 2 * w, 8)}[name]
+    assert r * w * channel_bytes > 1 << 28
+    q, sf = _out(r, width)
+    call(*ins, q, sf)
+    assert not torch.any(sf == -7.0)
+    for first in (0, r // 2, r - 100):
+        part = slice(first, first + 100)
+        few_q, few_sf = _out(100, width)
+        call(*[x[part] for x in ins], few_q, few_sf)
+        assert torch.equal(q[part], few_q) and torch.equal(sf[part], few_sf)
+    n = torch.tensor([r - 50], dtype=torch.int32, device=DEV)
+    q2, sf2 = _out(r, width)
+    call(*ins, q2, sf2, n)
+    assert torch.equal(q2[:-50], q[:-50]) and torch.equal(sf2[:-50], sf[:-50])
+    assert torch.all(q2[-50:] == 0x5A) and torch.all(sf2[-50:] == -7.0)
