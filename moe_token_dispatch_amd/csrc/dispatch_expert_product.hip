@@ -23,11 +23,11 @@
 // weights' bytes (5.3 TB/s); 32768 rows, 7168 -> 2048, 532 us, bound by the matrix
 // instructions and their operands from LDS (1.81 PFLOP/s; the library's 8192^3
 // fp8 product, with one scale for all, reaches 2.6 to 2.7).
-#include <cmath>
 #include <type_traits>
 
 #include "dispatch_common.hpp"
 #include "dispatch_device.hpp"
+#include "dispatch_expert_plan.hpp"
 #include "dispatch_experts.hpp"
 #include "dispatch_math.hpp"
 
@@ -40,11 +40,6 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kXcds = 8;  // workgroup i runs on XCD i % 8
-constexpr int kCus = 256;
-
-// Tickets at the start of a workspace, as many as any problem shares tiles
-// (then there are at most kCus), so that one workspace serves several.
-constexpr size_t kTicketBytes = kCus * sizeof(uint32_t);
 
 struct ProductParams {
     const int32_t* psum;
@@ -626,35 +621,6 @@ __global__ void __launch_bounds__(Shape::kWaves * kWave, 2) product_kernel(Produ
     }
 }
 
-// Row tiles at most: one of each expert that has a row may be partial.
-int64_t most_row_tiles(int64_t max_rows, int32_t num_experts, int tile_rows) {
-    return max_rows / tile_rows + (max_rows < num_experts ? max_rows : num_experts);
-}
-
-// How a product is cut.
-struct ProductPlan {
-    int64_t tiles;  // at most
-    int parts;      // workgroups per tile
-    size_t bytes;   // of workspace: tickets, then sums (0: nothing shared)
-};
-
-constexpr int kMaxParts = 16;
-
-template <class Shape>
-ProductPlan plan_product(int64_t max_rows, int32_t num_experts, int32_t N, int32_t k_blocks, bool workspace) {
-    ProductPlan s;
-    s.tiles = most_row_tiles(max_rows, num_experts, Shape::kTokens) * ((N + 255) / 256);
-    // As many parts as fill the CUs, each left with four blocks of K or more.
-    // (Not of tiles of 128 tokens and more: their sums take the workgroup that
-    // adds them 30 us a MB, and smaller tiles were faster in all of 28 problems.)
-    const int64_t want = kCus / (s.tiles < 1 ? 1 : s.tiles);
-    const int64_t most = workspace && Shape::kTokens <= 64 ? k_blocks / 4 : 1;
-    const int64_t parts = want < most ? want : most;
-    s.parts = (int)(parts < 1 ? 1 : (parts > kMaxParts ? kMaxParts : parts));
-    s.bytes = s.parts == 1 ? 0 : kTicketBytes + (size_t)(s.tiles * s.parts) * Shape::kSumFloats * sizeof(float);
-    return s;
-}
-
 using Shape16 = TileShape<16, 8, 4>;
 using Shape32 = TileShape<32, 8, 4>;
 using Shape64 = TileShape<64, 4, 3>;
@@ -662,10 +628,10 @@ using Shape128 = TileShape<128, 2, 3>;
 using Shape192 = TileShape<192, 2, 2>;
 using Shape256 = TileShape<256, 2, 2>;
 // Shape16 for the SwiGLU product of rows that fill no more than one tile of it per
-// expert: decoding, bound by the weights' bytes or the launch. Its result is
-// rounded to 8 bits, where what the fp8 instruction drops turns single roundings:
-// a layer of 1 to 30 rows was off from 64 bits by up to 0.0035 (0.0017 in the
-// median, and always with the operands widened). 8 rows on 32 experts, 7168 -> 2 x
+// expert (wide_operands): decoding, bound by the weights' bytes or the launch. Its
+// result is rounded to 8 bits, where what the fp8 instruction drops turns single
+// roundings: a layer of 1 to 30 rows was off from 64 bits by up to 0.0035 (0.0017 in
+// the median, and always with the operands widened). 8 rows on 32 experts, 7168 -> 2 x
 // 2048 -> 7168 channels, take 60 to 67 us with either; on 8 experts, 2048 -> 2 x 1024
 // -> 2048, 19.2 with these and 18.8; 200 rows there, past the rule, 22.7 and 20.1.
 // Widened operands in tiles of 32 and 64 tokens cost up to 35 %, and the other
@@ -673,9 +639,10 @@ using Shape256 = TileShape<256, 2, 2>;
 using Wide16 = TileShape<16, 8, 4, true>;
 
 template <class Shape, bool kSwiglu>
-hipError_t launch_product(ProductParams p, int64_t max_rows, void* workspace, hipStream_t stream) {
-    p.n_tiles = (p.N + 255) / 256;
-    const ProductPlan plan = plan_product<Shape>(max_rows, p.num_experts, p.N, p.k_blocks, workspace != nullptr);
+hipError_t launch_product(ProductParams p, const ProductSizes& sizes, void* workspace, hipStream_t stream) {
+    static_assert(Shape::kSumFloats == kTileChannels * Shape::kTokens, "a tile's sums");
+    p.n_tiles = (p.N + kTileChannels - 1) / kTileChannels;
+    const ProductPlan plan = plan_product(Shape::kTokens, sizes);
     p.parts = plan.parts;
     p.slots = plan.parts == 1 ? 0 : (int32_t)(plan.tiles * plan.parts);
     p.tickets = static_cast<uint32_t*>(workspace);
@@ -687,102 +654,26 @@ hipError_t launch_product(ProductParams p, int64_t max_rows, void* workspace, hi
     void* args[] = {&p};
     const void* kernel = (const void*)&product_kernel<Shape, kSwiglu>;
     if constexpr (kSwiglu && Shape::kTokens == Wide16::kTokens)
-        if (max_rows <= (int64_t)Wide16::kTokens * p.num_experts) kernel = (const void*)&product_kernel<Wide16, kSwiglu>;
+        if (wide_operands(sizes)) kernel = (const void*)&product_kernel<Wide16, kSwiglu>;
     return hipLaunchKernel(kernel, dim3((unsigned)groups), dim3(Shape::kWaves * kWave), args, Shape::kLdsBytes, stream);
 }
 
-// The shape whose tiles take least time by this estimate: rounds of tiles over
-// the CUs, each with its blocks of K and what a tile costs beside them
-// (beginning, epilogue, its output), and the sums of tiles that share their K.
-// The times are measured ones, us, of the full chip. An expert has about half
-// a tile more than its rows fill, fewer where its count (give or take its root)
-// fits a few tiles. Weights' bytes cost all shapes alike and are left out.
-//
-// Measured over 28 problems of 1 to 60 experts, 19 to 18847 rows, 272 to 8192 x 336
-// to 8192 channels: the choice is within 8 % of the fastest shape each time (a rule
-// by the mean of rows alone took up to 3.6 times that). Some of them, us by
-// tokens of a tile:
-//                                        16    32    64   128   192   256
-//   836 rows on 3, 2656 -> 336           13    12    14    27    31    38
-//   2000 rows on 8, 1024 -> 1024         21    17    11    14    15    19
-//   6175 rows on 45, 1856 -> 1536       143    89    62    55    65    67
-//   4096 rows on 8, 1024 -> 4096        128    77    52    44    39    44
-//   2562 rows on 6, 1280 -> 5376        115    73    51    36    42    30
-// and where the weights' bytes bound it, 32 experts, 2048 -> 7168, at mean 4, 16, 32
-// and 64 rows: 16 tokens 87, 103, 140, 217; 32: 90, 93, 107, 147; 64: 89, 92, 96, 124; 128:
-// 93, 97, 100, 111.
-struct TileTimes {
-    double tile, block;
-};
-constexpr TileTimes tile_times(int tokens) {
-    switch (tokens) {
-        case 16: return {3.1, 0.60};
-        case 32: return {4.7, 0.65};
-        case 64: return {5.7, 0.76};
-        case 128: return {7.7, 1.12};
-        case 192: return {9.9, 1.46};
-        default: return {11.0, 1.70};
-    }
-}
-
 template <class Shape>
-double product_time(int64_t max_rows, int32_t num_experts, int32_t N, int32_t k_blocks, bool workspace) {
-    const ProductPlan plan = plan_product<Shape>(max_rows, num_experts, N, k_blocks, workspace);
-    const double experts = max_rows < num_experts ? (double)max_rows : (double)num_experts;
-    const double mean = max_rows / experts, fill = mean / Shape::kTokens;
-    double per_expert = fill + 0.5;
-    if (num_experts == 1) {
-        per_expert = std::ceil(fill);
-    } else if (fill < 3) {
-        const double spread = std::sqrt(mean) / Shape::kTokens;
-        const double around = (std::ceil(fill - spread) + std::ceil(fill + spread)) / 2;
-        per_expert = around < per_expert ? around : per_expert;
-        per_expert = per_expert < 1 ? 1 : per_expert;
-    }
-    const double tiles = per_expert * experts * ((N + 255) / 256);
-    constexpr TileTimes times = tile_times(Shape::kTokens);
-    double us = std::ceil(tiles * plan.parts / kCus) * (times.tile + times.block * k_blocks / plan.parts);
-    if (plan.parts > 1) {
-        // The last workgroup's reading, and everybody's writing and reading.
-        const double kb = plan.parts * Shape::kSumFloats * 4e-3;
-        us += 2.5 + 0.012 * kb + tiles * kb * 2 / 5.2e3;
-    }
-    return us;
+hipError_t launch_product(const ProductParams& p, const ProductSizes& sizes, void* workspace, hipStream_t stream) {
+    return p.out_sf != nullptr ? launch_product<Shape, true>(p, sizes, workspace, stream)
+                               : launch_product<Shape, false>(p, sizes, workspace, stream);
 }
 
-template <class F>
-auto with_shape(int64_t max_rows, int32_t num_experts, int32_t N, int32_t k_blocks, bool workspace, F f) {
-    if (max_rows <= 0) return f(Shape16{});
-    const auto time = [&](auto shape) {
-        return product_time<decltype(shape)>(max_rows, num_experts, N, k_blocks, workspace);
-    };
-    const double us[] = {time(Shape16{}),  time(Shape32{}),  time(Shape64{}),
-                         time(Shape128{}), time(Shape192{}), time(Shape256{})};
-    int best = 0;
-    for (int i = 1; i < 6; ++i)
-        if (us[i] < us[best]) best = i;
-    switch (best) {
-        case 0: return f(Shape16{});
-        case 1: return f(Shape32{});
-        case 2: return f(Shape64{});
-        case 3: return f(Shape128{});
-        case 4: return f(Shape192{});
-        default: return f(Shape256{});
-    }
-}
-
-int64_t most_rows(const dispatch_expert_problem_t& p) {
-    return p.max_routed_rows < p.expert_rows ? p.max_routed_rows : p.expert_rows;
+ProductSizes sizes_of(const dispatch_expert_problem_t& p, bool workspace) {
+    return {p.max_routed_rows < p.expert_rows ? p.max_routed_rows : p.expert_rows, p.num_experts,
+            (int32_t)p.out_features, (int32_t)((p.in_features + 127) / 128), workspace};
 }
 
 }  // namespace
 
 size_t expert_workspace_bytes(const dispatch_expert_problem_t& prob) {
-    const int64_t max_rows = most_rows(prob);
-    const int32_t N = (int32_t)prob.out_features, k_blocks = (int32_t)((prob.in_features + 127) / 128);
-    return with_shape(max_rows, prob.num_experts, N, k_blocks, true, [&](auto shape) {
-        return plan_product<decltype(shape)>(max_rows, prob.num_experts, N, k_blocks, true).bytes;
-    });
+    const ProductSizes sizes = sizes_of(prob, true);
+    return plan_product(tile_tokens(sizes), sizes).bytes;
 }
 
 hipError_t launch_expert_product(const dispatch_expert_problem_t& prob, const int32_t* expert_psum,
@@ -805,12 +696,15 @@ hipError_t launch_expert_product(const dispatch_expert_problem_t& prob, const in
     p.N = (int32_t)prob.out_features;
     p.k_blocks = (p.K + 127) / 128;
     p.n_blocks = (p.N + 127) / 128;
-    const int64_t max_rows = most_rows(prob);
-    return with_shape(max_rows, prob.num_experts, p.N, p.k_blocks, workspace != nullptr, [&](auto shape) {
-        using Shape = decltype(shape);
-        return out_sf != nullptr ? launch_product<Shape, true>(p, max_rows, workspace, stream)
-                                 : launch_product<Shape, false>(p, max_rows, workspace, stream);
-    });
+    const ProductSizes sizes = sizes_of(prob, workspace != nullptr);
+    switch (tile_tokens(sizes)) {
+        case 16: return launch_product<Shape16>(p, sizes, workspace, stream);
+        case 32: return launch_product<Shape32>(p, sizes, workspace, stream);
+        case 64: return launch_product<Shape64>(p, sizes, workspace, stream);
+        case 128: return launch_product<Shape128>(p, sizes, workspace, stream);
+        case 192: return launch_product<Shape192>(p, sizes, workspace, stream);
+        default: return launch_product<Shape256>(p, sizes, workspace, stream);
+    }
 }
 
 }  // namespace moe_dispatch
