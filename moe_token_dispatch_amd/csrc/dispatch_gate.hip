@@ -483,14 +483,29 @@ __global__ void __launch_bounds__(kGateWaves<V> * kWave) gate_kernel(GateParams 
 // bitonic order that three steps sort. What is done once a token above (sums,
 // divisions, stores) is done once for four.
 //
-// Measured against the form above, us without and with balance outputs, 256
-// experts, top-8, softmax of fp32: 4096 tokens 4.6 and 12.7 (above 5.0, 12.3),
-// 8192 4.7 and 13.1 (7.1, 15.2), 65536 21.9 and 34.0 (38.2, 51.0); sigmoid of
-// bf16 with balance: 4096 15.6 (13.3), 8192 16.0 (16.9), 65536 46.9 (58.8). Its
-// time does not depend on k, a round above takes 3.3 us of 65536 tokens: even at
-// three rounds, four with sigmoid.
+// Its time does not depend on k; that of the form above does. Measured, us of this
+// form and of the one above with k = 3, 4, 6 and 8, without / with balance outputs:
+//
+//   softmax of fp32         here            k = 3         4            6            8
+//   128 experts,  4096   3.8 /  9.7    3.1 /  9.0   3.3 /  9.1   3.7 /  9.4   4.0 /  9.8
+//                 8192   3.8 / 10.1    4.0 / 10.0   4.2 / 10.3   4.7 / 11.1   5.2 / 11.7
+//                65536  14.4 / 24.1   17.2 / 23.6  18.6 / 25.5  21.8 / 29.4  24.9 / 33.4
+//   256 experts,  4096   4.4 / 11.0    3.6 /  9.5   3.9 /  9.8   4.5 / 10.3   5.1 / 10.9
+//                 8192   4.6 / 11.5    4.7 / 11.1   5.2 / 11.7   6.2 / 12.8   7.1 / 13.9
+//                65536  20.6 / 31.5   22.3 / 30.5  25.1 / 34.1  31.7 / 42.1  38.3 / 49.7
+//   sigmoid of bf16
+//   128 experts,  8192   5.0 / 11.4    4.3 / 11.0   4.5 / 11.2   5.0 / 12.0   5.5 / 12.7
+//                16384   6.9 / 14.4    6.4 / 14.2   6.8 / 14.8   7.7 / 15.8   8.6 / 16.8
+//                65536  19.3 / 30.1   19.4 / 29.9  21.1 / 31.7  24.2 / 35.6  27.3 / 39.5
+//   256 experts,  8192   6.5 / 13.9    5.5 / 12.5   5.9 / 12.9   6.8 / 14.0   7.8 / 15.1
+//                16384   9.5 / 18.9    8.6 / 19.3   9.2 / 20.1  10.9 / 22.4  12.7 / 24.6
+//                65536  30.1 / 42.4   27.0 / 46.9  29.6 / 50.8  35.5 / 59.0  42.1 / 67.6
+//
+// So it is taken for four entries and more from 8192 tokens on, with sigmoid and
+// fewer than six from twice as many. (72 experts as 128, 200 as 256.)
 constexpr int kBest = 8;
 constexpr int kFewestRounds = 4;
+constexpr int kFewestSigmoidRounds = 6;  // of less than 2 kManyTokens
 constexpr int64_t kManyTokens = 8192;
 constexpr int kRowLanes = 16;
 constexpr int kRowTokens = kWave / kRowLanes;
@@ -1044,8 +1059,8 @@ hipError_t launch_gate(const dispatch_gate_problem_t& prob, const void* logits, 
     const void* kernel;
     // Wavefronts of a workgroup, their tokens, the floats in LDS of each and of all.
     int waves, per_wave, row, extra = 0;
-    if (E > 64 && E <= 256 && prob.num_topk >= kFewestRounds && prob.num_topk <= kBest &&
-        prob.num_tokens >= kManyTokens) {
+    const int64_t many = sig && prob.num_topk < kFewestSigmoidRounds ? 2 * kManyTokens : kManyTokens;
+    if (E > 64 && E <= 256 && prob.num_topk >= kFewestRounds && prob.num_topk <= kBest && prob.num_tokens >= many) {
         waves = kRowWaves, per_wave = kRowTokens;
         const int v = E <= 128 ? 8 : 16;
         kernel = v == 8 ? gate_rows_of<8>(half, sig, balance) : gate_rows_of<16>(half, sig, balance);

@@ -548,3 +548,21 @@ def test_gradient_of_many_tokens(t, e, k, sigmoid, dtype):
         bits = torch.int16 if dtype == torch.bfloat16 else torch.int32
         assert torch.equal(got.view(bits), want.view(bits))
         assert m is None or torch.all(got[~md] == 0)
+
+
+@pytest.mark.parametrize("e,k", [(65, 4), (67, 5), (128, 5), (129, 4), (256, 5)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_many_tokens_of_four_and_five_sigmoids(e, k, dtype, monkeypatch):
+    """Either side of the batch from which few sigmoid entries take the form of many tokens."""
+    monkeypatch.setattr(R, "gate", R.gate_table)
+    for t in (2 * 8192 - 1, 2 * 8192 + e):
+        z, mask = _many(t, e, k, dtype, True, e, ties=True)
+        _, out, _ = _check(z, k, True, scale=2.5, mask=mask, exact_choice=False)
+        fp32 = 1.0 / (1.0 + torch.exp(-z.to(DEV).float()))
+        want = torch.sort(fp32, dim=1, descending=True, stable=True).indices[:, :k]
+        rows = mask.to(DEV)
+        rows[:4] = False  # (rows with fewer than k to take)
+        assert torch.equal(out.topk_idx[rows], want[rows])
+        z, mask = _many(t, e, k, dtype, True, e + 1)
+        bias = torch.randn((e,), generator=torch.Generator().manual_seed(e))
+        _check(z, k, True, normalize=False, mask=mask, bias=bias, idx_bytes=4, exact_choice=False)
