@@ -360,7 +360,8 @@ int dispatch_combine(const dispatch_combine_problem_t* problem, const int32_t* e
  *     experts with the largest s + select_bias are taken (the bias moves the
  *     choice alone, no weight).
  *   topk_weights = route_scale * s, divided by the taken experts' sum of s
- *     under DISPATCH_GATE_NORMALIZE.
+ *     under DISPATCH_GATE_NORMALIZE (0 where that sum is: a sigmoid below about
+ *     -88.7 is 0 in fp32).
  *   loss = loss_coef * E / (K * N^2) * sum_e expert_count[e] * prob_sum[e],
  *     prob_sum[e] = sum over the live tokens of p, N = live tokens: loss_coef
  *     when the counts are even.
@@ -433,7 +434,8 @@ int dispatch_gate_backward(const dispatch_gate_problem_t* problem, const void* l
  *   amax = max(largest |x| of the block, 2^-100), sf = amax / 448,
  *   q = x * (448 / amax) rounded to nearest, ties to even.
  * The last block may be short. A block holding NaN or an infinity gives a
- * scale of NaN or infinity and NaN values. x is bf16 and widened to fp32.
+ * scale of NaN or infinity, and values that are NaN by themselves or times that
+ * scale. x is bf16 and widened to fp32.
  * num_valid_rows: device int32 [1] or NULL; rows at or beyond it are neither
  * read nor written (an expert-major buffer's total, &expert_psum[E]).
  * ------------------------------------------------------------------------- */
@@ -470,7 +472,9 @@ int dispatch_swiglu_backward_quantize(const dispatch_quantize_problem_t* problem
  * fp32 sums across them. Within a block the sum is the fp8 matrix
  * instruction's, which drops what is below about 2^-14 of a run's largest
  * product; the SwiGLU product of few rows (at most 16 an expert announced)
- * adds in fp32 there too.
+ * adds in fp32 there too. The two scales are multiplied in fp32 first: a
+ * product of them below 2^-126 loses bits, which moves a block's part of the
+ * result by less than 2^-125, and one past fp32's range is infinite.
  * Pad rows and rows beyond the totals are neither read nor
  * written. The rows' gradient of a product with weights w[E, N, K] is this
  * product with the weights laid out as [E, K, N] and their scales as

@@ -430,6 +430,9 @@ __global__ void __launch_bounds__(Shape::kWaves * kWave, 2) product_kernel(Produ
 #pragma unroll
             for (int m = 0; m < kLive; ++m) {
                 x[m] = read_fragment<Shape::kWide>(x_at + m * Shape::kTokenWaves * 16 * 128, read_lo, read_hi);
+                // (Below 2^-126 the scales' product is rounded to multiples
+                // of 2^-149; a block's sum is under 2^25, so that its part of
+                // the result moves by less than 2^-125, an fp32 underflow.)
                 s[m] = s_at[m * Shape::kTokenWaves * 16] * sw;
             }
             f32x4 y[kLive];

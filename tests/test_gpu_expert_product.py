@@ -414,3 +414,19 @@ def test_swiglu_of_few_rows_in_fp32(counts, k):
         q, sf = q.cpu(), sf.cpu()
         assert torch.all(q[~live] == CANARY) and torch.all(sf[~live] == -7.0)
         R.assert_quantised(q[live].view(R.FP8).float(), sf[live], a, rel)
+
+
+@pytest.mark.parametrize("counts", [[3, 20], [300, 40]], ids=str)
+@pytest.mark.parametrize("x_exp,w_exp", [(-80, -50), (-80, -58), (-70, -79), (-110, -41)])
+def test_scales_whose_product_is_subnormal(counts, x_exp, w_exp):
+    """Their product is rounded to a multiple of 2^-149: each block's part moves by less than 2^-125."""
+    s = _problem(counts, 272, 256, 1, 37)
+    g = torch.Generator().manual_seed(38)
+    s["x_sf"] = (1.0 + torch.rand(s["x_sf"].shape, generator=g)) * 2.0 ** x_exp
+    s["w_sf"] = (1.0 + torch.rand(s["w_sf"].shape, generator=g)) * 2.0 ** w_exp
+    out = _run_product(s)
+    want, mag, top = R.product(s["x"], s["x_sf"], s["w"], s["w_sf"], s["psum"], s["counts"])
+    live = s["live"]
+    # As _check_product, and three blocks' underflow; bf16's own below 2^-126 is 2^-134.
+    bound = 2.0 ** -8 * want.abs() + 19 * EPS * mag + INNER * top + 3 * 2.0 ** -125 + 2.0 ** -134
+    assert torch.all((out.double() - want)[live].abs() <= bound[live])

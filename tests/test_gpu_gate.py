@@ -566,3 +566,16 @@ def test_many_tokens_of_four_and_five_sigmoids(e, k, dtype, monkeypatch):
         z, mask = _many(t, e, k, dtype, True, e + 1)
         bias = torch.randn((e,), generator=torch.Generator().manual_seed(e))
         _check(z, k, True, normalize=False, mask=mask, bias=bias, idx_bytes=4, exact_choice=False)
+
+
+def test_sigmoid_scores_that_are_all_zero():
+    """Logits below -88.7: experts are taken, with weights, shares and gradients of 0."""
+    t, e, k = 20, 70, 4
+    z = torch.full((t, e), -1000.0)
+    z[::2] = -89.0
+    z[5] = torch.finfo(torch.float32).min
+    p, out = _run(z, k, True, True, 2.5, 0.5)
+    assert torch.equal(out.topk_idx.cpu(), torch.arange(k).expand(t, k))
+    assert torch.all(out.topk_weights == 0) and torch.all(out.prob_sum == 0) and float(out.loss) == 0.0
+    dw = torch.randn((t, k), generator=torch.Generator().manual_seed(8))
+    assert torch.all(_gradient(p, z, out, dw, torch.tensor([1.0])) == 0)
