@@ -942,9 +942,13 @@ __global__ void __launch_bounds__(kGateWaves<V> * kWave) gate_backward_kernel(Ga
                 // (Less the gradient of the entry with the largest score, which
                 // changes nothing: a lone entry's weight is constant, and its
                 // gradient exactly 0. Another entry's gradient may be far larger
-                // than all that comes of it, and its rounding would stay.)
-                const uint32_t largest = wave_max(__float_as_uint(mine));
-                const int from = __builtin_ctzll(__ballot(__float_as_uint(mine) == largest));
+                // than all that comes of it, and its rounding would stay.
+                // Softmax entries are in descending order of their scores;
+                // sigmoid's may be of something else. Looked for there too,
+                // 65536 tokens of 256 experts took 26.8 us, 26.0 without.)
+                uint64_t first = __ballot(e >= 0) | uint64_t(1) << (kWave - 1);
+                if (kSigmoid) first = __ballot(__float_as_uint(mine) == wave_max(__float_as_uint(mine)));
+                const int from = __builtin_ctzll(first);
                 dw -= __int_as_float(__builtin_amdgcn_readlane(__float_as_int(dw), from));
                 const float total = wave_sum(mine);
                 if (kSigmoid) {
