@@ -471,8 +471,8 @@ int dispatch_swiglu_backward_quantize(const dispatch_quantize_problem_t* problem
  * with fp8 (e4m3) x and w, blocks of 128 channels (the last may be short) and
  * fp32 sums across them. Within a block the sum is the fp8 matrix
  * instruction's, which drops what is below about 2^-14 of a run's largest
- * product; the SwiGLU product of few rows (at most 16 an expert announced)
- * adds in fp32 there too. The two scales are multiplied in fp32 first: a
+ * product; the SwiGLU product of few rows (decoding: at most 16 an expert
+ * announced, and tiles of 16) adds in fp32 there too. The two scales are multiplied in fp32 first: a
  * product of them below 2^-126 loses bits, which moves a block's part of the
  * result by less than 2^-125, and one past fp32's range is infinite.
  * Pad rows and rows beyond the totals are neither read nor
