@@ -20,9 +20,10 @@
  * rank in the token (the page's dedup "master lane", section 4.2).
  *
  * It also holds the expert layer around the dispatch (last part of this file):
- * the gate that makes topk_idx and its weights, with the balance loss and the
- * logits' gradient; rows to fp8 with a scale per 128 channels; and the experts'
- * fp8 product over recv_x.
+ * the RMS norm before it and its gradient; the gate that makes topk_idx and its
+ * weights, from all experts or from a token's best groups of them, with the
+ * balance loss and the logits' gradient; rows to fp8 with a scale per 128
+ * channels; the experts' fp8 product over recv_x; and the combine's gradient.
  *
  * Conventions for every entry point:
  *   - Ownership: all buffer pointers are device pointers allocated and owned by
@@ -350,6 +351,21 @@ typedef struct dispatch_combine_problem {
 int dispatch_combine(const dispatch_combine_problem_t* problem, const int32_t* expert_slot,
                      const float* topk_weights, const void* y, void* out, hipStream_t stream);
 
+/* Gradient of the combine, from that of out (grad_out: device bf16 [T, H]):
+ *   grad_weights[t, k] = sum over h of grad_out[t, h] * y[expert_slot[t, k], h]
+ *   grad_y[expert_slot[t, k], :] = topk_weights[t, k] * grad_out[t, :]
+ * The first, device fp32 [T, K], is summed in fp32 and 0 where there is no
+ * slot. The second is rounded from fp32 to bf16 (grad_y: device [expert_rows,
+ * H]), or quantised as dispatch_quantize does (grad_q: device bytes
+ * [expert_rows, H], grad_sf: device fp32 [expert_rows, ceil(H / 128)]; H a
+ * multiple of 16), the rows that the experts' product takes; rows that no entry
+ * has (pads) are not written. Outputs that are NULL are left out, but one is
+ * needed, and either grad_y or grad_q may be given. y (as in dispatch_combine)
+ * is needed with grad_weights only. Row pointers are 16-byte aligned. */
+int dispatch_combine_backward(const dispatch_combine_problem_t* problem, const int32_t* expert_slot,
+                              const float* topk_weights, const void* y, const void* grad_out, float* grad_weights,
+                              void* grad_y, void* grad_q, float* grad_sf, hipStream_t stream);
+
 /* ---------------------------------------------------------------------------
  * Gate: the routing table and the top-k weights of a token batch from its
  * router logits z[T, E], with the per-expert counts and the balance loss.
@@ -415,6 +431,31 @@ int dispatch_gate(const dispatch_gate_problem_t* problem, const void* logits, co
                   const uint8_t* token_mask, const dispatch_gate_out_t* out, void* workspace,
                   size_t workspace_bytes, hipStream_t stream);
 
+/* The gate with its choice confined to a token's best groups of experts: group
+ * g holds the E / G experts from g * E / G on (as a rank of the dispatch does
+ * with G = R: a token then goes to at most topk_groups ranks). A group goes by
+ * the largest choice among its experts (z, or s + select_bias), or with
+ * score_experts = 2 by the fp32 sum of its two largest (of a lone one itself);
+ * choices of -inf or NaN do not count. The topk_groups groups with the largest
+ * of these are taken, ties to the lowest group; a group without any choice is
+ * never taken. The K experts come from the taken groups alone; scores, weights,
+ * counts and loss are those of dispatch_gate, over all experts, and
+ * dispatch_gate_backward gives the gradient. Arguments, outputs and workspace
+ * as dispatch_gate's. */
+#define DISPATCH_MAX_GATE_GROUPS 64
+
+typedef struct dispatch_gate_groups {
+    int32_t num_groups;    /* G, 1..DISPATCH_MAX_GATE_GROUPS, E % G == 0 */
+    int32_t topk_groups;   /* 1..G, K <= topk_groups * E / G */
+    int32_t score_experts; /* 1, or with DISPATCH_GATE_SIGMOID 2 */
+    uint32_t reserved;     /* must be 0 */
+} dispatch_gate_groups_t;
+
+int dispatch_gate_grouped(const dispatch_gate_problem_t* problem, const dispatch_gate_groups_t* groups,
+                          const void* logits, const float* select_bias, const uint8_t* token_mask,
+                          const dispatch_gate_out_t* out, void* workspace, size_t workspace_bytes,
+                          hipStream_t stream);
+
 /* Gradient of the logits, grad_logits [T, E] in the logits' type, from the
  * gradient of the weights (grad_weights: device fp32 [T, K], or NULL = 0) and
  * of the loss (grad_loss: device fp32 [1], or NULL = 0). topk_idx,
@@ -462,6 +503,52 @@ int dispatch_swiglu_quantize(const dispatch_quantize_problem_t* problem, const v
  * width must be a multiple of 128. */
 int dispatch_swiglu_backward_quantize(const dispatch_quantize_problem_t* problem, const void* h, const void* grad,
                                       const int32_t* num_valid_rows, void* q, float* sf, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * RMS norm of bf16 rows, with the residual's addition before it:
+ *   h = x + residual, added in fp32 and rounded to bf16 (without a residual h = x),
+ *   y = h * r * weight,  r = 1 / sqrt(mean of h^2 over the row + eps),
+ * in fp32, y rounded to bf16, quantised (from fp32) as dispatch_quantize does,
+ * or both: the rows that the router reads and those that the dispatch moves.
+ * Squares are added in fp32: a row whose sum passes its range has r = 0.
+ * num_valid_rows: device int32 [1] or NULL; rows at or beyond it are neither
+ * read nor written.
+ * ------------------------------------------------------------------------- */
+#define DISPATCH_MAX_NORM_WIDTH 65536
+
+typedef struct dispatch_rms_norm_problem {
+    int64_t num_rows;     /* R, 0..2^31 - 1 */
+    int64_t width;        /* W channels per row, a multiple of 16, 16..DISPATCH_MAX_NORM_WIDTH */
+    int32_t weight_bytes; /* weight: 2 (bf16) or 4 (fp32) */
+    float eps;            /* a normal positive fp32 number */
+} dispatch_rms_norm_problem_t;
+
+/* x: device bf16 [R, W]; residual and h (written): device bf16 [R, W], both or
+ * neither (NULL), h may be x or residual; weight: device [W]; y: device bf16
+ * [R, W] or NULL; q: device bytes [R, W] and sf: device fp32 [R, ceil(W / 128)],
+ * both or neither; y or q is needed. All but sf and num_valid_rows are 16-byte
+ * aligned. One kernel. */
+int dispatch_rms_norm(const dispatch_rms_norm_problem_t* problem, const void* x, const void* residual,
+                      const void* weight, const int32_t* num_valid_rows, void* h, void* y, void* q, float* sf,
+                      hipStream_t stream);
+
+/* Bytes of device workspace for the weight's gradient (256-byte aligned; it
+ * need not be initialised and holds nothing between calls). */
+int dispatch_rms_norm_workspace_size(const dispatch_rms_norm_problem_t* problem, size_t* bytes);
+
+/* The norm's gradient, from that of y (grad_y: device bf16 [R, W]): with
+ * u = h * r and g = grad_y * weight,
+ *   grad_x = r * (g - u * mean over the row of g * u) + grad_h,
+ *   grad_weight = sum over the rows of grad_y * u.
+ * grad_x, device bf16 [R, W], is the gradient of h, and so of x and of the
+ * residual; grad_h: device bf16 [R, W], what comes to h from elsewhere (along
+ * the residual), or NULL; grad_x may be grad_y or grad_h. h is the forward
+ * pass's (x without a residual). grad_weight: device fp32 [W], or NULL, and
+ * then no workspace is needed; its sums do not depend on the order in which
+ * workgroups run. num_valid_rows as above; rows beyond it add nothing. */
+int dispatch_rms_norm_backward(const dispatch_rms_norm_problem_t* problem, const void* h, const void* weight,
+                               const void* grad_y, const void* grad_h, const int32_t* num_valid_rows, void* grad_x,
+                               float* grad_weight, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* ---------------------------------------------------------------------------
  * The experts' product over an expert-major buffer: for every expert e and

@@ -2,9 +2,10 @@
 
 Layout (Count -> Prefix Sum -> stable slots) and row scatter of a token batch
 into a rank-contiguous buffer and an expert-major buffer, as hand-written HIP
-kernels for gfx950 behind a C ABI (``include/moe_dispatch.h``); the combine; and
-the expert layer around them: the gate with its balance loss and gradient, rows
-to fp8, and the experts' fp8 product. This package is the thin Python binding:
+kernels for gfx950 behind a C ABI (``include/moe_dispatch.h``); the combine and
+its gradient; and the expert layer around them: the RMS norm, the gate (from all
+experts or a token's best groups of them) with its balance loss, their
+gradients, rows to fp8, and the experts' fp8 product. This package is the thin Python binding:
 it marshals torch device tensors and the current stream into the C calls.
 """
 
@@ -25,5 +26,8 @@ from ._binding import (  # noqa: F401
     dispatch_expert_product, dispatch_expert_workspace_size,
     dispatch_expert_product_swiglu, dispatch_gate, dispatch_gate_backward, dispatch_gate_workspace_size,
     dispatch_quantize, dispatch_swiglu_backward_quantize, dispatch_swiglu_quantize, make_expert_problem,
-    make_gate_problem,
+    make_gate_problem, MAX_GATE_GROUPS, MAX_NORM_WIDTH, GateGroups, GroupedGatePlan, make_gate_groups,
+    dispatch_gate_grouped, RmsNormBackwardPlan, RmsNormPlan, RmsNormProblem, alloc_rms_norm_workspace,
+    dispatch_rms_norm, dispatch_rms_norm_backward, dispatch_rms_norm_workspace_size, CombineBackwardPlan,
+    dispatch_combine_backward,
 )

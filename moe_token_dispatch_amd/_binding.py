@@ -46,6 +46,8 @@ ROWS_READ_AHEAD = 8  # scatter hint: the rows were just read ahead (changes no r
 GATE_SOFTMAX = 0
 GATE_SIGMOID = 1
 GATE_NORMALIZE = 1
+MAX_GATE_GROUPS = 64
+MAX_NORM_WIDTH = 65536
 SF_BLOCK = 128  # channels per scale factor
 
 
@@ -129,6 +131,17 @@ class GateProblem(ctypes.Structure):
     ]
 
 
+class GateGroups(ctypes.Structure):
+    """dispatch_gate_groups_t."""
+
+    _fields_ = [
+        ("num_groups", ctypes.c_int32),
+        ("topk_groups", ctypes.c_int32),
+        ("score_experts", ctypes.c_int32),
+        ("reserved", ctypes.c_uint32),
+    ]
+
+
 class GateOutPtrs(ctypes.Structure):
     """dispatch_gate_out_t."""
 
@@ -140,6 +153,17 @@ class QuantizeProblem(ctypes.Structure):
     """dispatch_quantize_problem_t."""
 
     _fields_ = [("num_rows", ctypes.c_int64), ("width", ctypes.c_int64)]
+
+
+class RmsNormProblem(ctypes.Structure):
+    """dispatch_rms_norm_problem_t."""
+
+    _fields_ = [
+        ("num_rows", ctypes.c_int64),
+        ("width", ctypes.c_int64),
+        ("weight_bytes", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+    ]
 
 
 class ExpertProblem(ctypes.Structure):
@@ -166,7 +190,8 @@ SYMBOLS = ("dispatch_abi_version", "dispatch_strerror", "dispatch_workspace_size
            "dispatch_expand_scatter", "dispatch_expand_layout_and_scatter", "dispatch_combine",
            "dispatch_gate_workspace_size", "dispatch_gate", "dispatch_gate_backward", "dispatch_quantize",
            "dispatch_swiglu_quantize", "dispatch_swiglu_backward_quantize", "dispatch_expert_workspace_size",
-           "dispatch_expert_product", "dispatch_expert_product_swiglu")
+           "dispatch_expert_product", "dispatch_expert_product_swiglu", "dispatch_gate_grouped", "dispatch_rms_norm",
+           "dispatch_rms_norm_workspace_size", "dispatch_rms_norm_backward", "dispatch_combine_backward")
 
 
 def load_library(path: str = LIB_PATH):
@@ -218,6 +243,7 @@ def load_library(path: str = LIB_PATH):
     lib.dispatch_combine.argtypes = [ctypes.POINTER(CombineProblem), p, p, p, p, p]
     lib.dispatch_combine.restype = i
     gp, qp, xp = ctypes.POINTER(GateProblem), ctypes.POINTER(QuantizeProblem), ctypes.POINTER(ExpertProblem)
+    np = ctypes.POINTER(RmsNormProblem)
     for name, args in (("dispatch_gate_workspace_size", [gp, ctypes.POINTER(sz)]),
                        ("dispatch_gate", [gp, p, p, p, ctypes.POINTER(GateOutPtrs), p, sz, p]),
                        ("dispatch_gate_backward", [gp, p, p, p, p, p, p, p, p, p]),
@@ -226,7 +252,13 @@ def load_library(path: str = LIB_PATH):
                        ("dispatch_swiglu_backward_quantize", [qp, p, p, p, p, p, p]),
                        ("dispatch_expert_workspace_size", [xp, ctypes.POINTER(sz)]),
                        ("dispatch_expert_product", [xp, p, p, p, p, p, p, p, p, sz, p]),
-                       ("dispatch_expert_product_swiglu", [xp, p, p, p, p, p, p, p, p, p, sz, p])):
+                       ("dispatch_expert_product_swiglu", [xp, p, p, p, p, p, p, p, p, p, sz, p]),
+                       ("dispatch_gate_grouped", [gp, ctypes.POINTER(GateGroups), p, p, p, ctypes.POINTER(GateOutPtrs),
+                                                  p, sz, p]),
+                       ("dispatch_rms_norm", [np, p, p, p, p, p, p, p, p, p]),
+                       ("dispatch_rms_norm_workspace_size", [np, ctypes.POINTER(sz)]),
+                       ("dispatch_rms_norm_backward", [np, p, p, p, p, p, p, p, p, sz, p]),
+                       ("dispatch_combine_backward", [ctypes.POINTER(CombineProblem), p, p, p, p, p, p, p, p, p])):
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = i
     if lib.dispatch_abi_version() != ABI_VERSION:
@@ -890,9 +922,78 @@ class CombinePlan:
             raise DispatchError(rc, "dispatch_combine")
 
 
+FP8 = torch.float8_e4m3fn
+
+
+def _check_one_device(tensors) -> torch.device:
+    """The device that all tensors present are on."""
+    devices = {t.device for t in tensors if t is not None}
+    if len(devices) != 1:
+        raise ValueError(f"tensors must be on one device, got {sorted(str(d) for d in devices)}")
+    return devices.pop()
+
+
+class _Prepared:
+    """C arguments built once for one C function; a call makes the tensors'
+    device the current one where it is not (a null stream is the current
+    device's)."""
+
+    def __init__(self, name: str, args, device: torch.device, keep):
+        self._name, self._args, self._keep, self._device = name, args, keep, device.index
+        self._call = getattr(load_library(), name)
+
+    def __call__(self) -> None:
+        if torch.cuda.current_device() == self._device:
+            rc = self._call(*self._args)
+        else:
+            with torch.cuda.device(self._device):
+                rc = self._call(*self._args)
+        if rc:
+            raise DispatchError(rc, self._name)
+
+
+class CombineBackwardPlan(_Prepared):
+    """A prepared dispatch_combine_backward, like Plan."""
+
+    def __init__(self, expert_slot: torch.Tensor, topk_weights: torch.Tensor, y: Optional[torch.Tensor],
+                 grad_out: torch.Tensor, grad_weights: Optional[torch.Tensor] = None,
+                 grad_y: Optional[torch.Tensor] = None, grad_q: Optional[torch.Tensor] = None,
+                 grad_sf: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
+        _check_device_tensor(expert_slot, "expert_slot", torch.int32)
+        _check_device_tensor(topk_weights, "topk_weights", torch.float32)
+        _check_device_tensor(grad_out, "grad_out", torch.bfloat16)
+        rows = [t for t in (y, grad_y, grad_q) if t is not None]
+        if expert_slot.dim() != 2 or grad_out.dim() != 2 or not rows or any(r.dim() != 2 for r in rows):
+            raise ValueError("combine_backward: expert_slot, grad_out and the expert-major rows must be matrices")
+        t, k = expert_slot.shape
+        n, width = rows[0].shape
+        if topk_weights.shape != (t, k) or grad_out.shape != (t, width) or any(r.shape != (n, width) for r in rows):
+            raise ValueError("combine_backward: shapes do not line up")
+        _check_sized(y, "y", n * width, torch.bfloat16)
+        _check_sized(grad_weights, "grad_weights", t * k, torch.float32)
+        _check_sized(grad_y, "grad_y", n * width, torch.bfloat16)
+        _check_sized(grad_q, "grad_q", n * width, FP8, torch.uint8)
+        _check_sized(grad_sf, "grad_sf", n * _sf_blocks(width), torch.float32)
+        tensors = (expert_slot, topk_weights, y, grad_out, grad_weights, grad_y, grad_q, grad_sf)
+        device = _check_one_device(tensors)
+        problem = CombineProblem(t, k, 0, width, n)
+        super().__init__("dispatch_combine_backward", (ctypes.byref(problem), *map(_ptr, tensors),
+                                                       _stream_handle(stream, device)), device, (problem, tensors))
+
+
+def dispatch_combine_backward(expert_slot: torch.Tensor, topk_weights: torch.Tensor, y: Optional[torch.Tensor],
+                              grad_out: torch.Tensor, grad_weights: Optional[torch.Tensor] = None,
+                              grad_y: Optional[torch.Tensor] = None, grad_q: Optional[torch.Tensor] = None,
+                              grad_sf: Optional[torch.Tensor] = None,
+                              stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Enqueue the combine's gradient from grad_out [T, H]: grad_weights [T, K]
+    (needs y), and the expert-major rows' gradient, bf16 grad_y or fp8 grad_q
+    with its scales grad_sf. Rows that no entry has are not written."""
+    CombineBackwardPlan(expert_slot, topk_weights, y, grad_out, grad_weights, grad_y, grad_q, grad_sf, stream)()
+
+
 # ---------------------------------------------------------------------- gate
 
-FP8 = torch.float8_e4m3fn
 _LOGIT_TYPES = {torch.bfloat16: 2, torch.float32: 4}
 _INDEX_TYPES = {4: torch.int32, 8: torch.int64}
 
@@ -1008,6 +1109,36 @@ class GatePlan:
         rc = self._call(*self._args)
         if rc:
             raise DispatchError(rc, "dispatch_gate")
+
+
+def make_gate_groups(num_groups: int, topk_groups: int, score_experts: int = 1) -> GateGroups:
+    """``num_groups`` groups of neighbouring experts, ``topk_groups`` of them for
+    a token, by their largest choice or (``score_experts`` 2, sigmoid scores
+    only) by the sum of their two largest."""
+    return GateGroups(num_groups, topk_groups, score_experts, 0)
+
+
+class GroupedGatePlan(_Prepared):
+    """A prepared dispatch_gate_grouped, like Plan."""
+
+    def __init__(self, problem: GateProblem, groups: GateGroups, logits: torch.Tensor, out: GateTensors,
+                 workspace: Optional[torch.Tensor] = None, select_bias: Optional[torch.Tensor] = None,
+                 token_mask: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
+        problem, groups = GateProblem.from_buffer_copy(problem), GateGroups.from_buffer_copy(groups)
+        (first, *rest), ptrs = _gate_args(problem, logits, out, workspace, select_bias, token_mask, stream)
+        outs = [getattr(out, f.name) for f in dataclasses.fields(out)]
+        device = _check_one_device((logits, workspace, select_bias, token_mask, *outs))
+        super().__init__("dispatch_gate_grouped", (first, ctypes.byref(groups), *rest), device,
+                         (problem, groups, logits, outs, ptrs, workspace, select_bias, token_mask))
+
+
+def dispatch_gate_grouped(problem: GateProblem, groups: GateGroups, logits: torch.Tensor, out: GateTensors,
+                          workspace: Optional[torch.Tensor] = None, select_bias: Optional[torch.Tensor] = None,
+                          token_mask: Optional[torch.Tensor] = None,
+                          stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Enqueue the gate with each token's experts from its best groups (see
+    make_gate_groups); all else as dispatch_gate."""
+    GroupedGatePlan(problem, groups, logits, out, workspace, select_bias, token_mask, stream)()
 
 
 def _gate_backward_args(problem: GateProblem, logits, out: GateTensors, grad_weights, grad_loss, grad_logits,
@@ -1152,6 +1283,96 @@ class SwigluBackwardQuantizePlan(QuantizePlan):
                  num_valid_rows: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
         _check_grad(grad)
         self._prepare(h, grad, q, sf, num_valid_rows, stream)
+
+
+# ------------------------------------------------------------------ RMS norm
+
+_WEIGHT_TYPES = {torch.bfloat16: 2, torch.float32: 4}
+
+
+def _rms_norm_problem(rows: torch.Tensor, name: str, weight: torch.Tensor, eps: float) -> RmsNormProblem:
+    _check_device_tensor(rows, name, torch.bfloat16)
+    if rows.dim() != 2:
+        raise ValueError(f"{name} must be [rows, channels]")
+    _check_sized(weight, "weight", rows.shape[1], *_WEIGHT_TYPES)
+    return RmsNormProblem(rows.shape[0], rows.shape[1], _WEIGHT_TYPES[weight.dtype], eps)
+
+
+class RmsNormPlan(_Prepared):
+    """A prepared dispatch_rms_norm, like Plan."""
+
+    def __init__(self, x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Optional[torch.Tensor] = None,
+                 h: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
+                 sf: Optional[torch.Tensor] = None, num_valid_rows: Optional[torch.Tensor] = None,
+                 stream: Optional[torch.cuda.Stream] = None):
+        problem = _rms_norm_problem(x, "x", weight, eps)
+        size = x.numel()
+        for t, name in ((residual, "residual"), (h, "h"), (y, "y")):
+            _check_sized(t, name, size, torch.bfloat16)
+        _check_sized(q, "q", size, FP8, torch.uint8)
+        _check_sized(sf, "sf", x.shape[0] * _sf_blocks(x.shape[1]), torch.float32)
+        _check_sized(num_valid_rows, "num_valid_rows", 1, torch.int32)
+        tensors = (x, residual, weight, num_valid_rows, h, y, q, sf)
+        device = _check_one_device(tensors)
+        super().__init__("dispatch_rms_norm", (ctypes.byref(problem), *map(_ptr, tensors),
+                                               _stream_handle(stream, device)), device, (problem, tensors))
+
+
+def dispatch_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Optional[torch.Tensor] = None,
+                      h: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                      q: Optional[torch.Tensor] = None, sf: Optional[torch.Tensor] = None,
+                      num_valid_rows: Optional[torch.Tensor] = None,
+                      stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Enqueue h = x + residual and its RMS norm times weight, to bf16 rows y
+    [R, W], to fp8 rows q [R, W] with scales sf [R, ceil(W / 128)], or to both.
+    Without a residual there is no h; h may be x or residual."""
+    RmsNormPlan(x, weight, eps, residual, h, y, q, sf, num_valid_rows, stream)()
+
+
+def dispatch_rms_norm_workspace_size(problem: RmsNormProblem) -> int:
+    out = ctypes.c_size_t(0)
+    rc = load_library().dispatch_rms_norm_workspace_size(ctypes.byref(problem), ctypes.byref(out))
+    if rc:
+        raise DispatchError(rc, "dispatch_rms_norm_workspace_size")
+    return int(out.value)
+
+
+def alloc_rms_norm_workspace(num_rows: int, width: int, device) -> torch.Tensor:
+    """Workspace for the weight's gradient (it need not be initialised)."""
+    problem = RmsNormProblem(num_rows, width, 4, 1.0)
+    return torch.empty(dispatch_rms_norm_workspace_size(problem), dtype=torch.uint8, device=device)
+
+
+class RmsNormBackwardPlan(_Prepared):
+    """A prepared dispatch_rms_norm_backward, like Plan."""
+
+    def __init__(self, h: torch.Tensor, weight: torch.Tensor, grad_y: torch.Tensor, eps: float, grad_x: torch.Tensor,
+                 grad_h: Optional[torch.Tensor] = None, grad_weight: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None, num_valid_rows: Optional[torch.Tensor] = None,
+                 stream: Optional[torch.cuda.Stream] = None):
+        problem = _rms_norm_problem(h, "h", weight, eps)
+        for t, name in ((grad_y, "grad_y"), (grad_h, "grad_h"), (grad_x, "grad_x")):
+            _check_sized(t, name, h.numel(), torch.bfloat16)
+        _check_sized(grad_weight, "grad_weight", h.shape[1], torch.float32)
+        _check_sized(num_valid_rows, "num_valid_rows", 1, torch.int32)
+        nbytes = 0
+        if workspace is not None:
+            _check_device_tensor(workspace, "workspace")
+            nbytes = workspace.numel() * workspace.element_size()
+        tensors = (h, weight, grad_y, grad_h, num_valid_rows, grad_x, grad_weight, workspace)
+        device = _check_one_device(tensors)
+        super().__init__("dispatch_rms_norm_backward", (ctypes.byref(problem), *map(_ptr, tensors), nbytes,
+                                                        _stream_handle(stream, device)), device, (problem, tensors))
+
+
+def dispatch_rms_norm_backward(h: torch.Tensor, weight: torch.Tensor, grad_y: torch.Tensor, eps: float,
+                               grad_x: torch.Tensor, grad_h: Optional[torch.Tensor] = None,
+                               grad_weight: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                               num_valid_rows: Optional[torch.Tensor] = None,
+                               stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Enqueue the norm's gradient: grad_x [R, W], that of h (grad_h is added to
+    it), and grad_weight [W] (needs a workspace)."""
+    RmsNormBackwardPlan(h, weight, grad_y, eps, grad_x, grad_h, grad_weight, workspace, num_valid_rows, stream)()
 
 
 # ---------------------------------------------------------- experts' product

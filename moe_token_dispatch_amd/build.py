@@ -22,7 +22,7 @@ ARCH = "gfx950"
 
 SOURCES = ["dispatch_api.cpp", "dispatch_layout.hip", "dispatch_scatter.hip", "dispatch_combine.hip",
            "dispatch_noalloc.hip", "dispatch_experts_api.cpp", "dispatch_gate.hip", "dispatch_quantize.hip",
-           "dispatch_expert_product.hip"]
+           "dispatch_expert_product.hip", "dispatch_norm.hip", "dispatch_combine_backward.hip"]
 
 HIPCC_FLAGS = [
     f"--offload-arch={ARCH}",

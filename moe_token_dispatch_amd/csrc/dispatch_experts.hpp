@@ -1,5 +1,5 @@
-// Launchers of the gate, the quantisation and the experts' product, called by
-// the C ABI after its host checks, and what sizes their workspaces and grids.
+// Launchers of the gate, the norm, the quantisation, the experts' product and the
+// combine's gradient, called by the C ABI after its host checks, and what sizes their workspaces and grids.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -39,9 +39,10 @@ inline GateWorkspace gate_workspace(int32_t num_experts) {
 }
 inline size_t gate_workspace_bytes(int32_t num_experts) { return gate_workspace(num_experts).bytes; }
 
-hipError_t launch_gate(const dispatch_gate_problem_t& p, const void* logits, const float* select_bias,
-                       const uint8_t* token_mask, const dispatch_gate_out_t& out, void* workspace,
-                       hipStream_t stream);
+// groups: NULL, or the groups that the choice is confined to.
+hipError_t launch_gate(const dispatch_gate_problem_t& p, const dispatch_gate_groups_t* groups, const void* logits,
+                       const float* select_bias, const uint8_t* token_mask, const dispatch_gate_out_t& out,
+                       void* workspace, hipStream_t stream);
 hipError_t launch_gate_backward(const dispatch_gate_problem_t& p, const void* logits, const uint8_t* token_mask,
                                 const void* topk_idx, const float* grad_weights, const int32_t* expert_count,
                                 const int32_t* live_tokens, const float* grad_loss, void* grad_logits,
@@ -50,6 +51,22 @@ hipError_t launch_gate_backward(const dispatch_gate_problem_t& p, const void* lo
 enum class QuantizeSource { kRows, kSwiglu, kSwigluGrad };
 hipError_t launch_quantize(QuantizeSource source, const dispatch_quantize_problem_t& p, const void* x,
                            const void* grad, const int32_t* num_valid_rows, void* q, float* sf, hipStream_t stream);
+
+// The norm's forward pass and its gradient; workspace of
+// rms_norm_workspace_bytes where there is a grad_weight.
+hipError_t launch_rms_norm(const dispatch_rms_norm_problem_t& p, const void* x, const void* residual,
+                           const void* weight, const int32_t* num_valid_rows, void* h, void* y, void* q, float* sf,
+                           hipStream_t stream);
+size_t rms_norm_workspace_bytes(const dispatch_rms_norm_problem_t& p);
+hipError_t launch_rms_norm_backward(const dispatch_rms_norm_problem_t& p, const void* h, const void* weight,
+                                    const void* grad_y, const void* grad_h, const int32_t* num_valid_rows,
+                                    void* grad_x, float* grad_weight, void* workspace, hipStream_t stream);
+
+// grad_weights and the rows' gradient (bf16 grad_y, or grad_q and grad_sf): what is NULL is left out.
+hipError_t launch_combine_backward(const dispatch_combine_problem_t& p, const int32_t* expert_slot,
+                                   const float* topk_weights, const void* y, const void* grad_out,
+                                   float* grad_weights, void* grad_y, void* grad_q, float* grad_sf,
+                                   hipStream_t stream);
 
 // out_sf: not NULL for the product with the SwiGLU and quantisation behind it.
 // workspace: NULL or of expert_workspace_bytes.

@@ -59,6 +59,11 @@ struct GateParams {
     int32_t idx_bytes;
     uint32_t flags;
     float route_scale;
+    int32_t num_groups;  // of a choice by groups, these:
+    int32_t topk_groups;
+    int32_t group_size;   // experts of a group
+    int32_t group_lanes;  // lanes that look at one, as a power of two
+    bool group_pairs;     // a group goes by the sum of its two largest choices
 };
 
 // Wavefronts per workgroup that leave each enough registers for its V
@@ -310,12 +315,71 @@ struct Pairs {
     }
 };
 
+// Two largest keys, and those of two such pairs together.
+struct TopTwo {
+    uint32_t first = kNoKey, second = kNoKey;
+    __device__ __forceinline__ void add(uint32_t key) {
+        const uint32_t low = first < key ? first : key;
+        second = second > low ? second : low;
+        first = first > key ? first : key;
+    }
+    __device__ __forceinline__ void join(uint32_t other, uint32_t next) {
+        second = second > next ? second : next;
+        add(other);
+    }
+    // What a group goes by: its largest choice, or the fp32 sum of its two
+    // largest (of a lone one itself; a sum below fp32's range is its lowest
+    // number, as the group has something to take).
+    __device__ __forceinline__ uint32_t mark(bool pairs) const {
+        if (!pairs || second == kNoKey) return first;
+        const uint32_t sum = order_key(key_value(first) + key_value(second));
+        return sum > kNoKey ? sum : kNoKey + 1;
+    }
+};
+
+// The lane that stands for an expert's group: (e + 0.5) / size is further from
+// a whole number than the product is off, as there are at most 64 groups.
+__device__ __forceinline__ int group_lane(int e, float per_size, int log_lanes) {
+    return (int)(((float)e + 0.5f) * per_size) << log_lanes;
+}
+
+// The groups that a token's experts are taken from, a bit for the first lane
+// of each: the wavefront's keys go through its row in LDS, the lanes of a group
+// look at its experts in turn and join what they found, and the best marks are
+// taken, of equal ones the lowest group's.
+template <int V>
+__device__ __forceinline__ uint64_t open_groups(const uint32_t (&key)[V], float* row, const GateParams& p, int lane) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) row[lane_slot<V>(lane, v)] = __uint_as_float(key[v]);
+    __builtin_amdgcn_wave_barrier();
+    const int lanes = 1 << p.group_lanes, part = lane & (lanes - 1), group = lane >> p.group_lanes;
+    TopTwo top;
+    if (group < p.num_groups) {
+        const int first = group * p.group_size;
+        for (int i = part; i < p.group_size; i += lanes)
+            top.add(__float_as_uint(row[slot_of<V>(first + i, p.num_experts)]));
+    }
+    __builtin_amdgcn_wave_barrier();
+    for (int step = 1; step < lanes; step *= 2)
+        top.join((uint32_t)__shfl_xor((int)top.first, step), (uint32_t)__shfl_xor((int)top.second, step));
+    uint32_t mark = part == 0 ? top.mark(p.group_pairs) : kNoKey;
+    uint64_t open = 0;
+    for (int n = 0; n < p.topk_groups; ++n) {
+        const uint32_t m = wave_max(mark);
+        if (m == kNoKey) break;
+        const int l = __builtin_ctzll(__ballot(mark == m));
+        open |= uint64_t(1) << l;
+        mark = lane == l ? kNoKey : mark;
+    }
+    return open;
+}
+
 // From the sum of counts times probability sums.
 __device__ __forceinline__ float balance_loss(float coef, int E, int K, int live, double sum) {
     return live == 0 ? 0.f : (float)((double)coef * E / ((double)K * live * live) * sum);
 }
 
-template <int V, bool kHalf, bool kSigmoid, bool kBalance>
+template <int V, bool kHalf, bool kSigmoid, bool kBalance, bool kGrouped>
 __global__ void __launch_bounds__(kGateWaves<V> * kWave) gate_kernel(GateParams p) {
     // A row of scores per wavefront, then with kBalance the workgroup's
     // counts [E] and live tokens [1].
@@ -360,6 +424,16 @@ __global__ void __launch_bounds__(kGateWaves<V> * kWave) gate_kernel(GateParams 
 #pragma unroll
         for (int v = 0; v < V; ++v) bias[v] = bias_of(v);
     }
+    const float per_size = kGrouped ? 1.f / (float)p.group_size : 0.f;
+    // Only experts of the token's groups keep their keys.
+    const auto close_groups = [&](uint32_t(&key)[V]) {
+        const uint64_t open = open_groups<V>(key, score_row, p, lane);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int at = group_lane(expert_of<V>(lane, v, E), per_size, p.group_lanes);
+            key[v] = (open >> at) & 1 ? key[v] : kNoKey;
+        }
+    };
     if (t < p.num_tokens) arrive();
     for (; t < p.num_tokens; t += stride) {
         int picked = -1;     // lane k: entry k's slot, then its expert
@@ -379,11 +453,14 @@ __global__ void __launch_bounds__(kGateWaves<V> * kWave) gate_kernel(GateParams 
                     const float b = kKeepBias ? bias[kKeepBias ? v : 0] : bias_of(v);
                     pairs.key[v] = never[v] ? kNoKey : order_key(s[v] + b);
                 }
+                if constexpr (kGrouped) close_groups(pairs.key);
                 pairs.sort();
                 m = pairs.top();
             } else {
 #pragma unroll
                 for (int v = 0; v < V; ++v) pairs.key[v] = order_key(s[v]);
+                // (The largest logit's group is among them.)
+                if constexpr (kGrouped) close_groups(pairs.key);
                 pairs.sort();
                 m = pairs.top();
                 row_sum = scores<V, false>(s, m);
@@ -990,15 +1067,18 @@ __global__ void __launch_bounds__(kGateWaves<V> * kWave) gate_backward_kernel(Ga
     }
 }
 
-template <int V, bool kHalf>
+template <int V, bool kHalf, bool kGrouped>
 const void* gate_kernel_of(bool sigmoid, bool balance) {
     if (sigmoid)
-        return balance ? (const void*)&gate_kernel<V, kHalf, true, true> : (const void*)&gate_kernel<V, kHalf, true, false>;
-    return balance ? (const void*)&gate_kernel<V, kHalf, false, true> : (const void*)&gate_kernel<V, kHalf, false, false>;
+        return balance ? (const void*)&gate_kernel<V, kHalf, true, true, kGrouped>
+                       : (const void*)&gate_kernel<V, kHalf, true, false, kGrouped>;
+    return balance ? (const void*)&gate_kernel<V, kHalf, false, true, kGrouped>
+                   : (const void*)&gate_kernel<V, kHalf, false, false, kGrouped>;
 }
 template <int V>
-const void* gate_kernel_of(bool half, bool sigmoid, bool balance) {
-    return half ? gate_kernel_of<V, true>(sigmoid, balance) : gate_kernel_of<V, false>(sigmoid, balance);
+const void* gate_kernel_of(bool half, bool sigmoid, bool balance, bool grouped) {
+    if (grouped) return half ? gate_kernel_of<V, true, true>(sigmoid, balance) : gate_kernel_of<V, false, true>(sigmoid, balance);
+    return half ? gate_kernel_of<V, true, false>(sigmoid, balance) : gate_kernel_of<V, false, false>(sigmoid, balance);
 }
 template <int V, bool kHalf>
 const void* gate_rows_of(bool sigmoid, bool balance) {
@@ -1032,10 +1112,12 @@ const void* gate_backward_of(bool half, bool sigmoid) {
 
 }  // namespace
 
-hipError_t launch_gate(const dispatch_gate_problem_t& prob, const void* logits, const float* select_bias,
-                       const uint8_t* token_mask, const dispatch_gate_out_t& out, void* workspace,
-                       hipStream_t stream) {
+hipError_t launch_gate(const dispatch_gate_problem_t& prob, const dispatch_gate_groups_t* groups_of,
+                       const void* logits, const float* select_bias, const uint8_t* token_mask,
+                       const dispatch_gate_out_t& out, void* workspace, hipStream_t stream) {
     const int E = prob.num_experts;
+    // (All groups open: the choice is the gate's without them.)
+    const bool grouped = groups_of != nullptr && groups_of->topk_groups < groups_of->num_groups;
     GateParams p{};
     p.logits = logits;
     p.bias = select_bias;
@@ -1057,6 +1139,13 @@ hipError_t launch_gate(const dispatch_gate_problem_t& prob, const void* logits, 
     p.idx_bytes = prob.topk_idx_bytes;
     p.flags = prob.flags;
     p.route_scale = prob.route_scale;
+    if (grouped) {
+        p.num_groups = groups_of->num_groups;
+        p.topk_groups = groups_of->topk_groups;
+        p.group_size = E / p.num_groups;
+        p.group_pairs = groups_of->score_experts == 2;
+        while ((2 << p.group_lanes) * p.num_groups <= kWave) ++p.group_lanes;
+    }
     const bool sig = prob.scoring == DISPATCH_GATE_SIGMOID, half = prob.logits_bytes == 2;
     const bool balance = out.loss != nullptr;
     if (prob.num_tokens == 0 && !balance) return hipSuccess;
@@ -1064,7 +1153,7 @@ hipError_t launch_gate(const dispatch_gate_problem_t& prob, const void* logits, 
     // Wavefronts of a workgroup, their tokens, the floats in LDS of each and of all.
     int waves, per_wave, row, extra = 0;
     const int64_t many = sig && prob.num_topk < kFewestSigmoidRounds ? 2 * kManyTokens : kManyTokens;
-    if (E > 64 && E <= 256 && prob.num_topk >= kFewestRounds && prob.num_topk <= kBest && prob.num_tokens >= many) {
+    if (!grouped && E > 64 && E <= 256 && prob.num_topk >= kFewestRounds && prob.num_topk <= kBest && prob.num_tokens >= many) {
         waves = kRowWaves, per_wave = kRowTokens;
         const int v = E <= 128 ? 8 : 16;
         kernel = v == 8 ? gate_rows_of<8>(half, sig, balance) : gate_rows_of<16>(half, sig, balance);
@@ -1072,7 +1161,7 @@ hipError_t launch_gate(const dispatch_gate_problem_t& prob, const void* logits, 
         extra = sig ? v * kRowLanes : 0;
     } else {
         per_wave = 1;
-#define DISPATCH_F(V) gate_kernel_of<V>(half, sig, balance)
+#define DISPATCH_F(V) gate_kernel_of<V>(half, sig, balance, grouped)
         kernel = DISPATCH_GATE_BY_V(E, DISPATCH_F);
 #undef DISPATCH_F
 #define DISPATCH_F(V) kGateWaves<V>

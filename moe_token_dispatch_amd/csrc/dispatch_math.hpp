@@ -22,6 +22,29 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, v);
 }
 
+// Eight bf16 values of a 16-byte vector as floats, and back.
+typedef uint32_t Bf16x8 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ void widen_bf16(const Bf16x8& w, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[2 * i] = bf16_low(w[i]), v[2 * i + 1] = bf16_high(w[i]);
+}
+__device__ __forceinline__ Bf16x8 narrow_bf16(const float (&v)[8]) {
+    return Bf16x8{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+}
+
+// A 16-byte vector to or from memory, kStream: past the caches.
+template <bool kStream>
+__device__ __forceinline__ Bf16x8 load_vec(const Bf16x8* at) {
+    return kStream ? __builtin_nontemporal_load(at) : *at;
+}
+template <bool kStream>
+__device__ __forceinline__ void store_vec(Bf16x8* at, const Bf16x8& v) {
+    if (kStream)
+        __builtin_nontemporal_store(v, at);
+    else
+        *at = v;
+}
+
 // Four fp32 values rounded to e4m3 (to nearest, ties to even), packed.
 __device__ __forceinline__ uint32_t pack_fp8(float a, float b, float c, float d) {
     int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
@@ -68,20 +91,11 @@ __device__ __forceinline__ float row_sum(float v) {
     return v;
 }
 
-// One block's 8 channels of a lane: quantised to dst, the scale by lane 0.
-// kStream: stored past the caches.
+// A lane's 8 channels over the scale of their block, whose largest magnitude is
+// amax, to dst; `first` also stores the scale. kStream: stored past the caches.
 template <bool kStream>
-__device__ __forceinline__ void quantize8(const float (&v)[8], bool live, bool first, uint8_t* dst, float* sf) {
+__device__ __forceinline__ void scale8(const float (&v)[8], float amax, bool live, bool first, uint8_t* dst, float* sf) {
     typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-    // The largest magnitude by its bits, which order as the values do, NaN
-    // above infinity.
-    uint32_t top = __float_as_uint(kAmaxFloor);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t m = __float_as_uint(v[i]) & 0x7fffffffu;
-        top = top > m ? top : m;
-    }
-    const float amax = __uint_as_float(row_max(top));
     const float scale = kFp8Max / amax;
     const u32x2 o = {pack_fp8(v[0] * scale, v[1] * scale, v[2] * scale, v[3] * scale),
                      pack_fp8(v[4] * scale, v[5] * scale, v[6] * scale, v[7] * scale)};
@@ -92,6 +106,20 @@ __device__ __forceinline__ void quantize8(const float (&v)[8], bool live, bool f
             *reinterpret_cast<u32x2*>(dst) = o;
     }
     if (first) *sf = amax / kFp8Max;
+}
+
+// One block's 8 channels of a lane: quantised to dst, the scale by lane 0.
+template <bool kStream>
+__device__ __forceinline__ void quantize8(const float (&v)[8], bool live, bool first, uint8_t* dst, float* sf) {
+    // The largest magnitude by its bits, which order as the values do, NaN
+    // above infinity.
+    uint32_t top = __float_as_uint(kAmaxFloor);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t m = __float_as_uint(v[i]) & 0x7fffffffu;
+        top = top > m ? top : m;
+    }
+    scale8<kStream>(v, __uint_as_float(row_max(top)), live, first, dst, sf);
 }
 
 // Reductions over the 64 lanes, the result uniform. The order of the sum is

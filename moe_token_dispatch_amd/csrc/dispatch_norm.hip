@@ -1,0 +1,375 @@
+// The RMS norm on gfx950, with the residual's addition before it and bf16 or
+// fp8 rows behind it, and its gradient.
+//
+//   h = bf16(x + residual), r = 1 / sqrt(mean(h^2) + eps), y = h r w
+//   u = h r, g = grad_y w:  grad_x = r (g - u mean(g u)) + grad_h,
+//   grad_w = sum over the rows of grad_y u
+//
+// A row belongs to as many wavefronts as hold it in registers, V vectors of 8
+// channels a lane, so that it is read once; its sums go through LDS. 16
+// neighbouring lanes hold a block of 128 channels, which is quantised from
+// registers as rows of their own are. The gradient needs no statistics kept
+// from the forward pass: the mean of h^2 is added again beside that of g h.
+#include "dispatch_common.hpp"
+#include "dispatch_experts.hpp"
+#include "dispatch_math.hpp"
+
+namespace moe_dispatch {
+namespace {
+
+constexpr int kNormMaxWaves = 16;  // of a workgroup, and so of a row
+constexpr int64_t kMaxNormGroups = 1 << 20;  // larger grids loop
+constexpr int64_t kInfinityCacheBytes = int64_t(256) << 20;
+
+struct NormParams {
+    const Bf16x8* x;
+    const Bf16x8* residual;
+    const void* weight;
+    const int32_t* num_valid_rows;
+    Bf16x8* h;
+    Bf16x8* y;
+    uint8_t* q;
+    float* sf;
+    int64_t num_rows;
+    int32_t vecs;        // vectors of 8 channels in a row
+    int32_t blocks;      // blocks of 128 channels, the last one may be short
+    int32_t row_waves;   // wavefronts of a row
+    int32_t group_rows;  // rows that a workgroup works on at a time
+    float width;
+    float eps;
+    bool weight_half;
+};
+
+__device__ __forceinline__ int64_t rows_of(int64_t num_rows, const int32_t* num_valid_rows) {
+    if (num_valid_rows == nullptr) return num_rows;
+    const int64_t valid = *num_valid_rows;
+    return valid < 0 ? 0 : (valid < num_rows ? valid : num_rows);
+}
+
+__device__ __forceinline__ void load_weight(const void* weight, bool half, int vec, float (&w)[8]) {
+    const Bf16x8* const at = static_cast<const Bf16x8*>(weight);
+    if (half) {
+        widen_bf16(at[vec], w);
+    } else {
+        const Bf16x8 a = at[2 * vec], b = at[2 * vec + 1];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __uint_as_float(a[i]), w[4 + i] = __uint_as_float(b[i]);
+    }
+}
+
+template <int V, bool kStream>
+__global__ void __launch_bounds__(kNormMaxWaves * kWave) norm_kernel(NormParams p) {
+    __shared__ float part[2][kNormMaxWaves];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int mine = wave / p.row_waves;  // which of the workgroup's rows
+    const int first = threadIdx.x - mine * p.row_waves * kWave, step = p.row_waves * kWave;
+    const int64_t rows = rows_of(p.num_rows, p.num_valid_rows);
+    int turn = 0;
+    for (int64_t base = (int64_t)blockIdx.x * p.group_rows; base < rows; base += (int64_t)gridDim.x * p.group_rows) {
+        const int64_t row = base + mine;
+        const bool here = row < rows;
+        const int64_t at = row * p.vecs;
+        Bf16x8 h[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int vec = first + v * step;
+            h[v] = Bf16x8{0, 0, 0, 0};
+            if (here && vec < p.vecs) h[v] = load_vec<kStream>(p.x + at + vec);
+        }
+        if (p.residual != nullptr) {
+            Bf16x8 r[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int vec = first + v * step;
+                r[v] = Bf16x8{0, 0, 0, 0};
+                if (here && vec < p.vecs) r[v] = load_vec<kStream>(p.residual + at + vec);
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int vec = first + v * step;
+                float a[8], b[8];
+                widen_bf16(h[v], a);
+                widen_bf16(r[v], b);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) a[i] += b[i];
+                h[v] = narrow_bf16(a);
+                if (here && vec < p.vecs) store_vec<kStream>(p.h + at + vec, h[v]);
+            }
+        }
+        if (p.y == nullptr && p.q == nullptr) continue;
+        float sum = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float a[8];
+            widen_bf16(h[v], a);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(a[i], a[i], sum);
+        }
+        sum = wave_sum(sum);
+        if (p.row_waves > 1) {
+            // (Two rows of parts in turn: a wavefront may be a row ahead.)
+            if ((threadIdx.x & (kWave - 1)) == 0) part[turn][wave] = sum;
+            __syncthreads();
+            sum = 0.f;
+            for (int w = 0; w < p.row_waves; ++w) sum += part[turn][mine * p.row_waves + w];
+            turn ^= 1;
+        }
+        if (!here) continue;
+        const float r = 1.f / sqrtf(sum / p.width + p.eps);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int vec = first + v * step;
+            const bool live = vec < p.vecs;
+            if ((vec & ~15) >= p.vecs) break;  // (the lanes of a block stay together)
+            float a[8], w[8] = {};
+            widen_bf16(h[v], a);
+            if (live) load_weight(p.weight, p.weight_half, vec, w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) a[i] = a[i] * r * w[i];
+            if (p.y != nullptr && live) store_vec<kStream>(p.y + at + vec, narrow_bf16(a));
+            if (p.q != nullptr)
+                quantize8<kStream>(a, live, vec % 16 == 0, p.q + (at + vec) * 8, p.sf + row * p.blocks + vec / 16);
+        }
+    }
+}
+
+struct NormBackwardParams {
+    const Bf16x8* h;
+    const void* weight;
+    const Bf16x8* grad_y;
+    const Bf16x8* grad_h;
+    const int32_t* num_valid_rows;
+    Bf16x8* grad_x;
+    float* grad_weight;  // a row of sums for each row that the grid works on at a time
+    int64_t num_rows;
+    int32_t vecs;
+    int32_t row_waves;
+    int32_t group_rows;
+    float width;
+    float eps;
+    bool weight_half;
+};
+
+template <int V, bool kStream, bool kWeight>
+__global__ void __launch_bounds__(kNormMaxWaves * kWave) norm_backward_kernel(NormBackwardParams p) {
+    __shared__ float2 part[2][kNormMaxWaves];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int mine = wave / p.row_waves;
+    const int first = threadIdx.x - mine * p.row_waves * kWave, step = p.row_waves * kWave;
+    const int64_t rows = rows_of(p.num_rows, p.num_valid_rows);
+    float dw[kWeight ? V : 1][8] = {};
+    int turn = 0;
+    for (int64_t base = (int64_t)blockIdx.x * p.group_rows; base < rows; base += (int64_t)gridDim.x * p.group_rows) {
+        const int64_t row = base + mine;
+        const int64_t at = row * p.vecs;
+        Bf16x8 h[V], dy[V], dh[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int vec = first + v * step;
+            h[v] = dy[v] = dh[v] = Bf16x8{0, 0, 0, 0};
+            if (row < rows && vec < p.vecs) {
+                h[v] = load_vec<kStream>(p.h + at + vec);
+                dy[v] = load_vec<kStream>(p.grad_y + at + vec);
+                if (p.grad_h != nullptr) dh[v] = load_vec<kStream>(p.grad_h + at + vec);
+            }
+        }
+        float square = 0.f, along = 0.f;
+        float w[V][8] = {};
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int vec = first + v * step;
+            if (vec < p.vecs) load_weight(p.weight, p.weight_half, vec, w[v]);
+            float a[8], d[8];
+            widen_bf16(h[v], a);
+            widen_bf16(dy[v], d);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                square = __builtin_fmaf(a[i], a[i], square);
+                along = __builtin_fmaf(d[i] * w[v][i], a[i], along);
+            }
+        }
+        square = wave_sum(square);
+        along = wave_sum(along);
+        if (p.row_waves > 1) {
+            if ((threadIdx.x & (kWave - 1)) == 0) part[turn][wave] = float2{square, along};
+            __syncthreads();
+            square = along = 0.f;
+            for (int i = 0; i < p.row_waves; ++i) {
+                const float2 x = part[turn][mine * p.row_waves + i];
+                square += x.x;
+                along += x.y;
+            }
+            turn ^= 1;
+        }
+        const float r = 1.f / sqrtf(square / p.width + p.eps);
+        const float mean = along / p.width * r;  // of g u
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int vec = first + v * step;
+            float a[8], d[8], b[8];
+            widen_bf16(h[v], a);
+            widen_bf16(dy[v], d);
+            widen_bf16(dh[v], b);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float u = a[i] * r;
+                if (kWeight) dw[kWeight ? v : 0][i] = __builtin_fmaf(d[i], u, dw[kWeight ? v : 0][i]);
+                b[i] = __builtin_fmaf(r, d[i] * w[v][i] - u * mean, b[i]);
+            }
+            if (row < rows && vec < p.vecs) store_vec<kStream>(p.grad_x + at + vec, narrow_bf16(b));
+        }
+    }
+    if constexpr (kWeight) {
+        float* const to = p.grad_weight + ((int64_t)blockIdx.x * p.group_rows + mine) * p.vecs * 8;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int vec = first + v * step;
+            if (vec >= p.vecs) continue;
+#pragma unroll
+            for (int i = 0; i < 8; i += 4)
+                *reinterpret_cast<float4*>(to + (int64_t)vec * 8 + i) = float4{dw[v][i], dw[v][i + 1], dw[v][i + 2], dw[v][i + 3]};
+        }
+    }
+}
+
+// Adds the rows of sums: a workgroup takes 64 channels, 16 threads of four; its
+// 64 groups of such threads add every 64th row, then the groups are added in
+// order.
+constexpr int kSumThreads = 1024;
+constexpr int kSumLanes = 16;
+constexpr int kSumGroups = kSumThreads / kSumLanes;
+
+__global__ void __launch_bounds__(kSumThreads) norm_sum_kernel(const float4* partial, int rows, int quads, float4* out) {
+    __shared__ float4 part[kSumGroups][kSumLanes];
+    const int g = threadIdx.x / kSumLanes, c = threadIdx.x % kSumLanes;
+    const int quad = blockIdx.x * kSumLanes + c;
+    float4 s{0.f, 0.f, 0.f, 0.f};
+    const auto add = [&](const float4& x) { s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w; };
+    if (quad < quads)
+        for (int row = g; row < rows; row += kSumGroups) add(partial[(int64_t)row * quads + quad]);
+    part[g][c] = s;
+    __syncthreads();
+    if (g != 0 || quad >= quads) return;
+    for (int i = 1; i < kSumGroups; ++i) add(part[i][c]);
+    out[quad] = s;
+}
+
+// How a row is cut: V vectors a lane, wavefronts of a row, rows of a workgroup
+// at a time, workgroups.
+struct NormShape {
+    int v, row_waves, group_rows, groups;
+};
+
+int waves_for(int vecs, int v) { return (vecs + v * kWave - 1) / (v * kWave); }
+
+NormShape norm_shape(int64_t rows, int vecs) {
+    NormShape s;
+    s.v = 1;
+    while (waves_for(vecs, s.v) > kNormMaxWaves) s.v *= 2;
+    if (rows >= 512 && s.v == 1 && vecs > kWave) s.v = 2;
+    s.row_waves = waves_for(vecs, s.v);
+    s.group_rows = s.row_waves >= 4 ? 1 : 4 / s.row_waves;
+    const int64_t groups = (rows + s.group_rows - 1) / s.group_rows;
+    s.groups = (int)(groups < kMaxNormGroups ? groups : kMaxNormGroups);
+    return s;
+}
+
+// The gradient's: each workgroup leaves a row of sums, so there are no more of
+// them than the GPU holds at a time.
+constexpr int kBackwardGroups = 512;
+
+NormShape norm_backward_shape(int64_t rows, int vecs) {
+    NormShape s = norm_shape(rows, vecs);
+    if (s.groups > kBackwardGroups) s.groups = kBackwardGroups;
+    if (s.groups < 1) s.groups = 1;
+    return s;
+}
+
+template <int V>
+const void* norm_kernel_of(bool past) {
+    return past ? (const void*)&norm_kernel<V, true> : (const void*)&norm_kernel<V, false>;
+}
+template <int V>
+const void* norm_backward_of(bool past, bool weight) {
+    if (weight)
+        return past ? (const void*)&norm_backward_kernel<V, true, true> : (const void*)&norm_backward_kernel<V, false, true>;
+    return past ? (const void*)&norm_backward_kernel<V, true, false> : (const void*)&norm_backward_kernel<V, false, false>;
+}
+
+#define DISPATCH_NORM_BY_V(V_, F) ((V_) == 1 ? F(1) : (V_) == 2 ? F(2) : (V_) == 4 ? F(4) : F(8))
+
+}  // namespace
+
+hipError_t launch_rms_norm(const dispatch_rms_norm_problem_t& prob, const void* x, const void* residual,
+                           const void* weight, const int32_t* num_valid_rows, void* h, void* y, void* q, float* sf,
+                           hipStream_t stream) {
+    if (prob.num_rows == 0) return hipSuccess;
+    NormParams p{};
+    p.x = static_cast<const Bf16x8*>(x);
+    p.residual = static_cast<const Bf16x8*>(residual);
+    p.weight = weight;
+    p.num_valid_rows = num_valid_rows;
+    p.h = static_cast<Bf16x8*>(h);
+    p.y = static_cast<Bf16x8*>(y);
+    p.q = static_cast<uint8_t*>(q);
+    p.sf = sf;
+    p.num_rows = prob.num_rows;
+    p.vecs = (int32_t)(prob.width / 8);
+    p.blocks = (int32_t)((prob.width + DISPATCH_SF_BLOCK - 1) / DISPATCH_SF_BLOCK);
+    p.width = (float)prob.width;
+    p.eps = prob.eps;
+    p.weight_half = prob.weight_bytes == 2;
+    const NormShape s = norm_shape(prob.num_rows, p.vecs);
+    p.row_waves = s.row_waves;
+    p.group_rows = s.group_rows;
+    const int64_t channel_bytes = 2 + (residual ? 4 : 0) + (y ? 2 : 0) + (q ? 1 : 0);
+    const bool past = prob.num_rows * prob.width * channel_bytes > kInfinityCacheBytes;
+#define DISPATCH_F(V) norm_kernel_of<V>(past)
+    const void* kernel = DISPATCH_NORM_BY_V(s.v, DISPATCH_F);
+#undef DISPATCH_F
+    void* args[] = {&p};
+    return hipLaunchKernel(kernel, dim3(s.groups), dim3(s.row_waves * s.group_rows * kWave), args, 0, stream);
+}
+
+size_t rms_norm_workspace_bytes(const dispatch_rms_norm_problem_t& prob) {
+    const NormShape s = norm_backward_shape(prob.num_rows, (int)(prob.width / 8));
+    return ((size_t)s.groups * s.group_rows * prob.width * sizeof(float) + 255) & ~size_t(255);
+}
+
+hipError_t launch_rms_norm_backward(const dispatch_rms_norm_problem_t& prob, const void* h, const void* weight,
+                                    const void* grad_y, const void* grad_h, const int32_t* num_valid_rows,
+                                    void* grad_x, float* grad_weight, void* workspace, hipStream_t stream) {
+    if (prob.num_rows == 0 && grad_weight == nullptr) return hipSuccess;
+    NormBackwardParams p{};
+    p.h = static_cast<const Bf16x8*>(h);
+    p.weight = weight;
+    p.grad_y = static_cast<const Bf16x8*>(grad_y);
+    p.grad_h = static_cast<const Bf16x8*>(grad_h);
+    p.num_valid_rows = num_valid_rows;
+    p.grad_x = static_cast<Bf16x8*>(grad_x);
+    p.num_rows = prob.num_rows;
+    p.vecs = (int32_t)(prob.width / 8);
+    p.width = (float)prob.width;
+    p.eps = prob.eps;
+    p.weight_half = prob.weight_bytes == 2;
+    const NormShape s = norm_backward_shape(prob.num_rows, p.vecs);
+    p.row_waves = s.row_waves;
+    p.group_rows = s.group_rows;
+    int rows = s.groups * s.group_rows;
+    p.grad_weight = rows == 1 ? grad_weight : static_cast<float*>(workspace);
+    const bool past = prob.num_rows * prob.width * (grad_h ? 8 : 6) > kInfinityCacheBytes;
+#define DISPATCH_F(V) norm_backward_of<V>(past, grad_weight != nullptr)
+    const void* kernel = DISPATCH_NORM_BY_V(s.v, DISPATCH_F);
+#undef DISPATCH_F
+    void* args[] = {&p};
+    const hipError_t err =
+        hipLaunchKernel(kernel, dim3(s.groups), dim3(s.row_waves * s.group_rows * kWave), args, 0, stream);
+    if (err != hipSuccess || grad_weight == nullptr || rows == 1) return err;
+    const float* partial = p.grad_weight;
+    int quads = (int)(prob.width / 4);
+    void* sum_args[] = {&partial, &rows, &quads, &grad_weight};
+    return hipLaunchKernel((const void*)&norm_sum_kernel, dim3((quads + kSumLanes - 1) / kSumLanes), dim3(kSumThreads),
+                           sum_args, 0, stream);
+}
+
+}  // namespace moe_dispatch
