@@ -19,7 +19,11 @@ namespace {
 
 constexpr int kNormMaxWaves = 16;  // of a workgroup, and so of a row
 constexpr int64_t kMaxNormGroups = 1 << 20;  // larger grids loop
-constexpr int64_t kInfinityCacheBytes = int64_t(256) << 20;
+constexpr int kCus = 256;
+// What moves more than this goes past the caches both ways: most of the Infinity
+// Cache's 256 MB (the gradient of 4096 x 7168, 235 MB: 50.4 us, through the caches
+// 54.4). A smaller result stays where its reader finds it.
+constexpr int64_t kPastBytes = int64_t(192) << 20;
 
 struct NormParams {
     const Bf16x8* x;
@@ -140,7 +144,7 @@ struct NormBackwardParams {
     const Bf16x8* grad_h;
     const int32_t* num_valid_rows;
     Bf16x8* grad_x;
-    float* grad_weight;  // a row of sums for each row that the grid works on at a time
+    float* grad_weight;  // a row of sums for each workgroup
     int64_t num_rows;
     int32_t vecs;
     int32_t row_waves;
@@ -150,42 +154,65 @@ struct NormBackwardParams {
     bool weight_half;
 };
 
+// With one vector a lane the next row is on its way while this one is worked
+// on, and the weight stays in registers: a load of it between the two would be
+// waited for behind the next row's. From four vectors on a row is loaded again
+// for the second look, there is no room for it beside the weight's sums.
 template <int V, bool kStream, bool kWeight>
 __global__ void __launch_bounds__(kNormMaxWaves * kWave) norm_backward_kernel(NormBackwardParams p) {
+    constexpr bool kAhead = V == 1, kKeep = V <= 2;
     __shared__ float2 part[2][kNormMaxWaves];
+    extern __shared__ float4 sums[];  // with kWeight, and rows beside each other: one row
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int mine = wave / p.row_waves;
     const int first = threadIdx.x - mine * p.row_waves * kWave, step = p.row_waves * kWave;
     const int64_t rows = rows_of(p.num_rows, p.num_valid_rows);
+    const int64_t stride = (int64_t)gridDim.x * p.group_rows;
     float dw[kWeight ? V : 1][8] = {};
-    int turn = 0;
-    for (int64_t base = (int64_t)blockIdx.x * p.group_rows; base < rows; base += (int64_t)gridDim.x * p.group_rows) {
-        const int64_t row = base + mine;
-        const int64_t at = row * p.vecs;
-        Bf16x8 h[V], dy[V], dh[V];
+    float kept_w[8] = {};
+    if (kAhead && first < p.vecs) load_weight(p.weight, p.weight_half, first, kept_w);
+    const auto weight_of = [&](int vec, float(&w)[8]) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int vec = first + v * step;
-            h[v] = dy[v] = dh[v] = Bf16x8{0, 0, 0, 0};
-            if (row < rows && vec < p.vecs) {
-                h[v] = load_vec<kStream>(p.h + at + vec);
-                dy[v] = load_vec<kStream>(p.grad_y + at + vec);
-                if (p.grad_h != nullptr) dh[v] = load_vec<kStream>(p.grad_h + at + vec);
-            }
+        for (int i = 0; i < 8; ++i) w[i] = kept_w[i];
+        if (!kAhead && vec < p.vecs) load_weight(p.weight, p.weight_half, vec, w);
+    };
+    const auto load = [&](const Bf16x8* from, int64_t row, int v) {
+        const int vec = first + v * step;
+        if (from == nullptr || row >= rows || vec >= p.vecs) return Bf16x8{0, 0, 0, 0};
+        return load_vec<kStream>(from + row * p.vecs + vec);
+    };
+    int turn = 0;
+    Bf16x8 next_h, next_dy, next_dh;
+    const auto load_next = [&](int64_t row) {
+        next_h = load(p.h, row, 0);
+        next_dy = load(p.grad_y, row, 0);
+        next_dh = load(p.grad_h, row, 0);
+    };
+    int64_t base = (int64_t)blockIdx.x * p.group_rows;
+    if (kAhead && base < rows) load_next(base + mine);
+    for (; base < rows; base += stride) {
+        const int64_t row = base + mine;
+        Bf16x8 h[V], dy[V], dh;
+        if constexpr (kAhead) {
+            h[0] = next_h, dy[0] = next_dy, dh = next_dh;
+            if (base + stride < rows) load_next(row + stride);
         }
         float square = 0.f, along = 0.f;
-        float w[V][8] = {};
+        if (kKeep && !kAhead) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) h[v] = load(p.h, row, v), dy[v] = load(p.grad_y, row, v);
+        }
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int vec = first + v * step;
-            if (vec < p.vecs) load_weight(p.weight, p.weight_half, vec, w[v]);
-            float a[8], d[8];
+            float a[8], d[8], w[8];
+            if (!kKeep) h[v] = load(p.h, row, v), dy[v] = load(p.grad_y, row, v);
+            weight_of(first + v * step, w);
             widen_bf16(h[v], a);
             widen_bf16(dy[v], d);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 square = __builtin_fmaf(a[i], a[i], square);
-                along = __builtin_fmaf(d[i] * w[v][i], a[i], along);
+                along = __builtin_fmaf(d[i] * w[i], a[i], along);
             }
         }
         square = wave_sum(square);
@@ -206,51 +233,80 @@ __global__ void __launch_bounds__(kNormMaxWaves * kWave) norm_backward_kernel(No
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int vec = first + v * step;
-            float a[8], d[8], b[8];
+            float a[8], d[8], b[8], w[8];
+            if (!kKeep) h[v] = load(p.h, row, v), dy[v] = load(p.grad_y, row, v);
+            if (!kAhead) dh = load(p.grad_h, row, v);
+            weight_of(vec, w);
             widen_bf16(h[v], a);
             widen_bf16(dy[v], d);
-            widen_bf16(dh[v], b);
+            widen_bf16(dh, b);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float u = a[i] * r;
                 if (kWeight) dw[kWeight ? v : 0][i] = __builtin_fmaf(d[i], u, dw[kWeight ? v : 0][i]);
-                b[i] = __builtin_fmaf(r, d[i] * w[v][i] - u * mean, b[i]);
+                b[i] = __builtin_fmaf(r, d[i] * w[i] - u * mean, b[i]);
             }
-            if (row < rows && vec < p.vecs) store_vec<kStream>(p.grad_x + at + vec, narrow_bf16(b));
+            if (row < rows && vec < p.vecs) store_vec<kStream>(p.grad_x + row * p.vecs + vec, narrow_bf16(b));
         }
     }
     if constexpr (kWeight) {
-        float* const to = p.grad_weight + ((int64_t)blockIdx.x * p.group_rows + mine) * p.vecs * 8;
+        // The workgroup's rows of sums, one after the other.
+        float4* const to = reinterpret_cast<float4*>(p.grad_weight) + (int64_t)blockIdx.x * p.vecs * 2;
+        for (int turn = 0; turn < p.group_rows; ++turn) {
+            if (turn == mine) {
+                const bool last = turn == p.group_rows - 1;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int vec = first + v * step;
-            if (vec >= p.vecs) continue;
+                for (int v = 0; v < V; ++v) {
+                    const int vec = first + v * step;
+                    if (vec >= p.vecs) continue;
 #pragma unroll
-            for (int i = 0; i < 8; i += 4)
-                *reinterpret_cast<float4*>(to + (int64_t)vec * 8 + i) = float4{dw[v][i], dw[v][i + 1], dw[v][i + 2], dw[v][i + 3]};
+                    for (int i = 0; i < 2; ++i) {
+                        float4 x{dw[v][4 * i], dw[v][4 * i + 1], dw[v][4 * i + 2], dw[v][4 * i + 3]};
+                        if (turn > 0) {
+                            const float4 y = sums[2 * vec + i];
+                            x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+                        }
+                        (last ? to : sums)[2 * vec + i] = x;
+                    }
+                }
+            }
+            if (p.group_rows > 1) __syncthreads();
         }
     }
 }
 
-// Adds the rows of sums: a workgroup takes 64 channels, 16 threads of four; its
-// 64 groups of such threads add every 64th row, then the groups are added in
-// order.
+// Adds the rows of sums: a workgroup takes 32 channels, 8 threads of four; its
+// 128 groups of such threads add every 128th row, eight of them on their way at
+// once, then the groups of a wavefront and the wavefronts are added in order.
 constexpr int kSumThreads = 1024;
-constexpr int kSumLanes = 16;
+constexpr int kSumLanes = 8;
 constexpr int kSumGroups = kSumThreads / kSumLanes;
 
 __global__ void __launch_bounds__(kSumThreads) norm_sum_kernel(const float4* partial, int rows, int quads, float4* out) {
-    __shared__ float4 part[kSumGroups][kSumLanes];
+    __shared__ float4 part[kSumThreads / kWave][kSumLanes];
     const int g = threadIdx.x / kSumLanes, c = threadIdx.x % kSumLanes;
     const int quad = blockIdx.x * kSumLanes + c;
     float4 s{0.f, 0.f, 0.f, 0.f};
     const auto add = [&](const float4& x) { s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w; };
-    if (quad < quads)
-        for (int row = g; row < rows; row += kSumGroups) add(partial[(int64_t)row * quads + quad]);
-    part[g][c] = s;
+    if (quad < quads) {
+        constexpr int kAtOnce = 4;
+        for (int row = g; row < rows; row += kAtOnce * kSumGroups) {
+            float4 x[kAtOnce];
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                const int at = row + i * kSumGroups;
+                x[i] = at < rows ? partial[(int64_t)at * quads + quad] : float4{0.f, 0.f, 0.f, 0.f};
+            }
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) add(x[i]);
+        }
+    }
+    for (int step = kSumLanes; step < kWave; step *= 2)
+        add(float4{__shfl_xor(s.x, step), __shfl_xor(s.y, step), __shfl_xor(s.z, step), __shfl_xor(s.w, step)});
+    if (threadIdx.x % kWave < kSumLanes) part[threadIdx.x / kWave][c] = s;
     __syncthreads();
-    if (g != 0 || quad >= quads) return;
-    for (int i = 1; i < kSumGroups; ++i) add(part[i][c]);
+    if (threadIdx.x >= kSumLanes || quad >= quads) return;
+    for (int i = 1; i < kSumThreads / kWave; ++i) add(part[i][c]);
     out[quad] = s;
 }
 
@@ -262,11 +318,14 @@ struct NormShape {
 
 int waves_for(int vecs, int v) { return (vecs + v * kWave - 1) / (v * kWave); }
 
+// One vector a lane for few rows, which are bound by latency; two from two
+// rows per CU on (4096 x 7168 channels 46.3 us, 49.1 with one and 47.8 with
+// four; 333 x 4096 4.5 us with one, 4.7 with two). Narrow rows share a
+// workgroup of four wavefronts.
 NormShape norm_shape(int64_t rows, int vecs) {
     NormShape s;
-    s.v = 1;
+    s.v = rows >= 512 && vecs > kWave ? 2 : 1;
     while (waves_for(vecs, s.v) > kNormMaxWaves) s.v *= 2;
-    if (rows >= 512 && s.v == 1 && vecs > kWave) s.v = 2;
     s.row_waves = waves_for(vecs, s.v);
     s.group_rows = s.row_waves >= 4 ? 1 : 4 / s.row_waves;
     const int64_t groups = (rows + s.group_rows - 1) / s.group_rows;
@@ -274,14 +333,20 @@ NormShape norm_shape(int64_t rows, int vecs) {
     return s;
 }
 
-// The gradient's: each workgroup leaves a row of sums, so there are no more of
-// them than the GPU holds at a time.
-constexpr int kBackwardGroups = 512;
-
+// The gradient's workgroups each leave a row of sums, so there are few: 8 to 16
+// wavefronts per CU, whose next rows are on their way, with narrow rows beside
+// each other in a workgroup (8191 x 2064: 26.6 to 27.2 us with 15 to 20
+// wavefronts of one row per CU, 34.7 without the next row's loads; 20000 x 512:
+// 18.9 us, 29.4 with a row of sums for every row at work).
 NormShape norm_backward_shape(int64_t rows, int vecs) {
-    NormShape s = norm_shape(rows, vecs);
-    if (s.groups > kBackwardGroups) s.groups = kBackwardGroups;
-    if (s.groups < 1) s.groups = 1;
+    NormShape s;
+    s.v = 1;
+    while (waves_for(vecs, s.v) > kNormMaxWaves) s.v *= 2;
+    s.row_waves = waves_for(vecs, s.v);
+    s.group_rows = s.row_waves >= 8 ? 1 : 8 / s.row_waves;
+    const int most = kCus * (kNormMaxWaves / (s.row_waves * s.group_rows));
+    const int64_t groups = (rows + s.group_rows - 1) / s.group_rows;
+    s.groups = groups < 1 ? 1 : (int)(groups < most ? groups : most);
     return s;
 }
 
@@ -323,7 +388,7 @@ hipError_t launch_rms_norm(const dispatch_rms_norm_problem_t& prob, const void* 
     p.row_waves = s.row_waves;
     p.group_rows = s.group_rows;
     const int64_t channel_bytes = 2 + (residual ? 4 : 0) + (y ? 2 : 0) + (q ? 1 : 0);
-    const bool past = prob.num_rows * prob.width * channel_bytes > kInfinityCacheBytes;
+    const bool past = prob.num_rows * prob.width * channel_bytes > kPastBytes;
 #define DISPATCH_F(V) norm_kernel_of<V>(past)
     const void* kernel = DISPATCH_NORM_BY_V(s.v, DISPATCH_F);
 #undef DISPATCH_F
@@ -333,7 +398,7 @@ hipError_t launch_rms_norm(const dispatch_rms_norm_problem_t& prob, const void* 
 
 size_t rms_norm_workspace_bytes(const dispatch_rms_norm_problem_t& prob) {
     const NormShape s = norm_backward_shape(prob.num_rows, (int)(prob.width / 8));
-    return ((size_t)s.groups * s.group_rows * prob.width * sizeof(float) + 255) & ~size_t(255);
+    return ((size_t)s.groups * prob.width * sizeof(float) + 255) & ~size_t(255);
 }
 
 hipError_t launch_rms_norm_backward(const dispatch_rms_norm_problem_t& prob, const void* h, const void* weight,
@@ -355,15 +420,16 @@ hipError_t launch_rms_norm_backward(const dispatch_rms_norm_problem_t& prob, con
     const NormShape s = norm_backward_shape(prob.num_rows, p.vecs);
     p.row_waves = s.row_waves;
     p.group_rows = s.group_rows;
-    int rows = s.groups * s.group_rows;
+    int rows = s.groups;
     p.grad_weight = rows == 1 ? grad_weight : static_cast<float*>(workspace);
-    const bool past = prob.num_rows * prob.width * (grad_h ? 8 : 6) > kInfinityCacheBytes;
+    const bool past = prob.num_rows * prob.width * (grad_h ? 8 : 6) > kPastBytes;
 #define DISPATCH_F(V) norm_backward_of<V>(past, grad_weight != nullptr)
     const void* kernel = DISPATCH_NORM_BY_V(s.v, DISPATCH_F);
 #undef DISPATCH_F
     void* args[] = {&p};
+    const size_t shared = s.group_rows > 1 && grad_weight != nullptr ? prob.width * sizeof(float) : 0;
     const hipError_t err =
-        hipLaunchKernel(kernel, dim3(s.groups), dim3(s.row_waves * s.group_rows * kWave), args, 0, stream);
+        hipLaunchKernel(kernel, dim3(s.groups), dim3(s.row_waves * s.group_rows * kWave), args, shared, stream);
     if (err != hipSuccess || grad_weight == nullptr || rows == 1) return err;
     const float* partial = p.grad_weight;
     int quads = (int)(prob.width / 4);
