@@ -650,12 +650,115 @@ __device__ __forceinline__ int quad_slot(int e, int32_t E) {
     return past == 0 || e < E - past ? e : e + 4 - past;
 }
 
-template <int V, bool kHalf, bool kSigmoid, bool kBalance>
+// Choice by groups, where a group is a number of whole runs and there are at
+// most 16: a lane finds the two largest keys of each of its runs, which go
+// through LDS, and the token's 16 lanes, Gp of them side by side for the groups
+// (Gp a power of two), join those of their group, the lanes that share one by
+// rotations. All of these have its mark then, and a group's place is the number
+// of marks above its own, of equal ones of lower groups: Gp - 1 rotations. (A
+// maximum and its removal for each group taken: 14 instructions for each of
+// them, where a rotation takes 4.) Looking for the groups takes longer in the
+// form of one token per wavefront, so this one is taken from 8192 tokens on
+// whatever the number of entries. Measured, 8 groups, 4 taken, us of this form
+// and of the other with k = 1, 4 and 8, without / with balance outputs:
+//
+//   softmax of fp32         here            k = 1         4            8
+//   128 experts,  4096   5.1 / 11.5    4.5 / 10.5   5.1 / 11.6   5.2 / 11.7
+//                 8192   4.9 / 11.8    5.5 / 12.4   6.2 / 13.1   7.1 / 14.1
+//                65536  19.1 / 27.5   26.0 / 39.7  30.3 / 47.5  36.5 / 58.1
+//   256 experts,  4096   5.9 / 12.7    4.9 / 11.1   5.6 / 11.6   6.8 / 12.6
+//                 8192   5.6 / 12.9    6.4 / 13.2   7.7 / 14.4   9.2 / 16.4
+//                65536  26.4 / 36.3   32.5 / 47.4  39.6 / 60.2  52.1 / 77.3
+//   sigmoid of bf16, pairs
+//   256 experts,  4096   7.9 / 15.1    6.0 / 12.3   6.6 / 12.6   7.4 / 13.7
+//                 8192   7.8 / 15.7    8.1 / 14.2   9.1 / 15.8  10.8 / 17.9
+//                65536  37.8 / 48.3   40.9 / 60.4  48.0 / 72.6  59.7 / 88.7
+constexpr int kMostRowGroups = kRowLanes;
+constexpr int kRunsStride = 8;  // words between the tokens' runs, so that they start in other banks
+
+__device__ __host__ constexpr int row_floats(int v, bool sigmoid, bool grouped) {
+    const int scores = (sigmoid ? kRowTokens : 1) * v * kRowLanes;
+    const int runs = grouped ? kRowTokens * (v * kRowLanes / 2 + kRunsStride) : 0;
+    return scores > runs ? scores : runs;
+}
+
+// With the lane N places on in a row of 16.
+template <int N>
+__device__ __forceinline__ void join_rotated(TopTwo& top) {
+    const uint32_t first = dpp_ror<kDppRowRor + N>(top.first), second = dpp_ror<kDppRowRor + N>(top.second);
+    top.join(first, second);
+}
+
+// Adds 1 where the mark N groups before (modulo Gp) goes before this one.
+template <int N>
+__device__ __forceinline__ void count_before(uint32_t mark, int group, int& place) {
+    place += dpp_ror<kDppRowRor + N>(mark) + (group >= N ? 1u : 0u) > mark ? 1 : 0;
+}
+
+// A bit for each group of the lane's token that is open.
+template <int V>
+__device__ __forceinline__ uint32_t open_row_groups(const uint32_t (&key)[V], float* runs_of, const GateParams& p,
+                                                    int lane) {
+    const int c = lane % kRowLanes;
+    uint2* const runs = reinterpret_cast<uint2*>(runs_of + lane / kRowLanes * (V * kRowLanes / 2 + kRunsStride));
+#pragma unroll
+    for (int v = 0; v < V; v += 4) {
+        TopTwo run;
+        const uint32_t a = key[v], b = key[v + 1], d = key[v + 2], e = key[v + 3];
+        run.first = a > b ? a : b;
+        run.second = a > b ? b : a;
+        run.join(d > e ? d : e, d > e ? e : d);
+        runs[v / 4 * kRowLanes + c] = uint2{run.first, run.second};
+    }
+    __builtin_amdgcn_wave_barrier();
+    const int side = kRowLanes >> p.group_lanes;  // Gp
+    const int group = c & (side - 1), size = p.group_size / 4;
+    TopTwo top;
+    if (group < p.num_groups) {
+        for (int i = c / side; i < size; i += 1 << p.group_lanes) {
+            const uint2 run = runs[group * size + i];
+            top.join(run.x, run.y);
+        }
+    }
+    __builtin_amdgcn_wave_barrier();
+    if (side <= 1) join_rotated<1>(top);
+    if (side <= 2) join_rotated<2>(top);
+    if (side <= 4) join_rotated<4>(top);
+    if (side <= 8) join_rotated<8>(top);
+    const uint32_t mark = top.mark(p.group_pairs);
+    int place = 0;
+    if (side > 1) count_before<1>(mark, group, place);
+    if (side > 2) {
+        count_before<2>(mark, group, place);
+        count_before<3>(mark, group, place);
+    }
+    if (side > 4) {
+        count_before<4>(mark, group, place);
+        count_before<5>(mark, group, place);
+        count_before<6>(mark, group, place);
+        count_before<7>(mark, group, place);
+    }
+    if (side > 8) {
+        count_before<8>(mark, group, place);
+        count_before<9>(mark, group, place);
+        count_before<10>(mark, group, place);
+        count_before<11>(mark, group, place);
+        count_before<12>(mark, group, place);
+        count_before<13>(mark, group, place);
+        count_before<14>(mark, group, place);
+        count_before<15>(mark, group, place);
+    }
+    const uint64_t open = __ballot(place < p.topk_groups && mark != kNoKey);
+    const uint32_t half = lane < kWave / 2 ? (uint32_t)open : (uint32_t)(open >> 32);
+    return (half >> (lane & kRowLanes)) & (uint32_t)(side == 16 ? 0xffff : (1 << side) - 1);
+}
+
+template <int V, bool kHalf, bool kSigmoid, bool kBalance, bool kGrouped>
 __global__ void __launch_bounds__(kRowWaves * kWave, 4) gate_rows_kernel(GateParams p) {
-    // Sigmoid: the wavefront's rows of scores; balance: its sums; then of the
-    // workgroup, sigmoid: a row of the selection bias; balance: counts [E] and
-    // live tokens [1].
-    constexpr int kWaveFloats = (kSigmoid ? kRowTokens : 1) * V * kRowLanes;
+    // Sigmoid: the wavefront's rows of scores; groups: its tokens' runs;
+    // balance: its sums; then of the workgroup, sigmoid: a row of the selection
+    // bias; balance: counts [E] and live tokens [1].
+    constexpr int kWaveFloats = row_floats(V, kSigmoid, kGrouped);
     extern __shared__ float lds[];
     const int lane = threadIdx.x & (kWave - 1), c = lane % kRowLanes;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -711,6 +814,15 @@ __global__ void __launch_bounds__(kRowWaves * kWave, 4) gate_rows_kernel(GatePar
             s[v] = taken && quad.first + v % 4 >= quad.start ? z : kNone;
         }
     };
+    // The groups of the lane's runs; what is past the last group is never open.
+    int run_group[V / 4] = {};
+    if constexpr (kGrouped) {
+#pragma unroll
+        for (int j = 0; j < V / 4; ++j) {
+            const int group = (j * kRowLanes + c) * 4 / p.group_size;
+            run_group[j] = group < kMostRowGroups ? group : kMostRowGroups;
+        }
+    }
     if (t0 < p.num_tokens) load(t0);
     if (t0 < p.num_tokens) arrive();
     for (; t0 < p.num_tokens; t0 += stride) {
@@ -718,20 +830,26 @@ __global__ void __launch_bounds__(kRowWaves * kWave, 4) gate_rows_kernel(GatePar
         const bool now = taken;
         float sum = 0.f;
         double best[kBest], more[kBest];
-        const auto place = [&](int v, uint32_t key) {
-            (v < kBest ? best : more)[v % kBest] = numbered(key, Quad<V>(c, v, E).first + v % 4);
-        };
+        uint32_t keys[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             if constexpr (kSigmoid) {
                 const bool never = !(s[v] > kNone);
                 s[v] = s[v] == kNone ? 0.f : sigmoid(s[v]);
                 sum += s[v];
-                place(v, never ? kNoKey : order_key(s[v] + bias[(v / 4 * kRowLanes + c) * 4 + v % 4]));
+                keys[v] = never ? kNoKey : order_key(s[v] + bias[(v / 4 * kRowLanes + c) * 4 + v % 4]);
             } else {
-                place(v, order_key(s[v]));
+                keys[v] = order_key(s[v]);
             }
         }
+        if constexpr (kGrouped) {
+            const uint32_t open = open_row_groups<V>(keys, mine, p, lane);
+#pragma unroll
+            for (int v = 0; v < V; ++v) keys[v] = (open >> run_group[v / 4]) & 1 ? keys[v] : kNoKey;
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            (v < kBest ? best : more)[v % kBest] = numbered(keys[v], Quad<V>(c, v, E).first + v % 4);
         sort(best);
         if constexpr (V > kBest) {
             sort(more);
@@ -1080,17 +1198,18 @@ const void* gate_kernel_of(bool half, bool sigmoid, bool balance, bool grouped) 
     if (grouped) return half ? gate_kernel_of<V, true, true>(sigmoid, balance) : gate_kernel_of<V, false, true>(sigmoid, balance);
     return half ? gate_kernel_of<V, true, false>(sigmoid, balance) : gate_kernel_of<V, false, false>(sigmoid, balance);
 }
-template <int V, bool kHalf>
+template <int V, bool kHalf, bool kGrouped>
 const void* gate_rows_of(bool sigmoid, bool balance) {
     if (sigmoid)
-        return balance ? (const void*)&gate_rows_kernel<V, kHalf, true, true>
-                       : (const void*)&gate_rows_kernel<V, kHalf, true, false>;
-    return balance ? (const void*)&gate_rows_kernel<V, kHalf, false, true>
-                   : (const void*)&gate_rows_kernel<V, kHalf, false, false>;
+        return balance ? (const void*)&gate_rows_kernel<V, kHalf, true, true, kGrouped>
+                       : (const void*)&gate_rows_kernel<V, kHalf, true, false, kGrouped>;
+    return balance ? (const void*)&gate_rows_kernel<V, kHalf, false, true, kGrouped>
+                   : (const void*)&gate_rows_kernel<V, kHalf, false, false, kGrouped>;
 }
 template <int V>
-const void* gate_rows_of(bool half, bool sigmoid, bool balance) {
-    return half ? gate_rows_of<V, true>(sigmoid, balance) : gate_rows_of<V, false>(sigmoid, balance);
+const void* gate_rows_of(bool half, bool sigmoid, bool balance, bool grouped) {
+    if (grouped) return half ? gate_rows_of<V, true, true>(sigmoid, balance) : gate_rows_of<V, false, true>(sigmoid, balance);
+    return half ? gate_rows_of<V, true, false>(sigmoid, balance) : gate_rows_of<V, false, false>(sigmoid, balance);
 }
 
 template <int V>
@@ -1144,7 +1263,6 @@ hipError_t launch_gate(const dispatch_gate_problem_t& prob, const dispatch_gate_
         p.topk_groups = groups_of->topk_groups;
         p.group_size = E / p.num_groups;
         p.group_pairs = groups_of->score_experts == 2;
-        while ((2 << p.group_lanes) * p.num_groups <= kWave) ++p.group_lanes;
     }
     const bool sig = prob.scoring == DISPATCH_GATE_SIGMOID, half = prob.logits_bytes == 2;
     const bool balance = out.loss != nullptr;
@@ -1152,12 +1270,20 @@ hipError_t launch_gate(const dispatch_gate_problem_t& prob, const dispatch_gate_
     const void* kernel;
     // Wavefronts of a workgroup, their tokens, the floats in LDS of each and of all.
     int waves, per_wave, row, extra = 0;
-    const int64_t many = sig && prob.num_topk < kFewestSigmoidRounds ? 2 * kManyTokens : kManyTokens;
-    if (!grouped && E > 64 && E <= 256 && prob.num_topk >= kFewestRounds && prob.num_topk <= kBest && prob.num_tokens >= many) {
+    const int64_t many = !grouped && sig && prob.num_topk < kFewestSigmoidRounds ? 2 * kManyTokens : kManyTokens;
+    const int fewest = grouped ? 1 : kFewestRounds;
+    const bool by_runs = !grouped || (p.group_size % 4 == 0 && p.num_groups <= kMostRowGroups);
+    const bool rows_form = E > 64 && E <= 256 && prob.num_topk >= fewest && prob.num_topk <= kBest &&
+                           prob.num_tokens >= many && by_runs;
+    if (grouped) {
+        const int lanes = rows_form ? kRowLanes : kWave;
+        while ((2 << p.group_lanes) * p.num_groups <= lanes) ++p.group_lanes;
+    }
+    if (rows_form) {
         waves = kRowWaves, per_wave = kRowTokens;
         const int v = E <= 128 ? 8 : 16;
-        kernel = v == 8 ? gate_rows_of<8>(half, sig, balance) : gate_rows_of<16>(half, sig, balance);
-        row = (sig ? kRowTokens : 1) * v * kRowLanes;
+        kernel = v == 8 ? gate_rows_of<8>(half, sig, balance, grouped) : gate_rows_of<16>(half, sig, balance, grouped);
+        row = row_floats(v, sig, grouped);
         extra = sig ? v * kRowLanes : 0;
     } else {
         per_wave = 1;
