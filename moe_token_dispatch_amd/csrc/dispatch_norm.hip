@@ -10,6 +10,10 @@
 // neighbouring lanes hold a block of 128 channels, which is quantised from
 // registers as rows of their own are. The gradient needs no statistics kept
 // from the forward pass: the mean of h^2 is added again beside that of g h.
+//
+// HBM bounds both: 4096 x 7168 with the residual to bf16 and fp8 rows 46.2 us
+// for 265 MB (5.7 TB/s), the gradient 45.6 us for 235 MB (5.2 TB/s, the weight's
+// sums 4 of them). One row takes 4.2 us, which is the launch.
 #include "dispatch_common.hpp"
 #include "dispatch_experts.hpp"
 #include "dispatch_math.hpp"
@@ -20,10 +24,10 @@ namespace {
 constexpr int kNormMaxWaves = 16;  // of a workgroup, and so of a row
 constexpr int64_t kMaxNormGroups = 1 << 20;  // larger grids loop
 constexpr int kCus = 256;
-// What moves more than this goes past the caches both ways: most of the Infinity
-// Cache's 256 MB (the gradient of 4096 x 7168, 235 MB: 50.4 us, through the caches
-// 54.4). A smaller result stays where its reader finds it.
-constexpr int64_t kPastBytes = int64_t(192) << 20;
+// What moves more goes past the caches both ways (the gradient of 4096 x 7168,
+// 235 MB: 50.4 us, through the caches 54.4; 20000 x 1024, 164 MB: 31.9 and 35; the
+// forward pass of 20000 x 1024, 184 MB: 33.0 and 37.6). A smaller result stays where its reader finds it.
+constexpr int64_t kPastBytes = int64_t(112) << 20;
 
 struct NormParams {
     const Bf16x8* x;
@@ -39,10 +43,18 @@ struct NormParams {
     int32_t blocks;      // blocks of 128 channels, the last one may be short
     int32_t row_waves;   // wavefronts of a row
     int32_t group_rows;  // rows that a workgroup works on at a time
-    float width;
+    float per_width;  // 1 / width
     float eps;
     bool weight_half;
 };
+
+// 1 / sqrt(x) within 1 ulp for a normal x: the hardware's, and one Newton step
+// (0 for an infinite x, which the step has no value for).
+__device__ __forceinline__ float inverse_root(float x) {
+    const float r = __builtin_amdgcn_rsqf(x);
+    const float e = __builtin_fmaf(-x * r, r, 1.f);
+    return r == 0.f ? 0.f : __builtin_fmaf(0.5f * e, r, r);
+}
 
 __device__ __forceinline__ int64_t rows_of(int64_t num_rows, const int32_t* num_valid_rows) {
     if (num_valid_rows == nullptr) return num_rows;
@@ -119,7 +131,7 @@ __global__ void __launch_bounds__(kNormMaxWaves * kWave) norm_kernel(NormParams 
             turn ^= 1;
         }
         if (!here) continue;
-        const float r = 1.f / sqrtf(sum / p.width + p.eps);
+        const float r = inverse_root(sum * p.per_width + p.eps);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int vec = first + v * step;
@@ -149,7 +161,7 @@ struct NormBackwardParams {
     int32_t vecs;
     int32_t row_waves;
     int32_t group_rows;
-    float width;
+    float per_width;  // 1 / width
     float eps;
     bool weight_half;
 };
@@ -188,20 +200,20 @@ __global__ void __launch_bounds__(kNormMaxWaves * kWave) norm_backward_kernel(No
         next_dy = load(p.grad_y, row, 0);
         next_dh = load(p.grad_h, row, 0);
     };
+    Bf16x8 h[V], dy[V], dh;
     int64_t base = (int64_t)blockIdx.x * p.group_rows;
     if (kAhead && base < rows) load_next(base + mine);
     for (; base < rows; base += stride) {
         const int64_t row = base + mine;
-        Bf16x8 h[V], dy[V], dh;
-        if constexpr (kAhead) {
+        if (kAhead) {
             h[0] = next_h, dy[0] = next_dy, dh = next_dh;
             if (base + stride < rows) load_next(row + stride);
         }
-        float square = 0.f, along = 0.f;
         if (kKeep && !kAhead) {
 #pragma unroll
             for (int v = 0; v < V; ++v) h[v] = load(p.h, row, v), dy[v] = load(p.grad_y, row, v);
         }
+        float square = 0.f, along = 0.f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             float a[8], d[8], w[8];
@@ -212,7 +224,7 @@ __global__ void __launch_bounds__(kNormMaxWaves * kWave) norm_backward_kernel(No
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 square = __builtin_fmaf(a[i], a[i], square);
-                along = __builtin_fmaf(d[i] * w[i], a[i], along);
+                along = __builtin_fmaf(w[i], d[i] * a[i], along);
             }
         }
         square = wave_sum(square);
@@ -228,8 +240,9 @@ __global__ void __launch_bounds__(kNormMaxWaves * kWave) norm_backward_kernel(No
             }
             turn ^= 1;
         }
-        const float r = 1.f / sqrtf(square / p.width + p.eps);
-        const float mean = along / p.width * r;  // of g u
+        // grad_x = (r w) grad_y - u (r mean(g u)) + grad_h.
+        const float r = inverse_root(square * p.per_width + p.eps);
+        const float back = along * p.per_width * r * r;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int vec = first + v * step;
@@ -244,7 +257,7 @@ __global__ void __launch_bounds__(kNormMaxWaves * kWave) norm_backward_kernel(No
             for (int i = 0; i < 8; ++i) {
                 const float u = a[i] * r;
                 if (kWeight) dw[kWeight ? v : 0][i] = __builtin_fmaf(d[i], u, dw[kWeight ? v : 0][i]);
-                b[i] = __builtin_fmaf(r, d[i] * w[i] - u * mean, b[i]);
+                b[i] = __builtin_fmaf(-u, back, __builtin_fmaf(r * w[i], d[i], b[i]));
             }
             if (row < rows && vec < p.vecs) store_vec<kStream>(p.grad_x + row * p.vecs + vec, narrow_bf16(b));
         }
@@ -319,7 +332,7 @@ struct NormShape {
 int waves_for(int vecs, int v) { return (vecs + v * kWave - 1) / (v * kWave); }
 
 // One vector a lane for few rows, which are bound by latency; two from two
-// rows per CU on (4096 x 7168 channels 46.3 us, 49.1 with one and 47.8 with
+// rows per CU on (4096 x 7168 channels 46.2 us, 49.1 with one and 47.8 with
 // four; 333 x 4096 4.5 us with one, 4.7 with two). Narrow rows share a
 // workgroup of four wavefronts.
 NormShape norm_shape(int64_t rows, int vecs) {
@@ -335,9 +348,9 @@ NormShape norm_shape(int64_t rows, int vecs) {
 
 // The gradient's workgroups each leave a row of sums, so there are few: 8 to 16
 // wavefronts per CU, whose next rows are on their way, with narrow rows beside
-// each other in a workgroup (8191 x 2064: 26.6 to 27.2 us with 15 to 20
-// wavefronts of one row per CU, 34.7 without the next row's loads; 20000 x 512:
-// 18.9 us, 29.4 with a row of sums for every row at work).
+// each other in a workgroup (8191 x 2064: 25.7 us with 15 wavefronts per CU, 31.7
+// with 10; without the next row's loads 10 us more; 20000 x 512:
+// 18.3 us, 29.4 with a row of sums for every row at work).
 NormShape norm_backward_shape(int64_t rows, int vecs) {
     NormShape s;
     s.v = 1;
@@ -381,7 +394,7 @@ hipError_t launch_rms_norm(const dispatch_rms_norm_problem_t& prob, const void* 
     p.num_rows = prob.num_rows;
     p.vecs = (int32_t)(prob.width / 8);
     p.blocks = (int32_t)((prob.width + DISPATCH_SF_BLOCK - 1) / DISPATCH_SF_BLOCK);
-    p.width = (float)prob.width;
+    p.per_width = 1.f / (float)prob.width;
     p.eps = prob.eps;
     p.weight_half = prob.weight_bytes == 2;
     const NormShape s = norm_shape(prob.num_rows, p.vecs);
@@ -414,7 +427,7 @@ hipError_t launch_rms_norm_backward(const dispatch_rms_norm_problem_t& prob, con
     p.grad_x = static_cast<Bf16x8*>(grad_x);
     p.num_rows = prob.num_rows;
     p.vecs = (int32_t)(prob.width / 8);
-    p.width = (float)prob.width;
+    p.per_width = 1.f / (float)prob.width;
     p.eps = prob.eps;
     p.weight_half = prob.weight_bytes == 2;
     const NormShape s = norm_backward_shape(prob.num_rows, p.vecs);
