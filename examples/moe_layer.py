@@ -1,15 +1,19 @@
 """An expert layer on one GPU: gate, fp8 dispatch, the experts' products, combine.
 
     python examples/moe_layer.py [--tokens 4096] [--hidden 7168] [--inter 2048] [--experts 32] [--topk 8]
+                                 [--groups 8 --topk-groups 4] [--norm]
 
 forward():  logits -> dispatch_gate -> topk_idx, topk_weights (and the balance loss)
             x -> dispatch_quantize -> dispatch_layout_and_scatter -> expert-major fp8 rows
             -> dispatch_expert_product_swiglu -> dispatch_expert_product -> dispatch_combine
 backward(): the gradients of the layer's input and of the logits, the experts'
             weights fixed: the same products with the weights laid out
-            transposed, SwiGLU's gradient from the up product kept in bf16, and
-            dispatch_gate_backward. (The combine's own gradient is a gather and
-            a product of rows, in torch.)
+            transposed, SwiGLU's gradient from the up product kept in bf16,
+            dispatch_combine_backward before them and dispatch_gate_backward.
+
+MoeBlock is the layer behind its norm: dispatch_rms_norm adds the residual and
+gives the router its bf16 rows and the dispatch its fp8 rows, in place of
+dispatch_quantize; dispatch_rms_norm_backward takes the gradient back.
 
 Every call is prepared once; a step is one C call each.
 """
@@ -46,7 +50,8 @@ def transposed(q, sf):
 
 class MoeLayer:
     def __init__(self, tokens, hidden, inter, experts, topk, device="cuda", alignment=16, seed=0, loss_coef=0.01,
-                 training=True):
+                 training=True, groups=None):
+        """groups: (groups of experts, groups that a token's experts come from), or None."""
         g = torch.Generator(device=device).manual_seed(seed)
         normal = lambda *shape: torch.randn(shape, generator=g, device=device)  # noqa: E731
         self.up, self.up_sf = quantise_weights(normal(experts, 2 * inter, hidden) * hidden ** -0.5)
@@ -72,8 +77,10 @@ class MoeLayer:
         pairs = tokens * topk
         up = M.make_expert_problem(experts, hidden, 2 * inter, cap, pairs)
         down = M.make_expert_problem(experts, inter, hidden, cap, pairs)
+        gate_ws = M.alloc_gate_workspace(gate, device)
         self.steps = [
-            M.GatePlan(gate, self.logits, self.route, M.alloc_gate_workspace(gate, device)),
+            M.GatePlan(gate, self.logits, self.route, gate_ws) if groups is None else
+            M.GroupedGatePlan(gate, M.make_gate_groups(*groups), self.logits, self.route, gate_ws),
             M.QuantizePlan(self.x, self.x_q, self.x_sf),
             M.Plan(self.prob, self.route.topk_idx, self.lay, ws, self.x_q.view(torch.uint8), self.x_sf, self.rows),
             M.ExpertSwigluPlan(up, *layout, *rows, self.up, self.up_sf, a, a_sf),
@@ -82,9 +89,10 @@ class MoeLayer:
         ]
         if not training:
             return
-        # Backward: dy -> da (down transposed) -> dh (SwiGLU) -> dx of each row (up transposed) -> dx of each token.
+        # Backward: dout -> dy of each row -> da (down transposed) -> dh (SwiGLU) -> dx of each row (up transposed)
+        # -> dx of each token.
         total = self.lay.expert_psum[-1:]
-        self.dy = new((cap, hidden), torch.bfloat16)
+        self.dout = new((tokens, hidden), torch.bfloat16)
         dy_q, dy_sf = new((cap, hidden), FP8), new((cap, self.x_sf.shape[1]), torch.float32)
         h, da = new((cap, 2 * inter), torch.bfloat16), new((cap, inter), torch.bfloat16)
         dh_q, dh_sf = new((cap, 2 * inter), FP8), new((cap, 2 * inter // BLOCK), torch.float32)
@@ -93,7 +101,8 @@ class MoeLayer:
         self.dlogits, ones = torch.zeros_like(self.logits), torch.ones((tokens, topk), device=device)
         up_t, down_t = transposed(self.up, self.up_sf), transposed(self.down, self.down_sf)
         self.back = [
-            M.QuantizePlan(self.dy, dy_q, dy_sf, num_valid_rows=total),
+            M.CombineBackwardPlan(self.lay.expert_slot.view(tokens, topk), self.route.topk_weights, self.y, self.dout,
+                                  grad_weights=self.dweights, grad_q=dy_q, grad_sf=dy_sf),
             M.ExpertProductPlan(M.make_expert_problem(experts, hidden, inter, cap, pairs), *layout, dy_q, dy_sf, *down_t, da),
             M.ExpertProductPlan(up, *layout, *rows, self.up, self.up_sf, h),
             M.SwigluBackwardQuantizePlan(h, da, dh_q, dh_sf, num_valid_rows=total),
@@ -113,30 +122,68 @@ class MoeLayer:
 
     def backward(self, dout):
         """dout [T, H] -> gradients of x through the experts and of the logits (weights, and the loss with gradient 1)."""
-        slot = self.lay.expert_slot.long()
-        live = slot >= 0
-        at = slot.clamp_min(0)
-        d = dout.float()[:, None, :].expand(-1, slot.shape[1], -1)
-        self.dweights.copy_(torch.where(live, (d * self.y[at].float()).sum(-1), 0.0))
-        self.dy[slot[live]] = (self.route.topk_weights[:, :, None] * d)[live].to(torch.bfloat16)
+        self.dout.copy_(dout)
         for step in self.back:
             step()
         return self.dx, self.dlogits
+
+
+class MoeBlock(MoeLayer):
+    """The layer behind its norm: h = x + residual, out = layer(norm(h)); h goes on along the residual."""
+
+    def __init__(self, tokens, hidden, *args, device="cuda", eps=1e-6, training=True, **kw):
+        super().__init__(tokens, hidden, *args, device=device, training=training, **kw)
+        new = lambda shape, dtype=torch.bfloat16: torch.zeros(shape, dtype=dtype, device=device)  # noqa: E731
+        self.x_in, self.residual, self.h = (new((tokens, hidden)) for _ in range(3))
+        self.norm_weight = torch.ones(hidden, dtype=torch.bfloat16, device=device)
+        self.steps[1] = None  # the rows come quantised from the norm
+        self.norm = M.RmsNormPlan(self.x_in, self.norm_weight, eps, residual=self.residual, h=self.h, y=self.x, q=self.x_q,
+                                  sf=self.x_sf)
+        self.steps = [step for step in self.steps if step is not None]
+        if training:
+            self.dy, self.dh, self.dx_in = (new((tokens, hidden)) for _ in range(3))
+            self.dnorm_weight = new(hidden, torch.float32)
+            self.norm_back = M.RmsNormBackwardPlan(self.h, self.norm_weight, self.dy, eps, self.dx_in, grad_h=self.dh,
+                                                   grad_weight=self.dnorm_weight,
+                                                   workspace=M.alloc_rms_norm_workspace(tokens, hidden, device))
+
+    def forward(self, x, residual):
+        """x, residual [T, H] bf16 -> out [T, H] and h [T, H] bf16."""
+        self.x_in.copy_(x)
+        self.residual.copy_(residual)
+        self.norm()
+        torch.matmul(self.x, self.router.t(), out=self.logits)
+        for step in self.steps:
+            step()
+        return self.out, self.h
+
+    def backward(self, dout, dh):
+        """dout, dh [T, H] -> gradients of h (x's and the residual's) and of the norm's weight."""
+        dx, dlogits = super().backward(dout)
+        self.dh.copy_(dh)
+        torch.addmm(dx, dlogits, self.router, out=self.dy)
+        self.norm_back()
+        return self.dx_in, self.dnorm_weight
 
 
 def main():
     ap = argparse.ArgumentParser()
     for name, value in (("tokens", 4096), ("hidden", 7168), ("inter", 2048), ("experts", 32), ("topk", 8), ("steps", 20)):
         ap.add_argument("--" + name, type=int, default=value)
+    ap.add_argument("--groups", type=int, help="a token's experts come from --topk-groups groups of them")
+    ap.add_argument("--topk-groups", type=int, default=1)
+    ap.add_argument("--norm", action="store_true", help="the layer behind its residual and norm")
     a = ap.parse_args()
-    layer = MoeLayer(a.tokens, a.hidden, a.inter, a.experts, a.topk, training=False)
+    groups = (a.groups, a.topk_groups) if a.groups else None
+    layer = (MoeBlock if a.norm else MoeLayer)(a.tokens, a.hidden, a.inter, a.experts, a.topk, training=False, groups=groups)
     x = torch.randn((a.tokens, a.hidden), device="cuda").to(torch.bfloat16)
+    inputs = (x, x) if a.norm else (x,)
     for _ in range(3):
-        layer.forward(x)
+        layer.forward(*inputs)
     torch.cuda.synchronize()
     start = time.perf_counter()
     for _ in range(a.steps):
-        layer.forward(x)
+        layer.forward(*inputs)
     torch.cuda.synchronize()
     us = (time.perf_counter() - start) / a.steps * 1e6
     flops = 6.0 * a.tokens * a.topk * a.hidden * a.inter
