@@ -346,20 +346,38 @@ NormShape norm_shape(int64_t rows, int vecs) {
     return s;
 }
 
-// The gradient's workgroups each leave a row of sums, so there are few: 8 to 16
-// wavefronts per CU, whose next rows are on their way, with narrow rows beside
-// each other in a workgroup (8191 x 2064: 25.7 us with 15 wavefronts per CU, 31.7
-// with 10; without the next row's loads 10 us more; 20000 x 512:
-// 18.3 us, 29.4 with a row of sums for every row at work).
+// The gradient's workgroups each leave a row of sums, so there are few, one to
+// three per CU, with rows beside each other in a workgroup and the next ones on
+// their way. Measured, us:
+//
+//   rows x width     wavefronts of a row, rows of a workgroup: time by workgroups
+//    4096 x 7168     14, 1: 256 45.6   512 48   (with 512 the rows of sums cost more)
+//    4000 x 4096      8, 2: 256 27.4   512 30.3    8, 1: 512 28.7
+//    8191 x 2064      5, 1: 768 25.6   512 31.7    5, 3: 256 27.9
+//   14000 x 2048      4, 2: 256 42.1   512 42.9    4, 4: 256 42.9
+//    2000 x 2048      4, 2: 256 10.9   512 11.8    4, 4: 256 11.6
+//   30000 x  768      2, 4: 512 35.5               2, 8: 256 36.6
+//   20000 x  512      1, 8: 512 18.3   256 19.2
+//
+// A workgroup that takes all rows in a few rounds needs no second kernel: 8 x
+// 2048 5.3 us, 7.0 with it; 32 x 512 5.5 and 7.0.
 NormShape norm_backward_shape(int64_t rows, int vecs) {
+    constexpr int kAlone = 32;  // wavefronts' rows
     NormShape s;
     s.v = 1;
     while (waves_for(vecs, s.v) > kNormMaxWaves) s.v *= 2;
     s.row_waves = waves_for(vecs, s.v);
-    s.group_rows = s.row_waves >= 8 ? 1 : 8 / s.row_waves;
-    const int most = kCus * (kNormMaxWaves / (s.row_waves * s.group_rows));
+    const int room = kNormMaxWaves / s.row_waves;
+    if (rows * s.row_waves <= kAlone) {
+        s.group_rows = rows < 1 ? 1 : (int)(rows < room ? rows : room);
+        s.groups = 1;
+        return s;
+    }
+    // (Five wavefronts: three rows would wait for each other.)
+    s.group_rows = s.row_waves > 5 ? room : s.row_waves == 5 ? 1 : (room + 1) / 2;
     const int64_t groups = (rows + s.group_rows - 1) / s.group_rows;
-    s.groups = groups < 1 ? 1 : (int)(groups < most ? groups : most);
+    const int most = kCus * (s.row_waves == 5 ? room : s.row_waves > 2 ? 1 : 2);
+    s.groups = (int)(groups < most ? groups : most);
     return s;
 }
 
