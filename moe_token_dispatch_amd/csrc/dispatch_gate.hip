@@ -547,7 +547,7 @@ __global__ void __launch_bounds__(kGateWaves<V> * kWave) gate_kernel(GateParams 
 }
 
 // The forward pass of many tokens and up to 256 experts: four tokens per
-// wavefront, 16 lanes for each, V = 8 or 16 experts per lane in runs of four
+// wavefront, 16 lanes for each, V = 8 or 16 experts per lane (or 4, with groups) in runs of four
 // neighbours (run j of lane c from expert 4 (16 j + c); a run that would pass
 // the last expert is moved back, as a pair above).
 //
@@ -593,7 +593,7 @@ struct Quad {
     int start, first;  // as of Pair
     __device__ __forceinline__ Quad(int c, int v, int32_t E) {
         start = (v / 4 * kRowLanes + c) * 4;
-        // (E > 8 V: the first half is whole.)
+        // (E > 8 V with V > 4: the first half is whole.)
         first = 4 * kRowLanes * (v / 4 + 1) <= 8 * V || start < E - 4 ? start : E - 4;
     }
 };
@@ -663,6 +663,9 @@ __device__ __forceinline__ int quad_slot(int e, int32_t E) {
 // and of the other with k = 1, 4 and 8, without / with balance outputs:
 //
 //   softmax of fp32         here            k = 1         4            8
+//    64 experts,  4096   4.5 / 10.4    4.1 /  9.7   4.3 / 10.4   4.7 / 10.6
+//                 8192   5.1 / 10.6    5.7 / 11.5   6.0 / 11.9   6.7 / 12.5
+//                65536  17.4 / 24.0   23.1 / 33.8  26.2 / 40.1  31.3 / 47.8
 //   128 experts,  4096   5.1 / 11.5    4.5 / 10.5   5.1 / 11.6   5.2 / 11.7
 //                 8192   4.9 / 11.8    5.5 / 12.4   6.2 / 13.1   7.1 / 14.1
 //                65536  19.1 / 27.5   26.0 / 39.7  30.3 / 47.5  36.5 / 58.1
@@ -850,6 +853,8 @@ __global__ void __launch_bounds__(kRowWaves * kWave, 4) gate_rows_kernel(GatePar
 #pragma unroll
         for (int v = 0; v < V; ++v)
             (v < kBest ? best : more)[v % kBest] = numbered(keys[v], Quad<V>(c, v, E).first + v % 4);
+#pragma unroll
+        for (int v = V; v < kBest; ++v) best[v] = numbered(kNoKey, 0);
         sort(best);
         if constexpr (V > kBest) {
             sort(more);
@@ -1199,17 +1204,20 @@ const void* gate_kernel_of(bool half, bool sigmoid, bool balance, bool grouped) 
     return half ? gate_kernel_of<V, true, false>(sigmoid, balance) : gate_kernel_of<V, false, false>(sigmoid, balance);
 }
 template <int V, bool kHalf, bool kGrouped>
-const void* gate_rows_of(bool sigmoid, bool balance) {
+const void* gate_rows_half(bool sigmoid, bool balance) {
     if (sigmoid)
         return balance ? (const void*)&gate_rows_kernel<V, kHalf, true, true, kGrouped>
                        : (const void*)&gate_rows_kernel<V, kHalf, true, false, kGrouped>;
     return balance ? (const void*)&gate_rows_kernel<V, kHalf, false, true, kGrouped>
                    : (const void*)&gate_rows_kernel<V, kHalf, false, false, kGrouped>;
 }
+template <int V, bool kGrouped>
+const void* gate_rows_of(bool half, bool sigmoid, bool balance) {
+    return half ? gate_rows_half<V, true, kGrouped>(sigmoid, balance) : gate_rows_half<V, false, kGrouped>(sigmoid, balance);
+}
 template <int V>
 const void* gate_rows_of(bool half, bool sigmoid, bool balance, bool grouped) {
-    if (grouped) return half ? gate_rows_of<V, true, true>(sigmoid, balance) : gate_rows_of<V, false, true>(sigmoid, balance);
-    return half ? gate_rows_of<V, true, false>(sigmoid, balance) : gate_rows_of<V, false, false>(sigmoid, balance);
+    return grouped ? gate_rows_of<V, true>(half, sigmoid, balance) : gate_rows_of<V, false>(half, sigmoid, balance);
 }
 
 template <int V>
@@ -1273,7 +1281,7 @@ hipError_t launch_gate(const dispatch_gate_problem_t& prob, const dispatch_gate_
     const int64_t many = !grouped && sig && prob.num_topk < kFewestSigmoidRounds ? 2 * kManyTokens : kManyTokens;
     const int fewest = grouped ? 1 : kFewestRounds;
     const bool by_runs = !grouped || (p.group_size % 4 == 0 && p.num_groups <= kMostRowGroups);
-    const bool rows_form = E > 64 && E <= 256 && prob.num_topk >= fewest && prob.num_topk <= kBest &&
+    const bool rows_form = E > (grouped ? 0 : 64) && E <= 256 && prob.num_topk >= fewest && prob.num_topk <= kBest &&
                            prob.num_tokens >= many && by_runs;
     if (grouped) {
         const int lanes = rows_form ? kRowLanes : kWave;
@@ -1281,8 +1289,10 @@ hipError_t launch_gate(const dispatch_gate_problem_t& prob, const dispatch_gate_
     }
     if (rows_form) {
         waves = kRowWaves, per_wave = kRowTokens;
-        const int v = E <= 128 ? 8 : 16;
-        kernel = v == 8 ? gate_rows_of<8>(half, sig, balance, grouped) : gate_rows_of<16>(half, sig, balance, grouped);
+        const int v = E <= 64 ? 4 : E <= 128 ? 8 : 16;
+        kernel = v == 4   ? gate_rows_of<4, true>(half, sig, balance)
+                 : v == 8 ? gate_rows_of<8>(half, sig, balance, grouped)
+                          : gate_rows_of<16>(half, sig, balance, grouped);
         row = row_floats(v, sig, grouped);
         extra = sig ? v * kRowLanes : 0;
     } else {

@@ -70,7 +70,9 @@ SHAPES = [(1, 256, 8, 4, 8), (33, 160, 8, 3, 6), (257, 72, 8, 2, 5), (40, 4096, 
           (300, 200, 5, 2, 8), (8192, 256, 8, 4, 8), (8193, 132, 33, 5, 6), (16385, 65, 5, 2, 4), (20000, 256, 64, 9, 7),
           (8200, 128, 16, 1, 8), (8200, 250, 10, 4, 8), (8192, 160, 8, 3, 6), (8192, 252, 9, 4, 1), (8195, 192, 3, 2, 2),
           (8193, 180, 15, 6, 8), (8194, 200, 5, 1, 7), (8197, 256, 2, 1, 8), (8191, 256, 16, 7, 8), (8192, 68, 17, 5, 4),
-          (8201, 72, 6, 5, 3), (8199, 76, 1, 1, 8)]
+          (8201, 72, 6, 5, 3), (8199, 76, 1, 1, 8), (8192, 64, 8, 3, 8), (8200, 32, 8, 3, 4), (8193, 16, 4, 2, 8),
+          (8195, 8, 2, 1, 4), (8200, 60, 15, 4, 8), (8201, 48, 12, 6, 1), (9000, 20, 5, 2, 8), (8192, 64, 2, 1, 9),
+          (8192, 64, 16, 9, 8), (8197, 12, 3, 2, 8)]
 
 
 @pytest.mark.parametrize("t,e,groups,taken,topk", SHAPES)
