@@ -359,7 +359,8 @@ int dispatch_combine(const dispatch_combine_problem_t* problem, const int32_t* e
  * H]), or quantised as dispatch_quantize does (grad_q: device bytes
  * [expert_rows, H], grad_sf: device fp32 [expert_rows, ceil(H / 128)]; H a
  * multiple of 16), the rows that the experts' product takes; rows that no entry
- * has (pads) are not written. Outputs that are NULL are left out, but one is
+ * has (pads) are not written, and slots are a layout's: no two entries have the
+ * same one (its row would be either's). Outputs that are NULL are left out, but one is
  * needed, and either grad_y or grad_q may be given. y (as in dispatch_combine)
  * is needed with grad_weights only. Row pointers are 16-byte aligned. */
 int dispatch_combine_backward(const dispatch_combine_problem_t* problem, const int32_t* expert_slot,
@@ -435,8 +436,9 @@ int dispatch_gate(const dispatch_gate_problem_t* problem, const void* logits, co
  * g holds the E / G experts from g * E / G on (as a rank of the dispatch does
  * with G = R: a token then goes to at most topk_groups ranks). A group goes by
  * the largest choice among its experts (z, or s + select_bias), or with
- * score_experts = 2 by the fp32 sum of its two largest (of a lone one itself);
- * choices of -inf or NaN do not count. The topk_groups groups with the largest
+ * score_experts = 2 by the fp32 sum of its two largest (of a lone one itself; a
+ * sum below fp32's range is its lowest number); choices of -inf or NaN do not
+ * count. The topk_groups groups with the largest
  * of these are taken, ties to the lowest group; a group without any choice is
  * never taken. The K experts come from the taken groups alone; scores, weights,
  * counts and loss are those of dispatch_gate, over all experts, and
@@ -545,7 +547,8 @@ int dispatch_rms_norm_workspace_size(const dispatch_rms_norm_problem_t* problem,
  * the residual), or NULL; grad_x may be grad_y or grad_h. h is the forward
  * pass's (x without a residual). grad_weight: device fp32 [W], or NULL, and
  * then no workspace is needed; its sums do not depend on the order in which
- * workgroups run. num_valid_rows as above; rows beyond it add nothing. */
+ * workgroups run. num_valid_rows as above; rows beyond it add nothing. One
+ * kernel, two with the weight's gradient of more than a few rows. */
 int dispatch_rms_norm_backward(const dispatch_rms_norm_problem_t* problem, const void* h, const void* weight,
                                const void* grad_y, const void* grad_h, const int32_t* num_valid_rows, void* grad_x,
                                float* grad_weight, void* workspace, size_t workspace_bytes, hipStream_t stream);

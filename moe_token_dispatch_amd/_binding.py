@@ -978,7 +978,8 @@ class CombineBackwardPlan(_Prepared):
         device = _check_one_device(tensors)
         problem = CombineProblem(t, k, 0, width, n)
         super().__init__("dispatch_combine_backward", (ctypes.byref(problem), *map(_ptr, tensors),
-                                                       _stream_handle(stream, device)), device, (problem, tensors))
+                                                       _stream_handle(stream, device)), device,
+                         (problem, tensors, stream))
 
 
 def dispatch_combine_backward(expert_slot: torch.Tensor, topk_weights: torch.Tensor, y: Optional[torch.Tensor],
@@ -1129,7 +1130,7 @@ class GroupedGatePlan(_Prepared):
         outs = [getattr(out, f.name) for f in dataclasses.fields(out)]
         device = _check_one_device((logits, workspace, select_bias, token_mask, *outs))
         super().__init__("dispatch_gate_grouped", (first, ctypes.byref(groups), *rest), device,
-                         (problem, groups, logits, outs, ptrs, workspace, select_bias, token_mask))
+                         (problem, groups, logits, outs, ptrs, workspace, select_bias, token_mask, stream))
 
 
 def dispatch_gate_grouped(problem: GateProblem, groups: GateGroups, logits: torch.Tensor, out: GateTensors,
@@ -1315,7 +1316,8 @@ class RmsNormPlan(_Prepared):
         tensors = (x, residual, weight, num_valid_rows, h, y, q, sf)
         device = _check_one_device(tensors)
         super().__init__("dispatch_rms_norm", (ctypes.byref(problem), *map(_ptr, tensors),
-                                               _stream_handle(stream, device)), device, (problem, tensors))
+                                               _stream_handle(stream, device)), device,
+                         (problem, tensors, stream))
 
 
 def dispatch_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Optional[torch.Tensor] = None,
@@ -1362,7 +1364,8 @@ class RmsNormBackwardPlan(_Prepared):
         tensors = (h, weight, grad_y, grad_h, num_valid_rows, grad_x, grad_weight, workspace)
         device = _check_one_device(tensors)
         super().__init__("dispatch_rms_norm_backward", (ctypes.byref(problem), *map(_ptr, tensors), nbytes,
-                                                        _stream_handle(stream, device)), device, (problem, tensors))
+                                                        _stream_handle(stream, device)), device,
+                         (problem, tensors, stream))
 
 
 def dispatch_rms_norm_backward(h: torch.Tensor, weight: torch.Tensor, grad_y: torch.Tensor, eps: float,

@@ -150,8 +150,10 @@ __global__ void __launch_bounds__(kMaxWaves * kWave) combine_backward_kernel(Com
 
 template <RowsTo kTo>
 const void* kernel_of(bool weights, bool past) {
-    if (weights) return past ? (const void*)&combine_backward_kernel<kTo, true, true> : (const void*)&combine_backward_kernel<kTo, true, false>;
-    return (const void*)&combine_backward_kernel<kTo, false, false>;  // (loads nothing to keep out)
+    if constexpr (kTo != RowsTo::kNone)
+        if (!weights) return (const void*)&combine_backward_kernel<kTo, false, false>;  // (loads nothing to keep out)
+    return past ? (const void*)&combine_backward_kernel<kTo, true, true>
+                : (const void*)&combine_backward_kernel<kTo, true, false>;
 }
 
 }  // namespace

@@ -112,7 +112,6 @@ __global__ void __launch_bounds__(kNormMaxWaves * kWave) norm_kernel(NormParams 
                 if (here && vec < p.vecs) store_vec<kStream>(p.h + at + vec, h[v]);
             }
         }
-        if (p.y == nullptr && p.q == nullptr) continue;
         float sum = 0.f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {

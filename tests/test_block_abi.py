@@ -3,6 +3,9 @@ the CPU: bad arguments come back as documented codes before any GPU work."""
 
 import ctypes
 import math
+import os
+import shutil
+import subprocess
 
 import pytest
 import torch
@@ -18,6 +21,29 @@ def test_constants_and_structures_match_the_header():
     assert (d["DISPATCH_MAX_GATE_GROUPS"], d["DISPATCH_MAX_NORM_WIDTH"]) == (M.MAX_GATE_GROUPS, M.MAX_NORM_WIDTH)
     assert ctypes.sizeof(M.GateGroups) == 16 and ctypes.sizeof(M.RmsNormProblem) == 24
     assert (M.RmsNormProblem.width.offset, M.RmsNormProblem.weight_bytes.offset, M.RmsNormProblem.eps.offset) == (8, 16, 20)
+
+
+def test_structures_from_c(tmp_path):
+    """The structures as a C99 compiler lays them out, and a host check called from C."""
+    gcc = shutil.which("gcc")
+    if gcc is None or not os.path.isdir("/opt/rocm/include"):
+        pytest.skip("gcc or the ROCm headers are not installed")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    structs = {"dispatch_gate_groups_t": M.GateGroups, "dispatch_rms_norm_problem_t": M.RmsNormProblem}
+    lines = [f'printf("%zu %zu\\n", sizeof({c}), offsetof({c}, {f}));' for c, t in structs.items() for f, _ in t._fields_]
+    want = [f"{ctypes.sizeof(t)} {getattr(t, f).offset}" for t in structs.values() for f, _ in t._fields_]
+    source = tmp_path / "probe.c"
+    source.write_text("#include <stddef.h>\n#include <stdio.h>\n#include \"moe_dispatch.h\"\nint main(void) {\n" + "\n".join(lines)
+                      + "\ndispatch_rms_norm_problem_t p = {0, 264, 2, 1e-6f};\nsize_t n = 0;\n"
+                        'printf("%d\\n", dispatch_rms_norm_workspace_size(&p, &n));\nreturn 0;\n}\n')
+    M.load_library()
+    pkg, exe = os.path.join(root, "moe_token_dispatch_amd"), str(tmp_path / "probe")
+    built = subprocess.run([gcc, "-std=c99", "-Wall", "-Wextra", "-Werror", "-D__HIP_PLATFORM_AMD__", "-I", "/opt/rocm/include",
+                            "-I", os.path.join(root, "include"), str(source), "-o", exe, "-L", pkg, "-lmoe_dispatch",
+                            f"-Wl,-rpath,{pkg}"], capture_output=True, text=True)
+    assert built.returncode == 0, built.stderr
+    out = subprocess.run([exe], capture_output=True, text=True, timeout=120).stdout.split("\n")
+    assert out[:len(want)] == want and int(out[len(want)]) == M.ERR_ALIGN
 
 
 # ------------------------------------------------------------- grouped gate
