@@ -31,6 +31,8 @@
 // partial row; a second kernel adds the partial rows in order. No float goes
 // through an atomic, so the sums do not depend on timing (the counts are
 // integers and do go through LDS atomics).
+#include <utility>
+
 #include "dispatch_common.hpp"
 #include "dispatch_experts.hpp"
 #include "dispatch_math.hpp"
@@ -644,23 +646,39 @@ __device__ __forceinline__ void join_lanes(double (&x)[kBest]) {
     join(x, y);
 }
 
+// The best eight of a token's lanes, from each lane's V numbers.
+template <int V>
+__device__ __forceinline__ void best_of(double (&best)[kBest], double (&more)[kBest]) {
+    sort(best);
+    if constexpr (V > kBest) {
+        sort(more);
+        join(best, more);
+    }
+    join_lanes<kDppQuadXor1>(best);
+    join_lanes<kDppQuadXor2>(best);
+    join_lanes<kDppRowHalfMirror>(best);
+    join_lanes<kDppRowMirror>(best);
+}
+
 // Where expert e is in a row of runs.
 __device__ __forceinline__ int quad_slot(int e, int32_t E) {
     const int past = E % 4;
     return past == 0 || e < E - past ? e : e + 4 - past;
 }
 
-// Choice by groups, where a group is a number of whole runs and there are at
-// most 16: a lane finds the two largest keys of each of its runs, which go
-// through LDS, and the token's 16 lanes, Gp of them side by side for the groups
-// (Gp a power of two), join those of their group, the lanes that share one by
-// rotations. All of these have its mark then, and a group's place is the number
-// of marks above its own, of equal ones of lower groups: Gp - 1 rotations. (A
-// maximum and its removal for each group taken: 14 instructions for each of
-// them, where a rotation takes 4.) Looking for the groups takes longer in the
-// form of one token per wavefront, so this one is taken from 8192 tokens on
-// whatever the number of entries. Measured, 8 groups, 4 taken, us of this form
-// and of the other with k = 1, 4 and 8, without / with balance outputs:
+// Choice by groups, of up to 32. Where a group is a number of whole runs, a lane
+// finds the two largest keys of each of its runs, and these go through LDS; else
+// the keys do. The token's 16 lanes, Gp of them side by side for the groups (Gp a
+// power of two; with more than 16 groups each lane has two) look for those of
+// their group and join what they found by rotations. All of these have its mark
+// then, and a group's place is the number of marks above its own, of equal ones
+// of lower groups: Gp - 1 rotations. (A maximum and its removal for each group
+// taken: 14 instructions for each of them, where a rotation takes 4.) Entries
+// past the eighth come from a second pass over the keys below the eighth's.
+// Looking for the groups takes longer in the form of one token per wavefront, so
+// this one is taken from 8192 tokens on whatever the number of entries. Measured,
+// 8 groups, 4 taken, us of this form and of the other with k = 1, 4 and 8, without
+// / with balance outputs:
 //
 //   softmax of fp32         here            k = 1         4            8
 //    64 experts,  4096   4.5 / 10.4    4.1 /  9.7   4.3 / 10.4   4.7 / 10.6
@@ -676,13 +694,31 @@ __device__ __forceinline__ int quad_slot(int e, int32_t E) {
 //   256 experts,  4096   7.9 / 15.1    6.0 / 12.3   6.6 / 12.6   7.4 / 13.7
 //                 8192   7.8 / 15.7    8.1 / 14.2   9.1 / 15.8  10.8 / 17.9
 //                65536  37.8 / 48.3   40.9 / 60.4  48.0 / 72.6  59.7 / 88.7
-constexpr int kMostRowGroups = kRowLanes;
-constexpr int kRunsStride = 8;  // words between the tokens' runs, so that they start in other banks
+//
+// Groups of other sizes, more than 16 of them or more than eight entries, softmax of
+// fp32, 65536 tokens, here / other form: 12 experts in 4 groups, k = 5 17.2 / 25.5;
+// 40 in 20, k = 2 22.6 / 24.3; 64 in 8, k = 12 27.1 / 34.6; 128 in 8, k = 12 32.5 /
+// 42.0 (8192 tokens 6.8 / 8.1). With 16 experts a lane the registers do not hold it
+// (150 in 10, k = 8 61.7 / 50.2), so that is left to the other form.
+constexpr int kMostRowGroups = 2 * kRowLanes;
+constexpr int kMostRowEntries = 2 * kBest;
+constexpr int kMostAnyExperts = 128;
 
-__device__ __host__ constexpr int row_floats(int v, bool sigmoid, bool grouped) {
-    const int scores = (sigmoid ? kRowTokens : 1) * v * kRowLanes;
-    const int runs = grouped ? kRowTokens * (v * kRowLanes / 2 + kRunsStride) : 0;
-    return scores > runs ? scores : runs;
+// Which groups a form is built for.
+enum class Groups {
+    kNone,
+    kRuns,  // up to 16, each a number of whole runs; up to eight entries
+    kAny,   // up to 32; up to 16 entries; up to 128 experts
+};
+
+// LDS words of a token's runs or keys (8 between the tokens', so that they start
+// in other banks), and floats of a wavefront.
+__device__ __host__ constexpr int token_words(int v, Groups groups) {
+    return groups == Groups::kNone ? 0 : v * kRowLanes / (groups == Groups::kRuns ? 2 : 1) + 8;
+}
+__device__ __host__ constexpr int row_floats(int v, bool sigmoid, Groups groups) {
+    const int scores = (sigmoid ? kRowTokens : 1) * v * kRowLanes, keys = kRowTokens * token_words(v, groups);
+    return scores > keys ? scores : keys;
 }
 
 // With the lane N places on in a row of 16.
@@ -692,35 +728,64 @@ __device__ __forceinline__ void join_rotated(TopTwo& top) {
     top.join(first, second);
 }
 
-// Adds 1 where the mark N groups before (modulo Gp) goes before this one.
+// Adds 1 where the mark of the group N before (modulo Gp) goes before this one.
 template <int N>
 __device__ __forceinline__ void count_before(uint32_t mark, int group, int& place) {
     place += dpp_ror<kDppRowRor + N>(mark) + (group >= N ? 1u : 0u) > mark ? 1 : 0;
 }
+template <int kFirst, int... N>
+__device__ __forceinline__ void count_from(std::integer_sequence<int, N...>, uint32_t mark, int group, int& place) {
+    (count_before<kFirst + N>(mark, group, place), ...);
+}
+// The same between the first 16 groups and the others: one of the first goes
+// before an equal one of the others.
+template <int... N>
+__device__ __forceinline__ void count_across(std::integer_sequence<int, N...>, uint32_t mark, uint32_t mark2, int& place,
+                                             int& place2) {
+    place += mark2 > mark ? 1 : 0;
+    place2 += mark >= mark2 ? 1 : 0;
+    ((place += dpp_ror<kDppRowRor + N + 1>(mark2) > mark ? 1 : 0,
+      place2 += dpp_ror<kDppRowRor + N + 1>(mark) >= mark2 ? 1 : 0),
+     ...);
+}
 
 // A bit for each group of the lane's token that is open.
-template <int V>
-__device__ __forceinline__ uint32_t open_row_groups(const uint32_t (&key)[V], float* runs_of, const GateParams& p,
+template <int V, Groups kGroups>
+__device__ __forceinline__ uint32_t open_row_groups(const uint32_t (&key)[V], float* mine, const GateParams& p,
                                                     int lane) {
     const int c = lane % kRowLanes;
-    uint2* const runs = reinterpret_cast<uint2*>(runs_of + lane / kRowLanes * (V * kRowLanes / 2 + kRunsStride));
-#pragma unroll
-    for (int v = 0; v < V; v += 4) {
-        TopTwo run;
-        const uint32_t a = key[v], b = key[v + 1], d = key[v + 2], e = key[v + 3];
-        run.first = a > b ? a : b;
-        run.second = a > b ? b : a;
-        run.join(d > e ? d : e, d > e ? e : d);
-        runs[v / 4 * kRowLanes + c] = uint2{run.first, run.second};
-    }
-    __builtin_amdgcn_wave_barrier();
     const int side = kRowLanes >> p.group_lanes;  // Gp
-    const int group = c & (side - 1), size = p.group_size / 4;
-    TopTwo top;
-    if (group < p.num_groups) {
-        for (int i = c / side; i < size; i += 1 << p.group_lanes) {
+    const int group = c & (side - 1), part = c / side, parts = 1 << p.group_lanes;
+    const bool two = kGroups == Groups::kAny && p.num_groups > kRowLanes;
+    float* const row = mine + lane / kRowLanes * token_words(V, kGroups);
+    TopTwo top, next;  // of the lane's group, and of the one 16 further on
+    if constexpr (kGroups == Groups::kRuns) {
+        uint2* const runs = reinterpret_cast<uint2*>(row);
+#pragma unroll
+        for (int v = 0; v < V; v += 4) {
+            TopTwo run;
+            const uint32_t a = key[v], b = key[v + 1], d = key[v + 2], e = key[v + 3];
+            run.first = a > b ? a : b;
+            run.second = a > b ? b : a;
+            run.join(d > e ? d : e, d > e ? e : d);
+            runs[v / 4 * kRowLanes + c] = uint2{run.first, run.second};
+        }
+        __builtin_amdgcn_wave_barrier();
+        const int size = p.group_size / 4;
+        for (int i = part; group < p.num_groups && i < size; i += parts) {
             const uint2 run = runs[group * size + i];
             top.join(run.x, run.y);
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; v += 4)
+            reinterpret_cast<uint4*>(row)[v / 4 * kRowLanes + c] = uint4{key[v], key[v + 1], key[v + 2], key[v + 3]};
+        __builtin_amdgcn_wave_barrier();
+        const uint32_t* const keys = reinterpret_cast<const uint32_t*>(row);
+        const int first = group * p.group_size, far = first + kRowLanes * p.group_size;
+        for (int i = part; i < p.group_size; i += parts) {
+            if (first < p.num_experts) top.add(keys[quad_slot(first + i, p.num_experts)]);
+            if (far < p.num_experts && two) next.add(keys[quad_slot(far + i, p.num_experts)]);
         }
     }
     __builtin_amdgcn_wave_barrier();
@@ -730,38 +795,32 @@ __device__ __forceinline__ uint32_t open_row_groups(const uint32_t (&key)[V], fl
     if (side <= 8) join_rotated<8>(top);
     const uint32_t mark = top.mark(p.group_pairs);
     int place = 0;
+    // (Past Gp - 1 rotations the same groups come again.)
     if (side > 1) count_before<1>(mark, group, place);
-    if (side > 2) {
-        count_before<2>(mark, group, place);
-        count_before<3>(mark, group, place);
-    }
-    if (side > 4) {
-        count_before<4>(mark, group, place);
-        count_before<5>(mark, group, place);
-        count_before<6>(mark, group, place);
-        count_before<7>(mark, group, place);
-    }
-    if (side > 8) {
-        count_before<8>(mark, group, place);
-        count_before<9>(mark, group, place);
-        count_before<10>(mark, group, place);
-        count_before<11>(mark, group, place);
-        count_before<12>(mark, group, place);
-        count_before<13>(mark, group, place);
-        count_before<14>(mark, group, place);
-        count_before<15>(mark, group, place);
-    }
-    const uint64_t open = __ballot(place < p.topk_groups && mark != kNoKey);
-    const uint32_t half = lane < kWave / 2 ? (uint32_t)open : (uint32_t)(open >> 32);
-    return (half >> (lane & kRowLanes)) & (uint32_t)(side == 16 ? 0xffff : (1 << side) - 1);
+    if (side > 2) count_from<2>(std::make_integer_sequence<int, 2>(), mark, group, place);
+    if (side > 4) count_from<4>(std::make_integer_sequence<int, 4>(), mark, group, place);
+    if (side > 8) count_from<8>(std::make_integer_sequence<int, 8>(), mark, group, place);
+    const auto bits = [&](bool open) {
+        const uint64_t all = __ballot(open);
+        const uint32_t word = lane < kWave / 2 ? (uint32_t)all : (uint32_t)(all >> 32);
+        return (word >> (lane & kRowLanes)) & ((1u << side) - 1);
+    };
+    if (!two) return bits(place < p.topk_groups && mark != kNoKey);
+    const uint32_t mark2 = next.mark(p.group_pairs);
+    int place2 = 0;
+    const auto others = std::make_integer_sequence<int, kRowLanes - 1>();
+    count_from<1>(others, mark2, group, place2);
+    count_across(others, mark, mark2, place, place2);
+    return bits(place < p.topk_groups && mark != kNoKey) | bits(place2 < p.topk_groups && mark2 != kNoKey) << kRowLanes;
 }
 
-template <int V, bool kHalf, bool kSigmoid, bool kBalance, bool kGrouped>
+template <int V, bool kHalf, bool kSigmoid, bool kBalance, Groups kGroups>
 __global__ void __launch_bounds__(kRowWaves * kWave, 4) gate_rows_kernel(GateParams p) {
     // Sigmoid: the wavefront's rows of scores; groups: its tokens' runs;
     // balance: its sums; then of the workgroup, sigmoid: a row of the selection
     // bias; balance: counts [E] and live tokens [1].
-    constexpr int kWaveFloats = row_floats(V, kSigmoid, kGrouped);
+    constexpr bool kGrouped = kGroups != Groups::kNone;
+    constexpr int kWaveFloats = row_floats(V, kSigmoid, kGroups);
     extern __shared__ float lds[];
     const int lane = threadIdx.x & (kWave - 1), c = lane % kRowLanes;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -817,14 +876,13 @@ __global__ void __launch_bounds__(kRowWaves * kWave, 4) gate_rows_kernel(GatePar
             s[v] = taken && quad.first + v % 4 >= quad.start ? z : kNone;
         }
     };
-    // The groups of the lane's runs; what is past the last group is never open.
+    // The groups of the lane's runs, where runs are of one (what is past the last
+    // group has nothing to take).
     int run_group[V / 4] = {};
-    if constexpr (kGrouped) {
+    const float per_size = kGroups == Groups::kAny ? 1.f / (float)p.group_size : 0.f;
+    if constexpr (kGroups == Groups::kRuns) {
 #pragma unroll
-        for (int j = 0; j < V / 4; ++j) {
-            const int group = (j * kRowLanes + c) * 4 / p.group_size;
-            run_group[j] = group < kMostRowGroups ? group : kMostRowGroups;
-        }
+        for (int j = 0; j < V / 4; ++j) run_group[j] = (j * kRowLanes + c) * 4 / p.group_size & 31;
     }
     if (t0 < p.num_tokens) load(t0);
     if (t0 < p.num_tokens) arrive();
@@ -832,40 +890,64 @@ __global__ void __launch_bounds__(kRowWaves * kWave, 4) gate_rows_kernel(GatePar
         if (t0 + stride < p.num_tokens) load(t0 + stride);
         const bool now = taken;
         float sum = 0.f;
-        double best[kBest], more[kBest];
-        uint32_t keys[V];
+        uint32_t keys[V], never = 0;
+        // The keys of scores (sigmoid) or logits, without what no choice is.
+        const auto key_of_expert = [&](int v) {
+            if constexpr (!kSigmoid) return order_key(s[v]);
+            return (never >> v) & 1 ? kNoKey : order_key(s[v] + bias[(v / 4 * kRowLanes + c) * 4 + v % 4]);
+        };
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             if constexpr (kSigmoid) {
-                const bool never = !(s[v] > kNone);
+                never |= (!(s[v] > kNone) ? 1u : 0u) << v;
                 s[v] = s[v] == kNone ? 0.f : sigmoid(s[v]);
                 sum += s[v];
-                keys[v] = never ? kNoKey : order_key(s[v] + bias[(v / 4 * kRowLanes + c) * 4 + v % 4]);
-            } else {
-                keys[v] = order_key(s[v]);
             }
+            keys[v] = key_of_expert(v);
         }
+        uint32_t open = 0;
+        const auto close_groups = [&] {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                int group = run_group[v / 4];
+                if (kGroups == Groups::kAny) group = group_lane(Quad<V>(c, v, E).first + v % 4, per_size, 0);
+                keys[v] = (open >> group) & 1 ? keys[v] : kNoKey;
+            }
+        };
         if constexpr (kGrouped) {
-            const uint32_t open = open_row_groups<V>(keys, mine, p, lane);
-#pragma unroll
-            for (int v = 0; v < V; ++v) keys[v] = (open >> run_group[v / 4]) & 1 ? keys[v] : kNoKey;
+            open = open_row_groups<V, kGroups>(keys, mine, p, lane);
+            close_groups();
         }
+        double best[kBest], more[kBest];
+        const auto number = [&](int v) { return numbered(keys[v], Quad<V>(c, v, E).first + v % 4); };
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-            (v < kBest ? best : more)[v % kBest] = numbered(keys[v], Quad<V>(c, v, E).first + v % 4);
+        for (int v = 0; v < V; ++v) (v < kBest ? best : more)[v % kBest] = number(v);
 #pragma unroll
         for (int v = V; v < kBest; ++v) best[v] = numbered(kNoKey, 0);
-        sort(best);
-        if constexpr (V > kBest) {
-            sort(more);
-            join(best, more);
-        }
-        join_lanes<kDppQuadXor1>(best);
-        join_lanes<kDppQuadXor2>(best);
-        join_lanes<kDppRowHalfMirror>(best);
-        join_lanes<kDppRowMirror>(best);
+        best_of<V>(best, more);
         const auto key_of = [](double x) { return (uint32_t)(__builtin_bit_cast(uint64_t, x) >> 8); };
         const uint32_t top = key_of(best[0]);
+        // Lane c of the token's 16 takes entry c.
+        double entry = best[0];
+#pragma unroll
+        for (int k = 1; k < kBest; ++k) entry = c == k ? best[k] : entry;
+        if (kGroups == Groups::kAny && K > kBest) {
+            // The entries past the eighth, from what is below that one.
+            const double last = best[kBest - 1];
+#pragma unroll
+            for (int v = 0; v < V; ++v) keys[v] = key_of_expert(v);
+            close_groups();
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const double x = number(v);
+                (v < kBest ? best : more)[v % kBest] = x < last ? x : numbered(kNoKey, 0);
+            }
+#pragma unroll
+            for (int v = V; v < kBest; ++v) best[v] = numbered(kNoKey, 0);
+            best_of<V>(best, more);
+#pragma unroll
+            for (int k = 0; k < kBest; ++k) entry = c == kBest + k ? best[k] : entry;
+        }
         const float high = top == kNoKey ? 0.f : key_value(top);
         if constexpr (!kSigmoid) {
 #pragma unroll
@@ -876,10 +958,6 @@ __global__ void __launch_bounds__(kRowWaves * kWave, 4) gate_rows_kernel(GatePar
         }
         sum = row_sum(sum);
         const RowSum all{sum, sum == 0.f ? 0.f : (kSigmoid ? 1.f / sum : reciprocal(sum))};
-        // Lane c of the token's 16 takes entry c.
-        double entry = best[0];
-#pragma unroll
-        for (int k = 1; k < kBest; ++k) entry = c == k ? best[k] : entry;
         const uint32_t key = key_of(entry);
         const int expert = 255 - (int)((uint32_t)__builtin_bit_cast(uint64_t, entry) & 0xff);
         const int picked = c < K && key != kNoKey ? expert : -1;
@@ -1203,21 +1281,27 @@ const void* gate_kernel_of(bool half, bool sigmoid, bool balance, bool grouped) 
     if (grouped) return half ? gate_kernel_of<V, true, true>(sigmoid, balance) : gate_kernel_of<V, false, true>(sigmoid, balance);
     return half ? gate_kernel_of<V, true, false>(sigmoid, balance) : gate_kernel_of<V, false, false>(sigmoid, balance);
 }
-template <int V, bool kHalf, bool kGrouped>
+template <int V, bool kHalf, Groups kGroups>
 const void* gate_rows_half(bool sigmoid, bool balance) {
     if (sigmoid)
-        return balance ? (const void*)&gate_rows_kernel<V, kHalf, true, true, kGrouped>
-                       : (const void*)&gate_rows_kernel<V, kHalf, true, false, kGrouped>;
-    return balance ? (const void*)&gate_rows_kernel<V, kHalf, false, true, kGrouped>
-                   : (const void*)&gate_rows_kernel<V, kHalf, false, false, kGrouped>;
-}
-template <int V, bool kGrouped>
-const void* gate_rows_of(bool half, bool sigmoid, bool balance) {
-    return half ? gate_rows_half<V, true, kGrouped>(sigmoid, balance) : gate_rows_half<V, false, kGrouped>(sigmoid, balance);
+        return balance ? (const void*)&gate_rows_kernel<V, kHalf, true, true, kGroups>
+                       : (const void*)&gate_rows_kernel<V, kHalf, true, false, kGroups>;
+    return balance ? (const void*)&gate_rows_kernel<V, kHalf, false, true, kGroups>
+                   : (const void*)&gate_rows_kernel<V, kHalf, false, false, kGroups>;
 }
 template <int V>
-const void* gate_rows_of(bool half, bool sigmoid, bool balance, bool grouped) {
-    return grouped ? gate_rows_of<V, true>(half, sigmoid, balance) : gate_rows_of<V, false>(half, sigmoid, balance);
+const void* gate_rows_of(bool half, bool sigmoid, bool balance, Groups groups) {
+    if (groups == Groups::kRuns)
+        return half ? gate_rows_half<V, true, Groups::kRuns>(sigmoid, balance)
+                    : gate_rows_half<V, false, Groups::kRuns>(sigmoid, balance);
+    if constexpr (V * kRowLanes <= kMostAnyExperts)
+        if (groups == Groups::kAny)
+            return half ? gate_rows_half<V, true, Groups::kAny>(sigmoid, balance)
+                        : gate_rows_half<V, false, Groups::kAny>(sigmoid, balance);
+    if constexpr (V > 4)  // (without groups from 65 experts on)
+        return half ? gate_rows_half<V, true, Groups::kNone>(sigmoid, balance)
+                    : gate_rows_half<V, false, Groups::kNone>(sigmoid, balance);
+    return nullptr;
 }
 
 template <int V>
@@ -1280,9 +1364,12 @@ hipError_t launch_gate(const dispatch_gate_problem_t& prob, const dispatch_gate_
     int waves, per_wave, row, extra = 0;
     const int64_t many = !grouped && sig && prob.num_topk < kFewestSigmoidRounds ? 2 * kManyTokens : kManyTokens;
     const int fewest = grouped ? 1 : kFewestRounds;
-    const bool by_runs = !grouped || (p.group_size % 4 == 0 && p.num_groups <= kMostRowGroups);
-    const bool rows_form = E > (grouped ? 0 : 64) && E <= 256 && prob.num_topk >= fewest && prob.num_topk <= kBest &&
-                           prob.num_tokens >= many && by_runs;
+    const bool runs = p.group_size % 4 == 0 && p.num_groups <= kRowLanes && prob.num_topk <= kBest;
+    const Groups form = !grouped ? Groups::kNone : runs ? Groups::kRuns : Groups::kAny;
+    const int most = form == Groups::kAny ? kMostRowEntries : kBest;
+    const bool rows_form = E >= (grouped ? 4 : 65) && E <= (form == Groups::kAny ? kMostAnyExperts : 256) &&
+                           prob.num_topk >= fewest && prob.num_topk <= most && prob.num_tokens >= many &&
+                           (!grouped || p.num_groups <= kMostRowGroups);
     if (grouped) {
         const int lanes = rows_form ? kRowLanes : kWave;
         while ((2 << p.group_lanes) * p.num_groups <= lanes) ++p.group_lanes;
@@ -1290,10 +1377,10 @@ hipError_t launch_gate(const dispatch_gate_problem_t& prob, const dispatch_gate_
     if (rows_form) {
         waves = kRowWaves, per_wave = kRowTokens;
         const int v = E <= 64 ? 4 : E <= 128 ? 8 : 16;
-        kernel = v == 4   ? gate_rows_of<4, true>(half, sig, balance)
-                 : v == 8 ? gate_rows_of<8>(half, sig, balance, grouped)
-                          : gate_rows_of<16>(half, sig, balance, grouped);
-        row = row_floats(v, sig, grouped);
+        kernel = v == 4   ? gate_rows_of<4>(half, sig, balance, form)
+                 : v == 8 ? gate_rows_of<8>(half, sig, balance, form)
+                          : gate_rows_of<16>(half, sig, balance, form);
+        row = row_floats(v, sig, form);
         extra = sig ? v * kRowLanes : 0;
     } else {
         per_wave = 1;
