@@ -547,8 +547,9 @@ int dispatch_rms_norm_workspace_size(const dispatch_rms_norm_problem_t* problem,
  * the residual), or NULL; grad_x may be grad_y or grad_h. h is the forward
  * pass's (x without a residual). grad_weight: device fp32 [W], or NULL, and
  * then no workspace is needed; its sums do not depend on the order in which
- * workgroups run. num_valid_rows as above; rows beyond it add nothing. One
- * kernel, two with the weight's gradient of more than a few rows. */
+ * workgroups run. num_valid_rows as above; rows beyond it add nothing. All but
+ * num_valid_rows are 16-byte aligned. One kernel, two with the weight's gradient
+ * of more than a few rows. */
 int dispatch_rms_norm_backward(const dispatch_rms_norm_problem_t* problem, const void* h, const void* weight,
                                const void* grad_y, const void* grad_h, const int32_t* num_valid_rows, void* grad_x,
                                float* grad_weight, void* workspace, size_t workspace_bytes, hipStream_t stream);
