@@ -614,6 +614,9 @@ struct Quad {
     }
 };
 
+// (LDS words of these types may be read as others, unlike HIP's uint2 and uint4.)
+typedef uint32_t Words2 __attribute__((ext_vector_type(2)));
+typedef uint32_t Words4 __attribute__((ext_vector_type(4)));
 typedef uint32_t Halves4 __attribute__((ext_vector_type(2), aligned(2)));
 typedef uint32_t Floats4 __attribute__((ext_vector_type(4), aligned(4)));
 
@@ -774,7 +777,7 @@ __device__ __forceinline__ uint32_t open_row_groups(const uint32_t (&key)[V], fl
     float* const row = mine + lane / kRowLanes * token_words(V, kGroups);
     TopTwo top, next;  // of the lane's group, and of the one 16 further on
     if constexpr (kGroups == Groups::kRuns) {
-        uint2* const runs = reinterpret_cast<uint2*>(row);
+        Words2* const runs = reinterpret_cast<Words2*>(row);
 #pragma unroll
         for (int v = 0; v < V; v += 4) {
             TopTwo run;
@@ -782,24 +785,24 @@ __device__ __forceinline__ uint32_t open_row_groups(const uint32_t (&key)[V], fl
             run.first = a > b ? a : b;
             run.second = a > b ? b : a;
             run.join(d > e ? d : e, d > e ? e : d);
-            runs[v / 4 * kRowLanes + c] = uint2{run.first, run.second};
+            runs[v / 4 * kRowLanes + c] = Words2{run.first, run.second};
         }
         __builtin_amdgcn_wave_barrier();
         const int size = p.group_size / 4;
         for (int i = part; group < p.num_groups && i < size; i += parts) {
-            const uint2 run = runs[group * size + i];
+            const Words2 run = runs[group * size + i];
             top.join(run.x, run.y);
         }
     } else {
 #pragma unroll
         for (int v = 0; v < V; v += 4)
-            reinterpret_cast<uint4*>(row)[v / 4 * kRowLanes + c] = uint4{key[v], key[v + 1], key[v + 2], key[v + 3]};
+            reinterpret_cast<Words4*>(row)[v / 4 * kRowLanes + c] = Words4{key[v], key[v + 1], key[v + 2], key[v + 3]};
         __builtin_amdgcn_wave_barrier();
-        const uint32_t* const keys = reinterpret_cast<const uint32_t*>(row);
+        const auto at = [&](int e) { return __float_as_uint(row[quad_slot(e, p.num_experts)]); };
         const int first = group * p.group_size, far = first + kRowLanes * p.group_size;
         for (int i = part; i < p.group_size; i += parts) {
-            if (first < p.num_experts) top.add(keys[quad_slot(first + i, p.num_experts)]);
-            if (far < p.num_experts && two) next.add(keys[quad_slot(far + i, p.num_experts)]);
+            if (first < p.num_experts) top.add(at(first + i));
+            if (far < p.num_experts && two) next.add(at(far + i));
         }
     }
     __builtin_amdgcn_wave_barrier();
