@@ -934,16 +934,17 @@ def _check_one_device(tensors) -> torch.device:
 
 
 class _Prepared:
-    """C arguments built once for one C function; a call makes the tensors'
-    device the current one where it is not (a null stream is the current
-    device's)."""
+    """C arguments built once for one C function; with several GPUs a call makes
+    the tensors' device the current one where it is not (a null stream is the
+    current device's)."""
 
     def __init__(self, name: str, args, device: torch.device, keep):
-        self._name, self._args, self._keep, self._device = name, args, keep, device.index
+        self._name, self._args, self._keep = name, args, keep
         self._call = getattr(load_library(), name)
+        self._device = device.index if torch.cuda.device_count() > 1 else None
 
     def __call__(self) -> None:
-        if torch.cuda.current_device() == self._device:
+        if self._device is None or torch.cuda.current_device() == self._device:
             rc = self._call(*self._args)
         else:
             with torch.cuda.device(self._device):
