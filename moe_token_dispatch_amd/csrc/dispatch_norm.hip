@@ -25,8 +25,9 @@ constexpr int kNormMaxWaves = 16;  // of a workgroup, and so of a row
 constexpr int64_t kMaxNormGroups = 1 << 20;  // larger grids loop
 constexpr int kCus = 256;
 // What moves more goes past the caches both ways (the gradient of 4096 x 7168,
-// 235 MB: 50.4 us, through the caches 54.4; 20000 x 1024, 164 MB: 31.9 and 35; the
-// forward pass of 20000 x 1024, 184 MB: 33.0 and 37.6). A smaller result stays where its reader finds it.
+// 235 MB: 50.4 us, through the caches 54.4; 20000 x 1024, 164 MB: 31.6 and 36.5;
+// the forward pass of 20000 x 1024, 184 MB: 33.3 and 37.8). A smaller result stays
+// where its reader finds it.
 constexpr int64_t kPastBytes = int64_t(112) << 20;
 
 struct NormParams {
@@ -43,7 +44,7 @@ struct NormParams {
     int32_t blocks;      // blocks of 128 channels, the last one may be short
     int32_t row_waves;   // wavefronts of a row
     int32_t group_rows;  // rows that a workgroup works on at a time
-    float per_width;  // 1 / width
+    float per_width;     // 1 / width
     float eps;
     bool weight_half;
 };
@@ -264,9 +265,9 @@ __global__ void __launch_bounds__(kNormMaxWaves * kWave) norm_backward_kernel(No
     if constexpr (kWeight) {
         // The workgroup's rows of sums, one after the other.
         float4* const to = reinterpret_cast<float4*>(p.grad_weight) + (int64_t)blockIdx.x * p.vecs * 2;
-        for (int turn = 0; turn < p.group_rows; ++turn) {
-            if (turn == mine) {
-                const bool last = turn == p.group_rows - 1;
+        for (int n = 0; n < p.group_rows; ++n) {
+            if (n == mine) {
+                const bool last = n == p.group_rows - 1;
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     const int vec = first + v * step;
@@ -274,7 +275,7 @@ __global__ void __launch_bounds__(kNormMaxWaves * kWave) norm_backward_kernel(No
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         float4 x{dw[v][4 * i], dw[v][4 * i + 1], dw[v][4 * i + 2], dw[v][4 * i + 3]};
-                        if (turn > 0) {
+                        if (n > 0) {
                             const float4 y = sums[2 * vec + i];
                             x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
                         }
@@ -288,7 +289,7 @@ __global__ void __launch_bounds__(kNormMaxWaves * kWave) norm_backward_kernel(No
 }
 
 // Adds the rows of sums: a workgroup takes 32 channels, 8 threads of four; its
-// 128 groups of such threads add every 128th row, eight of them on their way at
+// 128 groups of such threads add every 128th row, four of them on their way at
 // once, then the groups of a wavefront and the wavefronts are added in order.
 constexpr int kSumThreads = 1024;
 constexpr int kSumLanes = 8;
