@@ -65,7 +65,8 @@ def test_widths(width, form):
     _check(*_inputs(5, 3, width, 19, width), form)
 
 
-@pytest.mark.parametrize("t,k", [(0, 4), (1, 1), (1, 8), (63, 8), (40, 9), (21, 32), (300, 2), (17, 16)])
+@pytest.mark.parametrize("t,k", [(0, 4), (1, 1), (1, 8), (63, 8), (40, 9), (21, 32), (300, 2), (17, 16),
+                                 (255, 8), (256, 9), (300, 32), (128, 3), (100, 17)])
 @pytest.mark.parametrize("form", ["bf16", "fp8", "none"])
 def test_tokens_and_entries(t, k, form):
     _check(*_inputs(t, k, 272, t * k + 5, 100 * t + k), form)
@@ -192,6 +193,42 @@ def test_many_tokens():
     full = torch.zeros_like(y)
     full[at[live]] = rows
     assert torch.equal(dy, full)
+
+
+@pytest.mark.parametrize("form", ["bf16", "fp8"])
+def test_more_tokens_than_the_grid_holds(form):
+    t, width = 1060000, 16
+    rows = t + 5
+    g = torch.Generator(device=DEV).manual_seed(3)
+    slot = torch.randperm(rows, generator=g, device=DEV)[:t].to(torch.int32).view(t, 1)
+    w = torch.randn((t, 1), generator=g, device=DEV)
+    y = torch.randn((rows, width), generator=g, device=DEV).to(torch.bfloat16)
+    d = torch.randn((t, width), generator=g, device=DEV).to(torch.bfloat16)
+    dw = torch.empty((t, 1), device=DEV)
+    rows_of = (w * d.float())
+    at = slot.long().view(-1)
+    if form == "bf16":
+        dy = torch.zeros_like(y)
+        M.dispatch_combine_backward(slot, w, y, d, dw, dy)
+        assert torch.equal(dy[at], rows_of.to(torch.bfloat16))
+    else:
+        q, sf = torch.zeros((rows, width), dtype=torch.uint8, device=DEV), torch.zeros((rows, 1), device=DEV)
+        M.dispatch_combine_backward(slot, w, y, d, dw, None, q, sf)
+        amax = rows_of.abs().amax(1, keepdim=True).clamp_min(2.0 ** -100)
+        top = torch.full_like(amax, 448.0)
+        assert torch.equal(sf[at], amax / top)
+        assert torch.equal(q[at], (rows_of * (top / amax)).to(torch.float8_e4m3fn).view(torch.uint8))
+    terms = d.double() * y[at].double()
+    assert torch.all((dw.double().view(-1) - terms.sum(1)).abs() <= 30 * ULP * terms.abs().sum(1))
+
+
+def test_weights_gradient_of_a_large_batch_alone():
+    slot, w, y, d = _inputs(5000, 4, 4096, 20100, 31)
+    dw, _, _, _ = _run(slot, w, y, d, "none")
+    at = slot.long().clamp_min(0).to(DEV)
+    terms = d.to(DEV).float()[:, None, :] * y.to(DEV)[at].float()
+    want = torch.where((slot >= 0).to(DEV), terms.double().sum(2), 0.0)
+    assert torch.all((dw.double() - want).abs() <= 100 * ULP * terms.double().abs().sum(2))
 
 
 def test_plans_streams_and_a_graph():

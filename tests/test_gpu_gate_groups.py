@@ -53,7 +53,7 @@ def _check(z, groups, taken, topk, sigmoid, pairs, normalize=True, scale=1.0, co
     assert torch.all((used > 0).sum(1) <= taken)
     ref = R.gate_outputs(z, idx, sigmoid, normalize, scale, coef, mask)
     w = out.topk_weights.cpu().double()
-    assert torch.all((w - ref["weights"]).abs() <= REL * (ref["weights"].abs() + scale * 2.0 ** -20))
+    assert torch.all((w - ref["weights"]).abs() <= REL * (ref["weights"].abs() + abs(scale) * 2.0 ** -20))
     if out.loss is not None:
         assert torch.equal(out.expert_count.cpu().long(), ref["count"]) and int(out.live_tokens) == ref["live"]
         assert torch.all((out.prob_sum.cpu().double() - ref["prob_sum"]).abs() <= REL * (ref["prob_sum"] + 2.0 ** -60))
@@ -91,6 +91,18 @@ def test_shapes(t, e, groups, taken, topk, scoring):
 def test_token_counts(t, balance):
     z = _logits(t, 64, torch.bfloat16, 5 + t)
     _check(z, 4, 2, 6, True, True, normalize=False, idx_bytes=4, balance=balance)
+
+
+@pytest.mark.parametrize("t", [8200, 16400])
+@pytest.mark.parametrize("balance", [False, True])
+def test_large_batches_in_every_output(t, balance):
+    z = _logits(t, 120, torch.float32, t)
+    mask = torch.ones(t, dtype=torch.bool)
+    mask[5:8000] = False
+    for groups, taken, topk in ((6, 2, 8), (24, 3, 12), (40, 30, 3)):
+        _check(z, groups, taken, topk, True, True, normalize=False, scale=-1.5, idx_bytes=4, balance=balance, mask=mask)
+        _, out = _run(z, groups, taken, topk, False, False, mask=torch.zeros(t, dtype=torch.bool), balance=balance)
+        assert torch.all(out.topk_idx == -1) and torch.all(out.topk_weights == 0)
 
 
 @pytest.mark.parametrize("t", [300, 9000])

@@ -262,6 +262,45 @@ def test_rows_beyond_32_bit_offsets():
     assert torch.all((dw.cpu().double() - want_w).abs() <= 2 * REL * (dtail.double() * tail.double()).abs().sum(0))
 
 
+@pytest.mark.parametrize("rows,width", [(4300000, 16), (2100200, 1040)])
+def test_more_rows_than_the_grid_holds(rows, width):
+    """The same 100 rows again and again: every repetition gives the same bits."""
+    some = _bf16((100, width), 6).to(DEV)
+    x = some.repeat(rows // 100, 1)
+    w = _weight(width, torch.bfloat16).to(DEV)
+    y = torch.empty_like(x)
+    M.dispatch_rms_norm(x, w, 1e-6, y=y)
+    _close_bf16(y[:100], R.rms_norm(some.cpu(), w.cpu(), 1e-6), REL)
+    assert torch.all(y.view(-1, 100, width) == y[:100])
+    dx = y
+    M.dispatch_rms_norm_backward(x, w, x, 1e-6, dx)
+    want, _ = R.rms_norm_gradient(some.cpu(), w.cpu(), some.cpu(), 1e-6)
+    size = some.cpu().double().abs() * 2 + some.cpu().double().abs() * some.cpu().double().pow(2).mean(1, keepdim=True) * 2
+    assert torch.all((dx[:100].cpu().double() - want).abs() <= BF16 * want.abs() + 4 * REL * size)
+    assert torch.all(dx.view(-1, 100, width) == dx[:100])
+
+
+@pytest.mark.parametrize("rows,width,valid", [(600, 16400, 300), (700, 7168, 511), (3000, 528, 1), (2000, 40000, 1999)])
+def test_valid_rows_of_large_batches(rows, width, valid):
+    x, w = _bf16((rows, width), 1).to(DEV), _weight(width, torch.float32).to(DEV)
+    n = torch.tensor([valid], dtype=torch.int32, device=DEV)
+    y, dx = torch.full_like(x, -7.0), torch.full_like(x, -7.0)
+    dw, short = torch.empty(width, device=DEV), torch.empty(width, device=DEV)
+    M.dispatch_rms_norm(x, w, 1e-6, y=y, num_valid_rows=n)
+    M.dispatch_rms_norm_backward(x, w, x, 1e-6, dx, grad_weight=dw, num_valid_rows=n,
+                                 workspace=M.alloc_rms_norm_workspace(rows, width, DEV))
+    assert torch.all(y[valid:] == -7) and torch.all(dx[valid:] == -7)
+    want_y, want_x = torch.empty_like(x[:valid]), torch.empty_like(x[:valid])
+    M.dispatch_rms_norm(x[:valid], w, 1e-6, y=want_y)
+    M.dispatch_rms_norm_backward(x[:valid], w, x[:valid], 1e-6, want_x, grad_weight=short,
+                                 workspace=M.alloc_rms_norm_workspace(valid, width, DEV))
+    # (Fewer rows may be cut otherwise: their sums are added in another order, and a bf16 rounding may turn.)
+    near = lambda a, b: torch.all((a.double() - b.double()).abs() <= 2 * BF16 * b.double().abs() + 1e-5)  # noqa: E731
+    assert near(y[:valid], want_y) and near(dx[:valid], want_x)
+    terms = (x[:valid].double().pow(2) * (x[:valid].double().pow(2).mean(1, keepdim=True) + 1e-6).rsqrt()).sum(0)
+    assert torch.all((dw.double() - short.double()).abs() <= 2 * (REL + valid * ULP) * terms)
+
+
 def test_plans_streams_and_a_graph():
     rows, width = 200, 1040
     w = _weight(width, torch.bfloat16).to(DEV)
