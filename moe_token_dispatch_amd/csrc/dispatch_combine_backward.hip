@@ -22,7 +22,7 @@
 namespace moe_dispatch {
 namespace {
 
-constexpr int kBatch = 8;     // most entries of a workgroup
+constexpr int kMostEntries = 8;  // of a workgroup
 constexpr int kMaxWaves = 8;  // of a workgroup: longer rows take several rounds (16: 151 us in place of 142)
 constexpr int kCus = 256;
 // What moves more goes past the caches: y too, which is otherwise found there
@@ -50,7 +50,7 @@ struct CombineBackwardParams {
 
 enum class RowsTo { kNone, kBf16, kFp8 };
 
-template <RowsTo kTo, bool kWeights, bool kPast>
+template <RowsTo kTo, bool kWeights, bool kPast, int kBatch>
 __global__ void __launch_bounds__(kMaxWaves * kWave) combine_backward_kernel(CombineBackwardParams p) {
     __shared__ float part[2][kMaxWaves][kBatch];
     const int lane = threadIdx.x & (kWave - 1);
@@ -148,12 +148,22 @@ __global__ void __launch_bounds__(kMaxWaves * kWave) combine_backward_kernel(Com
     }
 }
 
-template <RowsTo kTo>
+template <RowsTo kTo, int kBatch>
 const void* kernel_of(bool weights, bool past) {
     if constexpr (kTo != RowsTo::kNone)
-        if (!weights) return (const void*)&combine_backward_kernel<kTo, false, false>;  // (loads nothing to keep out)
-    return past ? (const void*)&combine_backward_kernel<kTo, true, true>
-                : (const void*)&combine_backward_kernel<kTo, true, false>;
+        if (!weights) return (const void*)&combine_backward_kernel<kTo, false, false, kBatch>;  // (loads nothing to keep out)
+    return past ? (const void*)&combine_backward_kernel<kTo, true, true, kBatch>
+                : (const void*)&combine_backward_kernel<kTo, true, false, kBatch>;
+}
+// Built for 1, 2, 4 and 8 entries: a small call spends its time on fetching the
+// code (16 tokens x 8 x 7168 to fp8, an entry each: 3.7 us in a graph, 4.35 with
+// the code for eight; 2000 tokens of one entry of 4096: 8.2 and 11.3 us).
+template <RowsTo kTo>
+const void* kernel_of(bool weights, bool past, int per) {
+    return per <= 1   ? kernel_of<kTo, 1>(weights, past)
+           : per <= 2 ? kernel_of<kTo, 2>(weights, past)
+           : per <= 4 ? kernel_of<kTo, 4>(weights, past)
+                      : kernel_of<kTo, kMostEntries>(weights, past);
 }
 
 }  // namespace
@@ -178,10 +188,11 @@ hipError_t launch_combine_backward(const dispatch_combine_problem_t& prob, const
     p.blocks = (int32_t)((prob.hidden + DISPATCH_SF_BLOCK - 1) / DISPATCH_SF_BLOCK);
     p.num_topk = prob.num_topk;
     // Few tokens: their entries on several workgroups, about one per CU (63
-    // tokens of 8 entries x 7168 to bf16: 5.8 us with two each, 8.4 with eight).
+    // tokens of 8 entries x 7168 to bf16: 5.8 us with two each, 8.4 with eight;
+    // with one each, two workgroups per CU, as with two).
     int parts = (int)(prob.num_tokens < kCus ? kCus / prob.num_tokens : 1);
     parts = parts < p.num_topk ? parts : p.num_topk;
-    const int fewest = (p.num_topk + kBatch - 1) / kBatch;
+    const int fewest = (p.num_topk + kMostEntries - 1) / kMostEntries;
     parts = parts > fewest ? parts : fewest;
     p.per = (p.num_topk + parts - 1) / parts;
     p.parts = (p.num_topk + p.per - 1) / p.per;
@@ -192,9 +203,9 @@ hipError_t launch_combine_backward(const dispatch_combine_problem_t& prob, const
     const int64_t groups = items < kMaxGroups ? items : kMaxGroups;
     const int64_t row = prob.hidden * (2 + (grad_y ? 2 : grad_q ? 1 : 0));
     const bool w = grad_weights != nullptr, past = prob.num_tokens * p.num_topk * row > kPastBytes;
-    const void* kernel = grad_y   ? kernel_of<RowsTo::kBf16>(w, past)
-                         : grad_q ? kernel_of<RowsTo::kFp8>(w, past)
-                                  : kernel_of<RowsTo::kNone>(true, past);
+    const void* kernel = grad_y   ? kernel_of<RowsTo::kBf16>(w, past, p.per)
+                         : grad_q ? kernel_of<RowsTo::kFp8>(w, past, p.per)
+                                  : kernel_of<RowsTo::kNone>(true, past, p.per);
     void* args[] = {&p};
     return hipLaunchKernel(kernel, dim3((unsigned)groups), dim3(waves * kWave), args, 0, stream);
 }
