@@ -332,12 +332,13 @@ struct NormShape {
 int waves_for(int vecs, int v) { return (vecs + v * kWave - 1) / (v * kWave); }
 
 // One vector a lane for few rows, which are bound by latency; two from two
-// rows per CU on (4096 x 7168 channels 46.2 us, 49.1 with one and 47.8 with
-// four; 333 x 4096 4.5 us with one, 4.7 with two). Narrow rows share a
-// workgroup of four wavefronts.
+// rows per CU on, wide ones from one (4096 x 7168 channels 46.2 us, 49.1 with one
+// and 47.8 with four; 333 x 4096 4.5 us with one, 4.7 with two; 333 x 7168 6.6 and
+// 6.2, 64 x 7168 4.25 and 4.4). Narrow rows share a workgroup of four wavefronts.
 NormShape norm_shape(int64_t rows, int vecs) {
     NormShape s;
-    s.v = rows >= 512 && vecs > kWave ? 2 : 1;
+    const bool many = rows >= 2 * kCus ? vecs > kWave : rows > kCus && vecs > 8 * kWave;
+    s.v = many ? 2 : 1;
     while (waves_for(vecs, s.v) > kNormMaxWaves) s.v *= 2;
     s.row_waves = waves_for(vecs, s.v);
     s.group_rows = s.row_waves >= 4 ? 1 : 4 / s.row_waves;
