@@ -563,15 +563,16 @@ __global__ void __launch_bounds__(kGateWaves<V> * kWave) gate_kernel(GateParams 
 }
 
 // The forward pass of many tokens and up to 256 experts: four tokens per
-// wavefront, 16 lanes for each, V = 8 or 16 experts per lane (or 4, with groups) in runs of four
-// neighbours (run j of lane c from expert 4 (16 j + c); a run that would pass
-// the last expert is moved back, as a pair above).
+// wavefront, 16 lanes for each, V = 8 or 16 experts per lane (with groups also 4,
+// or 32 for up to 512 experts) in runs of four neighbours (run j of lane c from
+// expert 4 (16 j + c); a run that would pass the last expert is moved back, as a
+// pair above).
 //
 // Choice of up to eight: a key and its expert are one number, key * 256 + 255
-// - expert, exact in a double (2^52 is added, so that its bits are put together
-// by two instructions), and all differ: a maximum and a minimum, one full-rate
-// instruction each, order two of them with no tie to look at. A lane sorts its
-// numbers, and four times lanes join their best eight with a partner's: the
+// - expert (512 and 511 with V = 32), exact in a double (2^52 is added, so that
+// its bits are put together by two instructions), and all differ: a maximum and
+// a minimum, one full-rate instruction each, order two of them with no tie to
+// look at. A lane sorts its numbers, eight at a time, and four times lanes join their best eight with a partner's: the
 // larger of each and the partner's opposite are the best eight of both, in a
 // bitonic order that three steps sort. What is done once a token above (sums,
 // divisions, stores) is done once for four.
@@ -598,11 +599,15 @@ __global__ void __launch_bounds__(kGateWaves<V> * kWave) gate_kernel(GateParams 
 // fewer than six from twice as many. (72 experts as 128, 200 as 256.)
 constexpr int kBest = 8;
 constexpr int kFewestRounds = 4;
-constexpr int kFewestSigmoidRounds = 6;  // of less than 2 kManyTokens
+constexpr int kFewestSigmoidRounds = 6;  // of less than 2 kManyTokens, or of more than 256 experts
 constexpr int64_t kManyTokens = 8192;
 constexpr int kRowLanes = 16;
 constexpr int kRowTokens = kWave / kRowLanes;
-constexpr int kRowWaves = 8;
+// Wavefronts of a workgroup, and those that share a SIMD's registers.
+template <int V>
+constexpr int kRowWaves = V > 16 ? 4 : 8;
+template <int V>
+constexpr int kRowSimdWaves = V > 16 ? 2 : 4;
 
 template <int V>
 struct Quad {
@@ -623,9 +628,14 @@ typedef uint32_t Floats4 __attribute__((ext_vector_type(4), aligned(4)));
 __device__ __forceinline__ double larger(double a, double b) { return __builtin_fmax(a, b); }
 __device__ __forceinline__ double smaller(double a, double b) { return __builtin_fmin(a, b); }
 
+// An expert's bits below its key's.
+template <int V>
+constexpr int kExpertBits = V > 16 ? 9 : 8;
+template <int V>
 __device__ __forceinline__ double numbered(uint32_t key, int expert) {
-    const uint64_t bits = (uint64_t)(0x43300000u | key >> 24) << 32 | (key << 8 | (uint32_t)(255 - expert));
-    return __builtin_bit_cast(double, bits);
+    constexpr int kBits = kExpertBits<V>;
+    const uint32_t low = key << kBits | (uint32_t)((1 << kBits) - 1 - expert);
+    return __builtin_bit_cast(double, (uint64_t)(0x43300000u | key >> (32 - kBits)) << 32 | low);
 }
 
 __device__ __forceinline__ void order(double (&x)[kBest], int i, int j) {
@@ -663,11 +673,25 @@ __device__ __forceinline__ void join_lanes(double (&x)[kBest]) {
     join(x, y);
 }
 
-// The best eight of a token's lanes, from each lane's V numbers.
-template <int V>
-__device__ __forceinline__ void best_of(double (&best)[kBest], double (&more)[kBest]) {
+// The best eight of a token's lanes, from each lane's V keys; with kBelow of what
+// is below the number last.
+template <int V, bool kBelow>
+__device__ __forceinline__ void best_of(double (&best)[kBest], const uint32_t (&keys)[V], int c, int32_t E,
+                                        double last) {
+    const auto number = [&](int v) {
+        const double none = numbered<V>(kNoKey, 0);
+        if (v >= V) return none;
+        const double x = numbered<V>(keys[v < V ? v : 0], Quad<V>(c, v, E).first + v % 4);
+        return !kBelow || x < last ? x : none;
+    };
+#pragma unroll
+    for (int i = 0; i < kBest; ++i) best[i] = number(i);
     sort(best);
-    if constexpr (V > kBest) {
+#pragma unroll
+    for (int v = kBest; v < V; v += kBest) {
+        double more[kBest];
+#pragma unroll
+        for (int i = 0; i < kBest; ++i) more[i] = number(v + i);
         sort(more);
         join(best, more);
     }
@@ -716,7 +740,22 @@ __device__ __forceinline__ int quad_slot(int e, int32_t E) {
 // fp32, 65536 tokens, here / other form: 12 experts in 4 groups, k = 5 17.2 / 25.5;
 // 40 in 20, k = 2 22.6 / 24.3; 64 in 8, k = 12 27.1 / 34.6; 128 in 8, k = 12 32.5 /
 // 42.0 (8192 tokens 6.8 / 8.1). With 16 experts a lane the registers do not hold it
-// (150 in 10, k = 8 61.7 / 50.2), so that is left to the other form.
+// (150 in 10, k = 8 61.7 / 50.2; with two wavefronts on a SIMD 49.0 / 46.1 for k = 6),
+// so that is left to the other form.
+//
+// More than 256 experts take 32 a lane and two wavefronts on a SIMD, in groups of
+// whole runs only (500 in 20 58.0 / 60.4, sigmoid 79.9 / 67.2, 40000 tokens):
+//
+//   512 experts in 16, 4 taken  here            k = 3          4              6
+//   softmax of fp32,   8192   7.9 / 18.4   10.8 / 17.3   11.0 / 18.4   12.9 / 20.2
+//                     16384  14.2 / 25.4   17.6 / 29.4   19.0 / 31.4   22.5 / 35.2
+//                     65536  51.5 / 57.4   58.5 / 78.9   64.1 / 86.6   77.4 / 102.5
+//   sigmoid of bf16,   8192  12.2 / 25.9   13.1 / 20.6   13.4 / 21.3   15.3 / 23.3
+//                     16384  22.5 / 32.7   21.6 / 35.0   22.7 / 36.9   25.7 / 40.7
+//                     65536  84.2 / 90.0   73.0 / 101.1  77.6 / 108.7  88.4 / 123.6
+//
+// So there from four entries on, with sigmoid and no balance outputs from six,
+// with balance outputs from twice as many tokens.
 constexpr int kMostRowGroups = 2 * kRowLanes;
 constexpr int kMostRowEntries = 2 * kBest;
 constexpr int kMostAnyExperts = 128;
@@ -832,7 +871,7 @@ __device__ __forceinline__ uint32_t open_row_groups(const uint32_t (&key)[V], fl
 }
 
 template <int V, bool kHalf, bool kSigmoid, bool kBalance, Groups kGroups>
-__global__ void __launch_bounds__(kRowWaves * kWave, 4) gate_rows_kernel(GateParams p) {
+__global__ void __launch_bounds__(kRowWaves<V> * kWave, kRowSimdWaves<V>) gate_rows_kernel(GateParams p) {
     // Sigmoid: the wavefront's rows of scores; groups: its tokens' runs;
     // balance: its sums; then of the workgroup, sigmoid: a row of the selection
     // bias; balance: counts [E] and live tokens [1].
@@ -843,22 +882,22 @@ __global__ void __launch_bounds__(kRowWaves * kWave, 4) gate_rows_kernel(GatePar
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int E = p.num_experts, K = p.num_topk;
     float* const mine = lds + wave * kWaveFloats;
-    float* const bias = lds + kRowWaves * kWaveFloats;
+    float* const bias = lds + kRowWaves<V> * kWaveFloats;
     int* const counts = reinterpret_cast<int*>(bias + (kSigmoid ? V * kRowLanes : 0));
     float prob_sum[V];
     int live = 0;
     if (kBalance) {
         if (blockIdx.x == 0 && threadIdx.x == 0) *p.ticket = 0;
-        for (int i = threadIdx.x; i < E + 1; i += kRowWaves * kWave) counts[i] = 0;
+        for (int i = threadIdx.x; i < E + 1; i += kRowWaves<V> * kWave) counts[i] = 0;
 #pragma unroll
         for (int v = 0; v < V; ++v) prob_sum[v] = 0.f;
     }
     if (kSigmoid)
-        for (int e = threadIdx.x; e < E; e += kRowWaves * kWave)
+        for (int e = threadIdx.x; e < E; e += kRowWaves<V> * kWave)
             bias[quad_slot(e, E)] = p.bias != nullptr ? p.bias[e] : 0.f;
     if (kBalance || kSigmoid) __syncthreads();
-    const int64_t stride = (int64_t)gridDim.x * kRowWaves * kRowTokens;
-    int64_t t0 = ((int64_t)blockIdx.x * kRowWaves + wave) * kRowTokens;  // the wavefront's first token
+    const int64_t stride = (int64_t)gridDim.x * kRowWaves<V> * kRowTokens;
+    int64_t t0 = ((int64_t)blockIdx.x * kRowWaves<V> + wave) * kRowTokens;  // the wavefront's first token
     constexpr int kWords = kHalf ? V / 2 : V;
     uint32_t next[kWords];
     int next_live = 0;
@@ -935,14 +974,9 @@ __global__ void __launch_bounds__(kRowWaves * kWave, 4) gate_rows_kernel(GatePar
             open = open_row_groups<V, kGroups>(keys, mine, p, lane);
             close_groups();
         }
-        double best[kBest], more[kBest];
-        const auto number = [&](int v) { return numbered(keys[v], Quad<V>(c, v, E).first + v % 4); };
-#pragma unroll
-        for (int v = 0; v < V; ++v) (v < kBest ? best : more)[v % kBest] = number(v);
-#pragma unroll
-        for (int v = V; v < kBest; ++v) best[v] = numbered(kNoKey, 0);
-        best_of<V>(best, more);
-        const auto key_of = [](double x) { return (uint32_t)(__builtin_bit_cast(uint64_t, x) >> 8); };
+        double best[kBest];
+        best_of<V, false>(best, keys, c, E, 0.);
+        const auto key_of = [](double x) { return (uint32_t)(__builtin_bit_cast(uint64_t, x) >> kExpertBits<V>); };
         const uint32_t top = key_of(best[0]);
         // Lane c of the token's 16 takes entry c.
         double entry = best[0];
@@ -954,14 +988,7 @@ __global__ void __launch_bounds__(kRowWaves * kWave, 4) gate_rows_kernel(GatePar
 #pragma unroll
             for (int v = 0; v < V; ++v) keys[v] = key_of_expert(v);
             close_groups();
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const double x = number(v);
-                (v < kBest ? best : more)[v % kBest] = x < last ? x : numbered(kNoKey, 0);
-            }
-#pragma unroll
-            for (int v = V; v < kBest; ++v) best[v] = numbered(kNoKey, 0);
-            best_of<V>(best, more);
+            best_of<V, true>(best, keys, c, E, last);
 #pragma unroll
             for (int k = 0; k < kBest; ++k) entry = c == kBest + k ? best[k] : entry;
         }
@@ -976,7 +1003,8 @@ __global__ void __launch_bounds__(kRowWaves * kWave, 4) gate_rows_kernel(GatePar
         sum = row_sum(sum);
         const RowSum all{sum, sum == 0.f ? 0.f : (kSigmoid ? 1.f / sum : reciprocal(sum))};
         const uint32_t key = key_of(entry);
-        const int expert = 255 - (int)((uint32_t)__builtin_bit_cast(uint64_t, entry) & 0xff);
+        constexpr uint32_t kMost = (1u << kExpertBits<V>) - 1;
+        const int expert = (int)(kMost - ((uint32_t)__builtin_bit_cast(uint64_t, entry) & kMost));
         const int picked = c < K && key != kNoKey ? expert : -1;
         float weight = 0.f;
         if constexpr (kSigmoid) {
@@ -1025,13 +1053,13 @@ __global__ void __launch_bounds__(kRowWaves * kWave, 4) gate_rows_kernel(GatePar
     if (c == 0) atomicAdd(counts + E, live);
     __syncthreads();
     float* const out = p.partial + (int64_t)blockIdx.x * (2 * E + 1);
-    for (int i = threadIdx.x; i < 2 * E + 1; i += kRowWaves * kWave) {
+    for (int i = threadIdx.x; i < 2 * E + 1; i += kRowWaves<V> * kWave) {
         float x = __int_as_float(counts[i - E < 0 ? 0 : i - E]);
         if (i < E) {
             const float* at = lds + quad_slot(i, E);
             x = at[0];
 #pragma unroll
-            for (int w = 1; w < kRowWaves; ++w) x += at[w * kWaveFloats];
+            for (int w = 1; w < kRowWaves<V>; ++w) x += at[w * kWaveFloats];
         }
         out[i] = x;
     }
@@ -1315,7 +1343,7 @@ const void* gate_rows_of(bool half, bool sigmoid, bool balance, Groups groups) {
         if (groups == Groups::kAny)
             return half ? gate_rows_half<V, true, Groups::kAny>(sigmoid, balance)
                         : gate_rows_half<V, false, Groups::kAny>(sigmoid, balance);
-    if constexpr (V > 4)  // (without groups from 65 experts on)
+    if constexpr (V > 4 && V <= 16)  // (without groups from 65 experts on)
         return half ? gate_rows_half<V, true, Groups::kNone>(sigmoid, balance)
                     : gate_rows_half<V, false, Groups::kNone>(sigmoid, balance);
     return nullptr;
@@ -1379,12 +1407,14 @@ hipError_t launch_gate(const dispatch_gate_problem_t& prob, const dispatch_gate_
     const void* kernel;
     // Wavefronts of a workgroup, their tokens, the floats in LDS of each and of all.
     int waves, per_wave, row, extra = 0;
-    const int64_t many = !grouped && sig && prob.num_topk < kFewestSigmoidRounds ? 2 * kManyTokens : kManyTokens;
-    const int fewest = grouped ? 1 : kFewestRounds;
+    const bool wide = E > 256;
+    const int64_t many =
+        (grouped ? wide && balance : sig && prob.num_topk < kFewestSigmoidRounds) ? 2 * kManyTokens : kManyTokens;
+    const int fewest = grouped && !wide ? 1 : wide && sig && !balance ? kFewestSigmoidRounds : kFewestRounds;
     const bool runs = p.group_size % 4 == 0 && p.num_groups <= kRowLanes && prob.num_topk <= kBest;
     const Groups form = !grouped ? Groups::kNone : runs ? Groups::kRuns : Groups::kAny;
     const int most = form == Groups::kAny ? kMostRowEntries : kBest;
-    const bool rows_form = E >= (grouped ? 4 : 65) && E <= (form == Groups::kAny ? kMostAnyExperts : 256) &&
+    const bool rows_form = E >= (grouped ? 4 : 65) && E <= (form == Groups::kAny ? kMostAnyExperts : form == Groups::kRuns ? 512 : 256) &&
                            prob.num_topk >= fewest && prob.num_topk <= most && prob.num_tokens >= many &&
                            (!grouped || p.num_groups <= kMostRowGroups);
     if (grouped) {
@@ -1392,11 +1422,12 @@ hipError_t launch_gate(const dispatch_gate_problem_t& prob, const dispatch_gate_
         while ((2 << p.group_lanes) * p.num_groups <= lanes) ++p.group_lanes;
     }
     if (rows_form) {
-        waves = kRowWaves, per_wave = kRowTokens;
-        const int v = E <= 64 ? 4 : E <= 128 ? 8 : 16;
-        kernel = v == 4   ? gate_rows_of<4>(half, sig, balance, form)
-                 : v == 8 ? gate_rows_of<8>(half, sig, balance, form)
-                          : gate_rows_of<16>(half, sig, balance, form);
+        const int v = E <= 64 ? 4 : E <= 128 ? 8 : E <= 256 ? 16 : 32;
+        waves = v == 32 ? kRowWaves<32> : kRowWaves<16>, per_wave = kRowTokens;
+        kernel = v == 4    ? gate_rows_of<4>(half, sig, balance, form)
+                 : v == 8  ? gate_rows_of<8>(half, sig, balance, form)
+                 : v == 16 ? gate_rows_of<16>(half, sig, balance, form)
+                           : gate_rows_of<32>(half, sig, balance, form);
         row = row_floats(v, sig, form);
         extra = sig ? v * kRowLanes : 0;
     } else {

@@ -19,8 +19,10 @@ NEAR = 8 * 2.0 ** -23
 
 def grouped_choice(z, groups, taken, topk, sigmoid, pairs, bias=None, mask=None):
     """(idx [T, K], near [T]): the choice, -1 where nothing is left; whether fp32
-    scores may decide it otherwise (two values that it compares are different
-    and within NEAR)."""
+    scores may decide it otherwise (two values that it compares are within NEAR
+    and not of the same logits and biases). Equal sums of other operands count:
+    (x + b) + y and x + (y + b) are one number, but round to two in fp32, each
+    addition by up to 2^-24 of its result."""
     t, e = z.shape
     live = torch.ones(t, dtype=torch.bool) if mask is None else mask.bool()
     choice = z.double()
@@ -28,7 +30,11 @@ def grouped_choice(z, groups, taken, topk, sigmoid, pairs, bias=None, mask=None)
         choice = torch.where(torch.isneginf(choice), -math.inf, torch.sigmoid(choice))
         choice = choice + (0.0 if bias is None else bias.double())
     choice = torch.where(torch.isnan(choice), -math.inf, choice)
-    best = torch.sort(choice.view(t, groups, e // groups), dim=2, descending=True)[0]
+    made = torch.stack((z.double(), (z.new_zeros(e) if bias is None else bias).double().expand(t, e)), 2)  # of what
+    made = torch.nan_to_num(made, nan=1e30)
+    best, first = torch.sort(choice.view(t, groups, e // groups), dim=2, descending=True, stable=True)
+    first = first[:, :, :2 if pairs else 1] + e // groups * torch.arange(groups)[:, None]
+    parts = made.gather(1, first.flatten(1)[:, :, None].expand(-1, -1, 2)).view(t, groups, 2 * first.shape[2])
     marks = best[:, :, 0].clone()
     if pairs and best.shape[2] > 1:
         second = best[:, :, 1]
@@ -37,14 +43,21 @@ def grouped_choice(z, groups, taken, topk, sigmoid, pairs, bias=None, mask=None)
     opened = torch.zeros((t, groups), dtype=torch.bool)
     opened.scatter_(1, order[:, :taken], ~torch.isneginf(value[:, :taken]))
     inner = torch.where(opened.repeat_interleave(e // groups, 1), choice, -math.inf)
-    most, idx = torch.sort(inner, dim=1, descending=True, stable=True)
-    idx = torch.where(torch.isneginf(most[:, :topk]) | ~live[:, None], -1, idx[:, :topk])
+    most, full = torch.sort(inner, dim=1, descending=True, stable=True)
+    idx = torch.where(torch.isneginf(most[:, :topk]) | ~live[:, None], -1, full[:, :topk])
     near = torch.zeros(t, dtype=torch.bool)
     if sigmoid:
-        gap = lambda a, b: (a != b) & ((a - b).abs() <= NEAR)  # noqa: E731
+        # (Of what is taken against all that is left: between a value and another's
+        # there may be equals of the first.)
+        gap = lambda a, b, of, to: ((of != to).any(-1) & ((a - b).abs() <= NEAR)).any(1)  # noqa: E731
         if taken < groups:
-            near |= gap(value[:, taken - 1], value[:, taken])
-        near |= gap(most[:, :-1], most[:, 1:])[:, :topk].any(1)
+            rank = parts.gather(1, order[:, :, None].expand_as(parts))
+            cut = slice(taken - 1, taken), slice(taken, taken + 1)
+            near |= gap(value[:, cut[0]], value[:, taken:], rank[:, cut[0]], rank[:, taken:])
+            near |= gap(value[:, :taken], value[:, cut[1]], rank[:, :taken], rank[:, cut[1]])
+        rank = made.gather(1, full[:, :, None].expand_as(made))
+        near |= gap(most[:, :topk - 1], most[:, 1:topk], rank[:, :topk - 1], rank[:, 1:topk])
+        near |= gap(most[:, topk - 1:topk], most[:, topk:], rank[:, topk - 1:topk], rank[:, topk:])
     return idx, near & live
 
 

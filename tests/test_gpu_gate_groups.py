@@ -72,7 +72,8 @@ SHAPES = [(1, 256, 8, 4, 8), (33, 160, 8, 3, 6), (257, 72, 8, 2, 5), (40, 4096, 
           (8193, 180, 15, 6, 8), (8194, 200, 5, 1, 7), (8197, 256, 2, 1, 8), (8191, 256, 16, 7, 8), (8192, 68, 17, 5, 4),
           (8201, 72, 6, 5, 3), (8199, 76, 1, 1, 8), (8192, 64, 8, 3, 8), (8200, 32, 8, 3, 4), (8193, 16, 4, 2, 8),
           (8195, 8, 2, 1, 4), (8200, 60, 15, 4, 8), (8201, 48, 12, 6, 1), (9000, 20, 5, 2, 8), (8192, 64, 2, 1, 9),
-          (8192, 64, 16, 9, 8), (8197, 12, 3, 2, 8)]
+          (8192, 64, 16, 9, 8), (8197, 12, 3, 2, 8), (16384, 512, 16, 4, 8), (16387, 260, 13, 4, 4),
+          (16390, 384, 8, 3, 5), (16385, 264, 3, 2, 6), (16384, 508, 1, 1, 7), (16384, 500, 5, 1, 8)]
 
 
 @pytest.mark.parametrize("t,e,groups,taken,topk", SHAPES)
@@ -103,6 +104,28 @@ def test_large_batches_in_every_output(t, balance):
         _check(z, groups, taken, topk, True, True, normalize=False, scale=-1.5, idx_bytes=4, balance=balance, mask=mask)
         _, out = _run(z, groups, taken, topk, False, False, mask=torch.zeros(t, dtype=torch.bool), balance=balance)
         assert torch.all(out.topk_idx == -1) and torch.all(out.topk_weights == 0)
+
+
+@pytest.mark.parametrize("t", [8191, 8195, 16384])
+@pytest.mark.parametrize("e,groups,taken,topk", [(512, 16, 4, 8), (260, 13, 3, 4), (384, 8, 4, 6), (320, 4, 1, 3)])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid", "pairs"])
+def test_many_experts_with_ties_and_nothing_to_take(t, e, groups, taken, topk, scoring):
+    z = (2.0 * _logits(t, e, torch.float32, t + e)).round() / 2.0
+    z[0] = -math.inf
+    z[1, e // groups:] = -math.inf
+    z[2, :e - 1] = -math.inf
+    z[3] = 0.0
+    z[4, ::3] = -math.inf
+    bias = None
+    if scoring == "pairs":
+        bias = (0.05 * torch.randn(e, generator=torch.Generator().manual_seed(e))).round(decimals=1)
+        bias[e // groups + 1] = -math.inf
+    mask = torch.arange(t) % 7 != 6
+    for balance in (False, True):
+        _, out = _check(z, groups, taken, topk, scoring != "softmax", scoring == "pairs", scale=2.5, bias=bias, mask=mask,
+                        balance=balance)
+        idx = out.topk_idx.cpu()
+        assert torch.all(idx[0] == -1) and idx[2, 0] == e - 1 and torch.all(idx[2, 1:] == -1) and torch.all(idx[6] == -1)
 
 
 @pytest.mark.parametrize("t", [300, 9000])
@@ -187,7 +210,8 @@ def test_all_groups_are_the_gate(t, e, k, sigmoid):
         assert all(torch.equal(getattr(a, f), getattr(b, f)) for f in FIELDS)
 
 
-@pytest.mark.parametrize("t,e,groups,taken,k", [(64, 256, 8, 4, 8), (9000, 256, 8, 4, 8), (9000, 72, 6, 2, 4)])
+@pytest.mark.parametrize("t,e,groups,taken,k", [(64, 256, 8, 4, 8), (9000, 256, 8, 4, 8), (9000, 72, 6, 2, 4),
+                                                 (17000, 512, 16, 4, 8), (17000, 272, 4, 2, 4)])
 @pytest.mark.parametrize("pairs", [False, True])
 def test_forms_agree(t, e, groups, taken, k, pairs):
     """Rows choose alike in batches of every form, with and without balance outputs, and every time."""
