@@ -673,23 +673,17 @@ __device__ __forceinline__ void join_lanes(double (&x)[kBest]) {
     join(x, y);
 }
 
-// The best eight of a token's lanes, from each lane's V keys; with kBelow of what
-// is below the number last.
-template <int V, bool kBelow>
-__device__ __forceinline__ void best_of(double (&best)[kBest], const uint32_t (&keys)[V], int c, int32_t E,
-                                        double last) {
-    const auto number = [&](int v) {
-        const double none = numbered<V>(kNoKey, 0);
-        if (v >= V) return none;
-        const double x = numbered<V>(keys[v < V ? v : 0], Quad<V>(c, v, E).first + v % 4);
-        return !kBelow || x < last ? x : none;
-    };
-#pragma unroll
-    for (int i = 0; i < kBest; ++i) best[i] = number(i);
+// The best eight of a token's lanes, from each lane's V numbers: the first
+// sixteen in best and more, the others from number.
+template <int V, typename Number>
+__device__ __forceinline__ void best_of(double (&best)[kBest], double (&more)[kBest], const Number& number) {
     sort(best);
+    if constexpr (V > kBest) {
+        sort(more);
+        join(best, more);
+    }
 #pragma unroll
-    for (int v = kBest; v < V; v += kBest) {
-        double more[kBest];
+    for (int v = 2 * kBest; v < V; v += kBest) {
 #pragma unroll
         for (int i = 0; i < kBest; ++i) more[i] = number(v + i);
         sort(more);
@@ -974,8 +968,13 @@ __global__ void __launch_bounds__(kRowWaves<V> * kWave, kRowSimdWaves<V>) gate_r
             open = open_row_groups<V, kGroups>(keys, mine, p, lane);
             close_groups();
         }
-        double best[kBest];
-        best_of<V, false>(best, keys, c, E, 0.);
+        double best[kBest], more[kBest];
+        const auto number = [&](int v) { return numbered<V>(keys[v], Quad<V>(c, v, E).first + v % 4); };
+#pragma unroll
+        for (int v = 0; v < V && v < 2 * kBest; ++v) (v < kBest ? best : more)[v % kBest] = number(v);
+#pragma unroll
+        for (int v = V; v < kBest; ++v) best[v] = numbered<V>(kNoKey, 0);
+        best_of<V>(best, more, number);
         const auto key_of = [](double x) { return (uint32_t)(__builtin_bit_cast(uint64_t, x) >> kExpertBits<V>); };
         const uint32_t top = key_of(best[0]);
         // Lane c of the token's 16 takes entry c.
@@ -988,7 +987,14 @@ __global__ void __launch_bounds__(kRowWaves<V> * kWave, kRowSimdWaves<V>) gate_r
 #pragma unroll
             for (int v = 0; v < V; ++v) keys[v] = key_of_expert(v);
             close_groups();
-            best_of<V, true>(best, keys, c, E, last);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const double x = number(v);
+                (v < kBest ? best : more)[v % kBest] = x < last ? x : numbered<V>(kNoKey, 0);
+            }
+#pragma unroll
+            for (int v = V; v < kBest; ++v) best[v] = numbered<V>(kNoKey, 0);
+            best_of<V>(best, more, number);
 #pragma unroll
             for (int k = 0; k < kBest; ++k) entry = c == kBest + k ? best[k] : entry;
         }
