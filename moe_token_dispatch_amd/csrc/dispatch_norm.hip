@@ -6,10 +6,11 @@
 //   grad_w = sum over the rows of grad_y u
 //
 // A row belongs to as many wavefronts as hold it in registers, V vectors of 8
-// channels a lane, so that it is read once; its sums go through LDS. 16
-// neighbouring lanes hold a block of 128 channels, which is quantised from
-// registers as rows of their own are. The gradient needs no statistics kept
-// from the forward pass: the mean of h^2 is added again beside that of g h.
+// channels a lane, so that it is read once; its sums go through LDS. Many rows of
+// up to 256 channels share wavefronts, two or four in each. 16 neighbouring lanes
+// hold a block of 128 channels, which is quantised from registers as rows of
+// their own are. The gradient needs no statistics kept from the forward pass: the
+// mean of h^2 is added again beside that of g h.
 //
 // HBM bounds both: 4096 x 7168 with the residual to bf16 and fp8 rows 46.2 us
 // for 265 MB (5.7 TB/s), the gradient 45.6 us for 235 MB (5.2 TB/s, the weight's
@@ -24,6 +25,7 @@ namespace {
 constexpr int kNormMaxWaves = 16;  // of a workgroup, and so of a row
 constexpr int64_t kMaxNormGroups = 1 << 20;  // larger grids loop
 constexpr int kCus = 256;
+constexpr int kFewNarrow = 1024;  // rows, see lanes_for
 // What moves more goes past the caches both ways (the gradient of 4096 x 7168,
 // 235 MB: 50.4 us, through the caches 54.4; 20000 x 1024, 164 MB: 31.6 and 36.5;
 // the forward pass of 20000 x 1024, 184 MB: 33.3 and 37.8). A smaller result stays
@@ -74,12 +76,23 @@ __device__ __forceinline__ void load_weight(const void* weight, bool half, int v
     }
 }
 
-template <int V, bool kStream>
+// Sum over a row's lanes in a wavefront, in every one of them.
+template <int kLanes>
+__device__ __forceinline__ float lanes_sum(float v) {
+    if constexpr (kLanes == kWave) return wave_sum(v);
+    v = row_sum(v);
+    if constexpr (kLanes == 32) v += __shfl_xor(v, 16);
+    return v;
+}
+
+// kLanes: lanes of a row. Narrow rows share a wavefront.
+template <int V, bool kStream, int kLanes>
 __global__ void __launch_bounds__(kNormMaxWaves * kWave) norm_kernel(NormParams p) {
+    constexpr bool kWhole = kLanes == kWave;
     __shared__ float part[2][kNormMaxWaves];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int mine = wave / p.row_waves;  // which of the workgroup's rows
-    const int first = threadIdx.x - mine * p.row_waves * kWave, step = p.row_waves * kWave;
+    const int mine = kWhole ? wave / p.row_waves : threadIdx.x / kLanes;  // which of the workgroup's rows
+    const int step = kWhole ? p.row_waves * kWave : kLanes, first = threadIdx.x - mine * step;
     const int64_t rows = rows_of(p.num_rows, p.num_valid_rows);
     int turn = 0;
     for (int64_t base = (int64_t)blockIdx.x * p.group_rows; base < rows; base += (int64_t)gridDim.x * p.group_rows) {
@@ -121,8 +134,8 @@ __global__ void __launch_bounds__(kNormMaxWaves * kWave) norm_kernel(NormParams 
 #pragma unroll
             for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(a[i], a[i], sum);
         }
-        sum = wave_sum(sum);
-        if (p.row_waves > 1) {
+        sum = lanes_sum<kLanes>(sum);
+        if (kWhole && p.row_waves > 1) {
             // (Two rows of parts in turn: a wavefront may be a row ahead.)
             if ((threadIdx.x & (kWave - 1)) == 0) part[turn][wave] = sum;
             __syncthreads();
@@ -170,14 +183,15 @@ struct NormBackwardParams {
 // on, and the weight stays in registers: a load of it between the two would be
 // waited for behind the next row's. From four vectors on a row is loaded again
 // for the second look, there is no room for it beside the weight's sums.
-template <int V, bool kStream, bool kWeight>
+template <int V, bool kStream, bool kWeight, int kLanes>
 __global__ void __launch_bounds__(kNormMaxWaves * kWave) norm_backward_kernel(NormBackwardParams p) {
+    constexpr bool kWhole = kLanes == kWave;
     constexpr bool kAhead = V == 1, kKeep = V <= 2;
     __shared__ float2 part[2][kNormMaxWaves];
     extern __shared__ float4 sums[];  // with kWeight, and rows beside each other: one row
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int mine = wave / p.row_waves;
-    const int first = threadIdx.x - mine * p.row_waves * kWave, step = p.row_waves * kWave;
+    const int mine = kWhole ? wave / p.row_waves : threadIdx.x / kLanes;
+    const int step = kWhole ? p.row_waves * kWave : kLanes, first = threadIdx.x - mine * step;
     const int64_t rows = rows_of(p.num_rows, p.num_valid_rows);
     const int64_t stride = (int64_t)gridDim.x * p.group_rows;
     float dw[kWeight ? V : 1][8] = {};
@@ -227,9 +241,9 @@ __global__ void __launch_bounds__(kNormMaxWaves * kWave) norm_backward_kernel(No
                 along = __builtin_fmaf(w[i], d[i] * a[i], along);
             }
         }
-        square = wave_sum(square);
-        along = wave_sum(along);
-        if (p.row_waves > 1) {
+        square = lanes_sum<kLanes>(square);
+        along = lanes_sum<kLanes>(along);
+        if (kWhole && p.row_waves > 1) {
             if ((threadIdx.x & (kWave - 1)) == 0) part[turn][wave] = float2{square, along};
             __syncthreads();
             square = along = 0.f;
@@ -263,11 +277,16 @@ __global__ void __launch_bounds__(kNormMaxWaves * kWave) norm_backward_kernel(No
         }
     }
     if constexpr (kWeight) {
-        // The workgroup's rows of sums, one after the other.
+        // The workgroup's rows of sums, one after the other, a wavefront's together.
         float4* const to = reinterpret_cast<float4*>(p.grad_weight) + (int64_t)blockIdx.x * p.vecs * 2;
-        for (int n = 0; n < p.group_rows; ++n) {
-            if (n == mine) {
-                const bool last = n == p.group_rows - 1;
+#pragma unroll
+        for (int d = kLanes; d < kWave; d *= 2)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dw[0][i] += __shfl_xor(dw[0][i], d);
+        const int all = p.group_rows / (kWave / kLanes), at = kWhole ? mine : wave;
+        for (int n = 0; n < all; ++n) {
+            if (n == at && (kWhole || (threadIdx.x & (kWave - 1)) < kLanes)) {
+                const bool last = n == all - 1;
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     const int vec = first + v * step;
@@ -283,7 +302,7 @@ __global__ void __launch_bounds__(kNormMaxWaves * kWave) norm_backward_kernel(No
                     }
                 }
             }
-            if (p.group_rows > 1) __syncthreads();
+            if (all > 1) __syncthreads();
         }
     }
 }
@@ -327,9 +346,25 @@ __global__ void __launch_bounds__(kSumThreads) norm_sum_kernel(const float4* par
 // at a time, workgroups.
 struct NormShape {
     int v, row_waves, group_rows, groups;
+    int lanes = kWave;  // of a wavefront for a row: 32 or 16 where narrow rows share one
+    int threads() const { return group_rows * row_waves * lanes; }
 };
 
 int waves_for(int vecs, int v) { return (vecs + v * kWave - 1) / (v * kWave); }
+
+// Lanes of a row: half or a quarter of a wavefront for narrow rows, from `few`
+// rows for each row of a wavefront on. us, with the residual to bf16 and fp8 rows
+// / the gradient, and with a wavefront a row (fewer rows: no difference):
+//
+//   16384 x  64     4.7 /  8.3 ( 7.5 / 10.9)   60000 x  64   8.9 / 11.8 (21.8 / 22.7)
+//   16384 x 128     5.6 /  9.5 ( 8.5 / 11.3)   60000 x 128  12.8 / 15.4 (22.4 / 23.2)
+//   16384 x 176     6.9 / 10.7 ( 8.7 / 11.7)   60000 x 176  19.7 / 19.1 (28.1 / 24.4)
+//   16384 x 256     8.0 / 11.8 ( 9.7 / 12.1)   60000 x 256  25.2 / 25.7 (31.1 / 28.0)
+int lanes_for(int64_t rows, int vecs, int64_t few) {
+    int lanes = kWave;
+    while (lanes > 16 && vecs <= lanes / 2 && rows >= few * (2 * kWave / lanes)) lanes /= 2;
+    return lanes;
+}
 
 // One vector a lane for few rows, which are bound by latency; two from two
 // rows per CU on, wide ones from one (4096 x 7168 channels 46.2 us, 49.1 with one
@@ -342,6 +377,8 @@ NormShape norm_shape(int64_t rows, int vecs) {
     while (waves_for(vecs, s.v) > kNormMaxWaves) s.v *= 2;
     s.row_waves = waves_for(vecs, s.v);
     s.group_rows = s.row_waves >= 4 ? 1 : 4 / s.row_waves;
+    s.lanes = lanes_for(rows, vecs, kFewNarrow);
+    s.group_rows *= kWave / s.lanes;
     const int64_t groups = (rows + s.group_rows - 1) / s.group_rows;
     s.groups = (int)(groups < kMaxNormGroups ? groups : kMaxNormGroups);
     return s;
@@ -376,21 +413,25 @@ NormShape norm_backward_shape(int64_t rows, int vecs) {
     }
     // (Five wavefronts: three rows would wait for each other.)
     s.group_rows = s.row_waves > 5 ? room : s.row_waves == 5 ? 1 : (room + 1) / 2;
+    s.lanes = lanes_for(rows, vecs, 2 * kCus * s.group_rows);  // (so that there is work for as many workgroups)
+    s.group_rows *= kWave / s.lanes;
     const int64_t groups = (rows + s.group_rows - 1) / s.group_rows;
     const int most = kCus * (s.row_waves == 5 ? room : s.row_waves > 2 ? 1 : 2);
     s.groups = (int)(groups < most ? groups : most);
     return s;
 }
 
-template <int V>
+template <int V, int kLanes = kWave>
 const void* norm_kernel_of(bool past) {
-    return past ? (const void*)&norm_kernel<V, true> : (const void*)&norm_kernel<V, false>;
+    return past ? (const void*)&norm_kernel<V, true, kLanes> : (const void*)&norm_kernel<V, false, kLanes>;
 }
-template <int V>
+template <int V, int kLanes = kWave>
 const void* norm_backward_of(bool past, bool weight) {
     if (weight)
-        return past ? (const void*)&norm_backward_kernel<V, true, true> : (const void*)&norm_backward_kernel<V, false, true>;
-    return past ? (const void*)&norm_backward_kernel<V, true, false> : (const void*)&norm_backward_kernel<V, false, false>;
+        return past ? (const void*)&norm_backward_kernel<V, true, true, kLanes>
+                    : (const void*)&norm_backward_kernel<V, false, true, kLanes>;
+    return past ? (const void*)&norm_backward_kernel<V, true, false, kLanes>
+                : (const void*)&norm_backward_kernel<V, false, false, kLanes>;
 }
 
 #define DISPATCH_NORM_BY_V(V_, F) ((V_) == 1 ? F(1) : (V_) == 2 ? F(2) : (V_) == 4 ? F(4) : F(8))
@@ -422,10 +463,12 @@ hipError_t launch_rms_norm(const dispatch_rms_norm_problem_t& prob, const void* 
     const int64_t channel_bytes = 2 + (residual ? 4 : 0) + (y ? 2 : 0) + (q ? 1 : 0);
     const bool past = prob.num_rows * prob.width * channel_bytes > kPastBytes;
 #define DISPATCH_F(V) norm_kernel_of<V>(past)
-    const void* kernel = DISPATCH_NORM_BY_V(s.v, DISPATCH_F);
+    const void* kernel = s.lanes == 16   ? norm_kernel_of<1, 16>(past)
+                         : s.lanes == 32 ? norm_kernel_of<1, 32>(past)
+                                         : DISPATCH_NORM_BY_V(s.v, DISPATCH_F);
 #undef DISPATCH_F
     void* args[] = {&p};
-    return hipLaunchKernel(kernel, dim3(s.groups), dim3(s.row_waves * s.group_rows * kWave), args, 0, stream);
+    return hipLaunchKernel(kernel, dim3(s.groups), dim3(s.threads()), args, 0, stream);
 }
 
 size_t rms_norm_workspace_bytes(const dispatch_rms_norm_problem_t& prob) {
@@ -455,13 +498,16 @@ hipError_t launch_rms_norm_backward(const dispatch_rms_norm_problem_t& prob, con
     int rows = s.groups;
     p.grad_weight = rows == 1 ? grad_weight : static_cast<float*>(workspace);
     const bool past = prob.num_rows * prob.width * (grad_h ? 8 : 6) > kPastBytes;
-#define DISPATCH_F(V) norm_backward_of<V>(past, grad_weight != nullptr)
-    const void* kernel = DISPATCH_NORM_BY_V(s.v, DISPATCH_F);
+#define DISPATCH_F(V) norm_backward_of<V>(past, weighs)
+    const bool weighs = grad_weight != nullptr;
+    const void* kernel = s.lanes == 16   ? norm_backward_of<1, 16>(past, weighs)
+                         : s.lanes == 32 ? norm_backward_of<1, 32>(past, weighs)
+                                         : DISPATCH_NORM_BY_V(s.v, DISPATCH_F);
 #undef DISPATCH_F
     void* args[] = {&p};
     const size_t shared = s.group_rows > 1 && grad_weight != nullptr ? prob.width * sizeof(float) : 0;
     const hipError_t err =
-        hipLaunchKernel(kernel, dim3(s.groups), dim3(s.row_waves * s.group_rows * kWave), args, shared, stream);
+        hipLaunchKernel(kernel, dim3(s.groups), dim3(s.threads()), args, shared, stream);
     if (err != hipSuccess || grad_weight == nullptr || rows == 1) return err;
     const float* partial = p.grad_weight;
     int quads = (int)(prob.width / 4);

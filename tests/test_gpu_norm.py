@@ -72,7 +72,8 @@ def test_widths(rows, width):
 
 
 @pytest.mark.parametrize("rows,width", [(0, 128), (333, 4096), (511, 272), (512, 272), (513, 1024), (1030, 144), (4097, 16),
-                                        (700, 7168), (512, 16400)])
+                                        (700, 7168), (512, 16400), (2048, 256), (4097, 128), (5003, 176), (4099, 112),
+                                        (2047, 144)])
 @pytest.mark.parametrize("outs", ["both", "bf16", "fp8"])
 def test_rows(rows, width, outs):
     _check(_bf16((rows, width), rows), _weight(width, torch.bfloat16), _bf16((rows, width), 3, 4.0), outs)
@@ -181,7 +182,8 @@ def test_gradient_widths(rows, width):
 
 
 @pytest.mark.parametrize("rows,width", [(333, 4096), (511, 272), (512, 272), (513, 1024), (1030, 144), (4097, 16), (700, 7168),
-                                        (520, 16400), (2100, 128), (1100, 512)])
+                                        (520, 16400), (2100, 128), (1100, 512), (8192, 256), (8191, 176), (8213, 208),
+                                        (16385, 128), (16384, 16), (20001, 80), (30001, 240)])
 def test_gradient_rows(rows, width):
     _check_backward(_bf16((rows, width), 1, 3.0), _weight(width, torch.bfloat16), _bf16((rows, width), 2),
                     _bf16((rows, width), 3))
@@ -280,7 +282,8 @@ def test_more_rows_than_the_grid_holds(rows, width):
     assert torch.all(dx.view(-1, 100, width) == dx[:100])
 
 
-@pytest.mark.parametrize("rows,width,valid", [(600, 16400, 300), (700, 7168, 511), (3000, 528, 1), (2000, 40000, 1999)])
+@pytest.mark.parametrize("rows,width,valid", [(600, 16400, 300), (700, 7168, 511), (3000, 528, 1), (2000, 40000, 1999),
+                                              (9000, 176, 8201), (20000, 112, 5), (16384, 128, 16381), (8192, 256, 0)])
 def test_valid_rows_of_large_batches(rows, width, valid):
     x, w = _bf16((rows, width), 1).to(DEV), _weight(width, torch.float32).to(DEV)
     n = torch.tensor([valid], dtype=torch.int32, device=DEV)
