@@ -542,6 +542,9 @@ int dispatch_rms_norm_workspace_size(const dispatch_rms_norm_problem_t* problem,
  * u = h * r and g = grad_y * weight,
  *   grad_x = r * (g - u * mean over the row of g * u) + grad_h,
  *   grad_weight = sum over the rows of grad_y * u.
+ * All in fp32, the sums of h^2 and of g * h too: a row whose h^2 pass its range
+ * has r = 0, so that grad_x is grad_h and grad_weight gets nothing of it (NaN in
+ * the channels alone whose h or grad_y is not finite).
  * grad_x, device bf16 [R, W], is the gradient of h, and so of x and of the
  * residual; grad_h: device bf16 [R, W], what comes to h from elsewhere (along
  * the residual), or NULL; grad_x may be grad_y or grad_h. h is the forward

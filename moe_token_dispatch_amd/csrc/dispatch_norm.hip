@@ -254,9 +254,10 @@ __global__ void __launch_bounds__(kNormMaxWaves * kWave) norm_backward_kernel(No
             }
             turn ^= 1;
         }
-        // grad_x = (r w) grad_y - u (r mean(g u)) + grad_h.
+        // grad_x = (r w) grad_y - u (r mean(g u)) + grad_h. (Where r is 0 so is u,
+        // and the sum of g h may be infinite or have no value.)
         const float r = inverse_root(square * p.per_width + p.eps);
-        const float back = along * p.per_width * r * r;
+        const float back = r == 0.f ? 0.f : along * p.per_width * r * r;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int vec = first + v * step;

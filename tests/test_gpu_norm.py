@@ -375,3 +375,38 @@ def test_binding_refuses_wrong_tensors():
         M.dispatch_rms_norm_backward(x, w, x, 1e-6, y, grad_weight=torch.empty(256, device=DEV))
     with pytest.raises(ValueError, match="grad_x"):
         M.dispatch_rms_norm_backward(x, w, x, 1e-6, y[:3])
+
+
+@pytest.mark.parametrize("rows,width", [(6, 256), (6, 2064), (6, 16400), (16800, 128), (8400, 256), (1200, 4096)])
+@pytest.mark.parametrize("same", [True, False])
+def test_gradient_at_the_ends_of_the_range(rows, width, same):
+    """A row whose squares pass fp32's range has r = 0: what comes along the residual goes on as it is, whether
+    the sum of grad_y w h is infinite too (same signs) or has no value (either sign)."""
+    top = torch.finfo(torch.bfloat16).max
+    h = torch.zeros((6, width), dtype=torch.bfloat16)
+    h[1] = 2.0 ** -120
+    h[2, 5] = 2.0 ** 60
+    h[3] = 2.0 ** 48
+    h[4], h[5] = top, -1.0
+    h = h.repeat(rows // 6, 1)
+    past = torch.arange(rows) % 6 == 4
+    dy = torch.ones((rows, width), dtype=torch.bfloat16) if same else _bf16((rows, width), 2)
+    dh, w = _bf16((rows, width), 3), torch.ones(width)
+    for add in (None, dh):
+        dx, dw = _backward(h, w, dy, add)
+        dx, dw = dx.cpu(), dw.cpu().double()
+        assert torch.all(dx[past] == (0.0 if add is None else dh[past]))
+        x, d = h[~past].double(), dy[~past].double()
+        want_x, want_w = R.rms_norm_gradient(h[~past], w, dy[~past], 1e-6, None if add is None else dh[~past])
+        r = (x.pow(2).mean(1, keepdim=True) + 1e-6).rsqrt()
+        # As in _check_backward.
+        size = (r * d).abs() + (r * x * r).abs() * (d * x * r).abs().mean(1, keepdim=True)
+        size = size + (0.0 if add is None else dh[~past].double().abs())
+        assert torch.all((dx[~past].double() - want_x).abs() <= BF16 * want_x.abs() + 2 * REL * size + 2.0 ** -134)
+        assert torch.all((dw - want_w).abs() <= (REL + h.shape[0] * ULP) * (d * x * r).abs().sum(0) + 2.0 ** -140)
+    # What is no number stays one.
+    h[3, 3], h[5, 7], dy[4, 9] = math.inf, math.nan, math.nan
+    dx, dw = _backward(h, w, dy, dh)
+    dx = dx.cpu()
+    assert math.isnan(float(dx[3, 3])) and torch.all(torch.isnan(dx[5])) and math.isnan(float(dx[4, 9]))
+    assert all(math.isnan(float(dw[i])) for i in (3, 7, 9))
