@@ -410,3 +410,41 @@ def test_gradient_at_the_ends_of_the_range(rows, width, same):
     dx = dx.cpu()
     assert math.isnan(float(dx[3, 3])) and torch.all(torch.isnan(dx[5])) and math.isnan(float(dx[4, 9]))
     assert all(math.isnan(float(dw[i])) for i in (3, 7, 9))
+
+
+def _weight_gradient(h, dy, eps=1e-6):
+    """(the weight's gradient in float64, the sums of its terms' magnitudes) of device rows."""
+    x, d = h.double(), dy.double()
+    terms = d * x * (x.pow(2).mean(1, keepdim=True) + eps).rsqrt()
+    return terms.sum(0), terms.abs().sum(0)
+
+
+# Up to 8 rows a lane, 2 joins of a wavefront's rows, 16 wavefronts or rows of a workgroup, then the rows of
+# sums: up to 6 for each of 128 groups of threads, 3 joins and 16 wavefronts: 51 additions in a row.
+CHAIN = 51 * ULP
+
+
+# 16, 32 and 64 lanes a row and several wavefronts, for each a shape whose last row is alone in its round of the grid.
+@pytest.mark.parametrize("rows,width,valid", [(16385, 128, None), (16384, 16, None), (20001, 80, None), (8193, 240, None),
+                                              (30001, 240, None), (4097, 512, None), (8213, 208, None), (3073, 1040, None),
+                                              (1025, 4096, None), (769, 2064, None), (513, 7168, None), (257, 16400, None),
+                                              (9000, 176, 8201), (16384, 128, 16381), (600, 4096, 513)])
+def test_gradient_of_the_weight_has_every_row(rows, width, valid):
+    h, dy = (_bf16((rows, width), seed).to(DEV) for seed in (1, 2))
+    w, last = _weight(width, torch.bfloat16), (valid or rows) - 1
+    n = None if valid is None else torch.tensor([valid], dtype=torch.int32)
+    _, dw = _backward(h, w, dy, valid=n)
+    want, size = _weight_gradient(h[:last + 1], dy[:last + 1])
+    bound = (REL + CHAIN) * size
+    assert torch.all((dw.double() - want).abs() <= bound)
+    # The bound sees any one row that is left out.
+    for row in (0, last // 2, last):
+        less = want - _weight_gradient(h[row:row + 1], dy[row:row + 1])[0]
+        assert torch.any((less - want).abs() > 4 * bound)
+    # And of nothing but that row.
+    for row in (0, last // 2, last):
+        one = torch.zeros_like(dy)
+        one[row] = dy[row]
+        _, dw = _backward(h, w, one, valid=n)
+        want_one, size_one = _weight_gradient(h[row:row + 1], dy[row:row + 1])
+        assert torch.all((dw.double() - want_one).abs() <= REL * size_one)
