@@ -309,3 +309,11 @@ def test_binding_refuses_wrong_tensors():
             M.dispatch_gate_grouped(p, groups, z, out, ws)
     with pytest.raises(M.DispatchError):
         M.dispatch_gate_grouped(p, good, z, out, ws[:256])
+
+
+# Four tokens per wavefront with two groups a lane, and entries past the eighth in live rows of every scoring.
+@pytest.mark.parametrize("t,e,groups,taken,topk", [(8193, 40, 20, 7, 2), (8200, 60, 20, 5, 12), (8195, 32, 32, 9, 6),
+                                                   (8200, 128, 8, 3, 12)])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid", "pairs"])
+def test_many_groups_and_entries_of_few_experts(t, e, groups, taken, topk, scoring):
+    test_shapes(t, e, groups, taken, topk, scoring)
