@@ -448,3 +448,9 @@ def test_gradient_of_the_weight_has_every_row(rows, width, valid):
         _, dw = _backward(h, w, one, valid=n)
         want_one, size_one = _weight_gradient(h[row:row + 1], dy[row:row + 1])
         assert torch.all((dw.double() - want_one).abs() <= REL * size_one)
+
+
+# 16 and 32 lanes a row, and a wavefront a row: 1050000, 1050000 and 1075000 workgroups' rows for a grid of 2^20.
+@pytest.mark.parametrize("rows,width", [(16800000, 16), (8400000, 144), (4300000, 272)])
+def test_more_narrow_rows_than_the_grid_holds(rows, width):
+    test_more_rows_than_the_grid_holds(rows, width)
