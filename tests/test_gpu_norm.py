@@ -454,3 +454,22 @@ def test_gradient_of_the_weight_has_every_row(rows, width, valid):
 @pytest.mark.parametrize("rows,width", [(16800000, 16), (8400000, 144), (4300000, 272)])
 def test_more_narrow_rows_than_the_grid_holds(rows, width):
     test_more_rows_than_the_grid_holds(rows, width)
+
+
+# Four vectors a lane and eight, which the gradient loads again for its second look.
+@pytest.mark.parametrize("rows,width", [(3, 16400), (520, 16400), (3, 40000), (300, 40000)])
+def test_wide_rows_in_place(rows, width):
+    a, b, c = (_bf16((rows, width), seed).to(DEV) for seed in (1, 2, 3))
+    w = _weight(width, torch.float32).to(DEV)
+    want_h, want_y, _, _ = _forward(a, w, residual=b, outs="bf16")
+    want_x, want_w = _backward(a, w, b, c)
+    for target in (0, 1):
+        x, res, y = a.clone(), b.clone(), torch.empty_like(a)
+        h = (x, res)[target]
+        M.dispatch_rms_norm(x, w, 1e-6, residual=res, h=h, y=y)
+        assert torch.equal(h, want_h) and torch.equal(y, want_y)
+        dy, dh, dw = b.clone(), c.clone(), torch.empty(width, device=DEV)
+        dx = (dy, dh)[target]
+        M.dispatch_rms_norm_backward(a, w, dy, 1e-6, dx, grad_h=dh, grad_weight=dw,
+                                     workspace=M.alloc_rms_norm_workspace(rows, width, DEV))
+        assert torch.equal(dx, want_x) and torch.equal(dw, want_w)
