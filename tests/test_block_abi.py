@@ -182,3 +182,35 @@ def test_binding_refuses_host_tensors():
     p = M.make_gate_problem(4, 32, 2, M.GATE_SIGMOID, torch.float32)
     with pytest.raises(ValueError, match="logits must be a device tensor"):
         M.dispatch_gate_grouped(p, M.make_gate_groups(4, 2), torch.zeros((4, 32)), M.alloc_gate(p, "cpu"))
+
+
+@pytest.mark.parametrize("gpus,current,of,expected", [(1, 0, 0, 0), (2, 0, 0, 0), (2, 0, 1, 1), (8, 5, 2, 2)])
+def test_a_prepared_call_runs_on_its_tensors_device(monkeypatch, gpus, current, of, expected):
+    """With several GPUs the tensors' device is the current one during the call, and the caller's again after it."""
+    now, calls, codes = [current], [], [M.OK, M.ERR_HIP]
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, now[0] = now[0], self.index
+
+        def __exit__(self, *_):
+            now[0] = self.before
+
+    class Library:
+        @staticmethod
+        def dispatch_something(*args):
+            calls.append((args, now[0]))
+            return codes[len(calls) - 1]
+
+    monkeypatch.setattr(M._binding, "load_library", Library)
+    monkeypatch.setattr(torch.cuda, "device_count", lambda: gpus)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: now[0])
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    call = M._binding._Prepared("dispatch_something", (1, 2), torch.device("cuda", of), None)
+    call()
+    with pytest.raises(M.DispatchError, match="dispatch_something"):
+        call()
+    assert calls == [((1, 2), expected)] * 2 and now == [current]
