@@ -200,6 +200,8 @@ def test_a_prepared_call_runs_on_its_tensors_device(monkeypatch, gpus, current, 
             now[0] = self.before
 
     class Library:
+        dispatch_strerror = M.load_library().dispatch_strerror
+
         @staticmethod
         def dispatch_something(*args):
             calls.append((args, now[0]))
