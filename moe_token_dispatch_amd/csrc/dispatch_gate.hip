@@ -839,14 +839,14 @@ __device__ __forceinline__ uint32_t open_row_groups(const uint32_t (&key)[V], fl
         }
     }
     __builtin_amdgcn_wave_barrier();
-    if (side <= 1) join_rotated<1>(top);
+    // (There are two groups at least: Gp is 2 or more.)
     if (side <= 2) join_rotated<2>(top);
     if (side <= 4) join_rotated<4>(top);
     if (side <= 8) join_rotated<8>(top);
     const uint32_t mark = top.mark(p.group_pairs);
     int place = 0;
     // (Past Gp - 1 rotations the same groups come again.)
-    if (side > 1) count_before<1>(mark, group, place);
+    count_before<1>(mark, group, place);
     if (side > 2) count_from<2>(std::make_integer_sequence<int, 2>(), mark, group, place);
     if (side > 4) count_from<4>(std::make_integer_sequence<int, 4>(), mark, group, place);
     if (side > 8) count_from<8>(std::make_integer_sequence<int, 8>(), mark, group, place);
