@@ -360,9 +360,10 @@ int dispatch_combine(const dispatch_combine_problem_t* problem, const int32_t* e
  * [expert_rows, H], grad_sf: device fp32 [expert_rows, ceil(H / 128)]; H a
  * multiple of 16), the rows that the experts' product takes; rows that no entry
  * has (pads) are not written, and slots are a layout's: no two entries have the
- * same one (its row would be either's). Outputs that are NULL are left out, but one is
- * needed, and either grad_y or grad_q may be given. y (as in dispatch_combine)
- * is needed with grad_weights only. Row pointers are 16-byte aligned. */
+ * same one (its row would be either's). Outputs that are NULL are left out, but
+ * one is needed (unless expert_rows is 0), and either grad_y or grad_q may be
+ * given. y (as in dispatch_combine) is needed with grad_weights only. Row
+ * pointers are 16-byte aligned. */
 int dispatch_combine_backward(const dispatch_combine_problem_t* problem, const int32_t* expert_slot,
                               const float* topk_weights, const void* y, const void* grad_out, float* grad_weights,
                               void* grad_y, void* grad_q, float* grad_sf, hipStream_t stream);

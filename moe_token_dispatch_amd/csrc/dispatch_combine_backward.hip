@@ -172,7 +172,7 @@ hipError_t launch_combine_backward(const dispatch_combine_problem_t& prob, const
                                    const float* topk_weights, const void* y, const void* grad_out,
                                    float* grad_weights, void* grad_y, void* grad_q, float* grad_sf,
                                    hipStream_t stream) {
-    if (prob.num_tokens == 0) return hipSuccess;
+    if (prob.num_tokens == 0 || (!grad_weights && !grad_y && !grad_q)) return hipSuccess;
     CombineBackwardParams p{};
     p.expert_slot = expert_slot;
     p.topk_weights = topk_weights;

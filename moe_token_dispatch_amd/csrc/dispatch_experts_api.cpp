@@ -276,7 +276,8 @@ int dispatch_combine_backward(const dispatch_combine_problem_t* problem, const i
     if (grad_y && (grad_q || grad_sf)) return DISPATCH_ERR_ARG;
     if (p.hidden % 8 != 0 || (grad_q && p.hidden % 16 != 0)) return DISPATCH_ERR_ALIGN;
     if (p.num_tokens > 0) {
-        if (!expert_slot || !topk_weights || !grad_out || (!grad_weights && !grad_y && !grad_q)) return DISPATCH_ERR_NULL;
+        if (!expert_slot || !topk_weights || !grad_out) return DISPATCH_ERR_NULL;
+        if (p.expert_rows > 0 && !grad_weights && !grad_y && !grad_q) return DISPATCH_ERR_NULL;
         if (grad_weights && p.expert_rows > 0 && !y) return DISPATCH_ERR_NULL;
         if ((grad_q == nullptr) != (grad_sf == nullptr)) return DISPATCH_ERR_NULL;
     }

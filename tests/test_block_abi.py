@@ -171,6 +171,15 @@ def test_combine_gradient_arguments():
     assert _combine(tokens=0, slot=None, w=None, y=None, d=None, dw=None, dy=None) == M.OK
 
 
+def test_combine_gradient_without_expert_rows():
+    """Buffers of no rows may be NULL, as an empty tensor's pointer is; the weights' gradient is asked for otherwise."""
+    assert _combine(rows=0, y=None, dw=None, dy=None) == M.OK
+    for name in ("slot", "w", "d"):
+        assert _combine(rows=0, y=None, dw=None, dy=None, **{name: None}) == M.ERR_NULL, name
+    assert _combine(rows=0, y=None, dw=None, dy=None, dsf=4096) == M.ERR_NULL
+    assert _combine(rows=1, y=None, dw=None, dy=None) == M.ERR_NULL
+
+
 def test_binding_refuses_host_tensors():
     x, w = torch.zeros((4, 32), dtype=torch.bfloat16), torch.ones(32)
     with pytest.raises(ValueError, match="x must be a device tensor"):

@@ -285,3 +285,15 @@ def test_binding_refuses_wrong_tensors():
     for kw in (dict(grad_y=dy, grad_q=q, grad_sf=sf), dict(grad_q=q), dict()):
         with pytest.raises(M.DispatchError):
             M.dispatch_combine_backward(slot, w, y, d, **kw)
+
+
+@pytest.mark.parametrize("form", ["bf16", "fp8", "none"])
+@pytest.mark.parametrize("want_weights", [True, False])
+def test_no_expert_rows(form, want_weights):
+    """A buffer of no rows: every slot is outside it, the weights' gradient is 0."""
+    if form == "none" and not want_weights:
+        return
+    slot, w, y, d = _inputs(5, 3, 272, 19, 23)
+    dw, dy, dq, dsf = _run(slot, w, y[:0], d, form, want_weights)
+    assert dw is None or torch.all(dw == 0)
+    assert all(x is None or x.numel() == 0 for x in (dy, dq, dsf))
