@@ -114,7 +114,9 @@ __global__ void __launch_bounds__(kMaxWaves * kWave) combine_backward_kernel(Com
                     if (kTo == RowsTo::kBf16) {
                         if (live) store_vec<true>(p.grad_y + at, narrow_bf16(x));
                     } else {
-                        // (By their bits, so that NaN stays.)
+                        // (By their bits, so that NaN stays. An infinite weight's
+                        // scale is infinite also beside zeros, whose products are
+                        // NaN; the bytes are NaN with either.)
                         const uint32_t m = __float_as_uint(weight[b] * top) & 0x7fffffffu;
                         const uint32_t low = __float_as_uint(kAmaxFloor);
                         scale8<true>(x, __uint_as_float(m > low ? m : low), live, live && vec % 16 == 0,

@@ -13,8 +13,8 @@
 // mean of h^2 is added again beside that of g h.
 //
 // HBM bounds both: 4096 x 7168 with the residual to bf16 and fp8 rows 46.2 us
-// for 265 MB (5.7 TB/s), the gradient 45.6 us for 235 MB (5.2 TB/s, the weight's
-// sums 4 of them). One row takes 4.2 us, which is the launch.
+// for 265 MB (5.7 TB/s), the gradient 45.6 us for 235 MB (5.2 TB/s), with the
+// weight's 45 to 48.6 by the buffers. One row takes 4.2 us, which is the launch.
 #include "dispatch_common.hpp"
 #include "dispatch_experts.hpp"
 #include "dispatch_math.hpp"
